@@ -8,6 +8,7 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from ctypes import POINTER, Structure, c_char_p, c_float, c_int, c_int32, c_int64, c_size_t, c_uint16, c_void_p
 
@@ -48,6 +49,14 @@ class fg_kv_cache(Structure):
                 ("group", c_int32)]
 
 
+class fg_paged_kv(Structure):
+    _fields_ = [("k_codes", c_void_p), ("k_mins", c_void_p), ("k_scales", c_void_p),
+                ("v_codes", c_void_p), ("v_mins", c_void_p), ("v_scales", c_void_p),
+                ("weights", c_void_p), ("tokens", c_void_p), ("page_table", c_void_p),
+                ("num_pages", c_int32), ("page_size", c_int32), ("num_seqs", c_int32), ("max_pages", c_int32),
+                ("num_heads", c_int32), ("head_dim", c_int32), ("group", c_int32)]
+
+
 class fg_layer_config(Structure):
     _fields_ = [("hidden", c_int32), ("num_heads", c_int32), ("head_dim", c_int32), ("ffn", c_int32),
                 ("ln_eps", c_float), ("group", c_int32), ("act_bits", c_int32)]
@@ -82,6 +91,14 @@ _decl("fg_kv_cache_bytes", c_int, c_int, c_int, c_int, c_int, c_int, POINTER(c_s
 _decl("fg_kv_append", c_int, POINTER(fg_kv_cache), P, P, c_int64, c_int, c_int, P, P)
 _decl("fg_attention_decode", c_int, POINTER(fg_kv_cache), P, c_int64, P, c_int64, c_int, c_int, P, P)
 _decl("fg_attention_decode_append", c_int, POINTER(fg_kv_cache), P, c_int64, P, P, c_int64, P, c_int64, c_int, P, P)
+_decl("fg_paged_kv_bytes", c_int, c_int, c_int, c_int, c_int, c_int, POINTER(c_size_t), POINTER(c_size_t),
+      POINTER(c_size_t))
+_decl("fg_paged_kv_append", c_int, POINTER(fg_paged_kv), P, P, c_int64, c_int, c_int, P, P, P, P)
+_decl("fg_paged_attention_workspace_bytes", c_size_t, POINTER(fg_paged_kv), c_int, c_int, c_int, c_int, c_int)
+_decl("fg_paged_attention", c_int, POINTER(fg_paged_kv), P, c_int64, c_int, P, c_int64, c_int, c_int, P, P, c_int,
+      c_int, P, c_size_t, P)
+_decl("fg_paged_kv_evict_workspace_bytes", c_size_t, POINTER(fg_paged_kv), c_int, c_int)
+_decl("fg_paged_kv_evict", c_int, POINTER(fg_paged_kv), P, P, c_int, c_int, c_int, P, P, P, P, c_size_t, P)
 _decl("fg_linear_workspace_bytes", c_size_t, c_int, c_int, c_int)
 _decl("fg_linear_plan", c_int, c_int, c_int, c_int, POINTER(c_int), POINTER(c_int), POINTER(c_int))
 _decl("fg_linear_w4a16", c_int, P, c_int, c_int, POINTER(fg_qtensor), P, P, c_int, c_int, c_float, P, P, c_size_t, P)
@@ -286,6 +303,204 @@ def fg_attention_decode_append(cache: KVCache, q: torch.Tensor, k: torch.Tensor,
                                            _ptr(out), out.stride(0), rows, _ptr(positions), _stream(stream)),
            "fg_attention_decode_append")
     return out
+
+
+# ---------------------------------------------------------------------------------------
+# paged KV cache
+# ---------------------------------------------------------------------------------------
+
+class PagedKVCache:
+    """Paged 4-bit KV cache of one layer (fg_paged_kv): pools of ``num_pages`` pages of ``page_size``
+    slots for ``num_heads`` key-value heads, and ``page_table``, int32 [num_seqs, max_pages] on the
+    device.  ``track=True`` adds the pools that fg_paged_kv_evict ranks the slots by: ``weights``
+    (fp32) and ``tokens`` (int32).  The table's values may change between calls; the arrays
+    themselves are the cache's for its life."""
+
+    def __init__(self, num_pages, num_heads, head_dim, page_size, page_table, group: int = 64, track: bool = False,
+                 arrays=None, weights=None, tokens=None):
+        cb, mb, tb = c_size_t(), c_size_t(), c_size_t()
+        _check(_lib.fg_paged_kv_bytes(num_pages, num_heads, head_dim, page_size, group, ctypes.byref(cb),
+                                      ctypes.byref(mb), ctypes.byref(tb)), "fg_paged_kv_bytes")
+        _need(page_table, torch.int32, "page_table")
+        if page_table.dim() != 2:
+            raise ValueError("page_table: expected [num_seqs, max_pages]")
+        dev = page_table.device
+        lead = (num_pages, num_heads, page_size)
+        shapes = [lead + (head_dim // 2,), lead + (head_dim // group,), lead + (head_dim // group,)] * 2
+        types = [torch.uint8, torch.float16, torch.float16] * 2
+        if arrays is None:
+            arrays = [torch.zeros(sh, dtype=t, device=dev) for sh, t in zip(shapes, types)]
+        if track:
+            weights = torch.zeros(lead, dtype=torch.float32, device=dev) if weights is None else weights
+            tokens = torch.zeros(lead, dtype=torch.int32, device=dev) if tokens is None else tokens
+        for a, sh, t in zip(list(arrays) + [weights, tokens], shapes + [lead] * 2, types + [torch.float32, torch.int32]):
+            if a is not None:
+                _need(a, t, "cache pool")
+                if a.numel() != math.prod(sh) or a.device != dev:
+                    raise ValueError(f"cache pool: expected {tuple(sh)} on {dev}, got {tuple(a.shape)} on {a.device}")
+        self.num_pages, self.num_heads, self.head_dim, self.page_size = num_pages, num_heads, head_dim, page_size
+        self.group, self.device = group, dev
+        self.num_seqs, self.max_pages = page_table.shape
+        self.k_codes, self.k_mins, self.k_scales, self.v_codes, self.v_mins, self.v_scales = arrays
+        self.weights, self.tokens, self.page_table = weights, tokens, page_table
+        ptrs = [0 if a is None else a.data_ptr() for a in list(arrays) + [weights, tokens, page_table]]
+        self._s = fg_paged_kv(*ptrs, num_pages, page_size, self.num_seqs, self.max_pages, num_heads, head_dim, group)
+        self._ref = ctypes.byref(self._s)
+
+    @staticmethod
+    def from_cache(cache: KVCache, weights=None, tokens=None, track: bool = False) -> "PagedKVCache":
+        """The contiguous cache as a paged one that shares its memory: one page of max_len slots per
+        sequence, so that a cache filled by fg_layer_prefill goes on in paged calls."""
+        table = torch.arange(cache.num_seqs, dtype=torch.int32, device=cache.k_codes.device).view(-1, 1)
+        return PagedKVCache(cache.num_seqs, cache.num_heads, cache.head_dim, cache.max_len, table, group=cache.group,
+                            arrays=cache.arrays(), weights=weights, tokens=tokens, track=track)
+
+    def arrays(self):
+        return [self.k_codes, self.k_mins, self.k_scales, self.v_codes, self.v_mins, self.v_scales]
+
+    def struct(self) -> fg_paged_kv:
+        return self._s
+
+    def nbytes(self) -> int:
+        return sum(a.numel() * a.element_size() for a in self.arrays() + [self.weights, self.tokens] if a is not None)
+
+
+class _On:
+    """The device of a paged cache and the stream of a call: the caller's, or that device's current
+    one.  Memory that a call allocates belongs to that stream."""
+
+    def __init__(self, cache: PagedKVCache, stream):
+        self.dev, self.other = cache.device, cache.device.index != torch.cuda.current_device()
+        self.stream = torch.cuda.current_stream(cache.device) if stream is None else stream
+        if self.stream.device != cache.device:
+            raise ValueError(f"stream on {self.stream.device}, cache on {cache.device}")
+        self.own = stream is None
+        self.ptr = c_void_p(self.stream.cuda_stream)
+
+    def empty(self, shape, dtype):
+        if self.own:
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.dev)
+
+    def call(self, fn, *args) -> None:
+        if self.other:
+            with torch.cuda.device(self.dev):
+                rc = fn(*args)
+                if rc != 0:
+                    raise FgError(rc, fn.__name__)
+            return
+        rc = fn(*args)
+        if rc != 0:
+            raise FgError(rc, fn.__name__)
+
+
+def _rows(t: torch.Tensor, cache: PagedKVCache, name: str, width: int | None = None) -> None:
+    if t.dtype != torch.float16 or t.dim() != 2 or t.device != cache.device or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected float16 rows of unit element stride on {cache.device}")
+    if width is not None and t.shape[1] != width:
+        raise ValueError(f"{name}: expected rows of {width} values, got {t.shape[1]}")
+
+
+def _ints(t, cache: PagedKVCache, name: str, n: int) -> None:
+    if t is not None and (t.dtype != torch.int32 or t.device != cache.device or not t.is_contiguous() or t.numel() < n):
+        raise ValueError(f"{name}: expected at least {n} contiguous int32 on {cache.device}")
+
+
+def _stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _ws(t, cache: PagedKVCache) -> None:
+    if t is not None and (t.device != cache.device or not t.is_contiguous()):
+        raise ValueError(f"workspace: expected a contiguous tensor on {cache.device}")
+
+
+def fg_paged_kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                       rows_per_seq: int = 1, row_counts: torch.Tensor | None = None,
+                       first_tokens: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise and append rows k, v [rows, num_heads * head_dim]; row i of sequence s goes to slot
+    ``positions[s] + i`` (see fg.h for row_counts, first_tokens and inactive sequences)."""
+    rows = k.shape[0]
+    width = cache.num_heads * cache.head_dim
+    _rows(k, cache, "k", width)
+    _rows(v, cache, "v", width)
+    if v.shape[0] != rows or (rows > 1 and k.stride(0) != v.stride(0)):
+        raise ValueError("k and v must share their shape and a row stride")
+    n = -(-rows // max(1, rows_per_seq))
+    _ints(positions, cache, "positions", n)
+    _ints(row_counts, cache, "row_counts", n)
+    _ints(first_tokens, cache, "first_tokens", n)
+    on = _On(cache, stream)
+    on.call(_lib.fg_paged_kv_append, cache._ref, _ptr(k), _ptr(v), _stride(k), rows, rows_per_seq, _ptr(positions),
+            _ptr(row_counts), _ptr(first_tokens), on.ptr)
+
+
+def fg_paged_attention_workspace_bytes(cache: PagedKVCache, num_q_heads: int, rows: int, rows_per_seq: int = 1,
+                                       max_len: int | None = None, accumulate: bool = False) -> int:
+    return int(_lib.fg_paged_attention_workspace_bytes(cache._ref, num_q_heads, rows, rows_per_seq, max_len or 0,
+                                                       int(accumulate)))
+
+
+def fg_paged_attention(cache: PagedKVCache, q: torch.Tensor, positions: torch.Tensor, rows_per_seq: int = 1,
+                       row_counts: torch.Tensor | None = None, max_len: int | None = None, accumulate: bool = False,
+                       out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """Attention of q [rows, num_q_heads * head_dim] over the cache; ``accumulate=True`` adds each
+    slot's probabilities to ``cache.weights``.  ``workspace``: None allocates it."""
+    rows = q.shape[0]
+    _rows(q, cache, "q")
+    hq = q.shape[1] // cache.head_dim
+    if hq * cache.head_dim != q.shape[1]:
+        raise ValueError(f"q: rows of {q.shape[1]} values are no whole heads of {cache.head_dim}")
+    n = -(-rows // max(1, rows_per_seq))
+    _ints(positions, cache, "positions", n)
+    _ints(row_counts, cache, "row_counts", n)
+    on = _On(cache, stream)
+    if out is None:
+        out = on.empty(q.shape, torch.float16)
+    _rows(out, cache, "out", q.shape[1])
+    if out.shape[0] != rows:
+        raise ValueError(f"out: expected {rows} rows")
+    if workspace is None:
+        need = fg_paged_attention_workspace_bytes(cache, hq, rows, rows_per_seq, max_len, accumulate)
+        workspace = on.empty(need, torch.uint8) if need else None
+    _ws(workspace, cache)
+    on.call(_lib.fg_paged_attention, cache._ref, _ptr(q), _stride(q), hq, _ptr(out), _stride(out), rows, rows_per_seq,
+            _ptr(positions), _ptr(row_counts), max_len or 0, int(accumulate), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), on.ptr)
+    return out
+
+
+def fg_paged_kv_evict_workspace_bytes(cache: PagedKVCache, budget: int, max_len: int | None = None) -> int:
+    return int(_lib.fg_paged_kv_evict_workspace_bytes(cache._ref, budget, max_len or 0))
+
+
+def fg_paged_kv_evict(cache: PagedKVCache, lengths: torch.Tensor, next_tokens: torch.Tensor, budget: int,
+                      recent: int, max_len: int | None = None, new_lengths: torch.Tensor | None = None,
+                      weights_out: torch.Tensor | None = None, tokens_out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Evict every sequence's heads down to ``budget`` slots: the last ``recent`` tokens, then the
+    largest weights.  Returns the new lengths."""
+    n = cache.num_seqs
+    _ints(lengths, cache, "lengths", n)
+    _ints(next_tokens, cache, "next_tokens", n)
+    on = _On(cache, stream)
+    if new_lengths is None:
+        new_lengths = on.empty(n, torch.int32)
+    _ints(new_lengths, cache, "new_lengths", n)
+    for t, like, name in ((weights_out, cache.weights, "weights_out"), (tokens_out, cache.tokens, "tokens_out")):
+        if t is not None and (like is None or t.dtype != like.dtype or t.device != like.device or
+                              t.numel() != like.numel() or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected a pool like the cache's own")
+    if workspace is None:
+        need = fg_paged_kv_evict_workspace_bytes(cache, budget, max_len)
+        workspace = on.empty(need, torch.uint8) if need else None
+    _ws(workspace, cache)
+    on.call(_lib.fg_paged_kv_evict, cache._ref, _ptr(lengths), _ptr(next_tokens), budget, recent, max_len or 0,
+            _ptr(new_lengths), _ptr(weights_out), _ptr(tokens_out), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), on.ptr)
+    return new_lengths
 
 
 # ---------------------------------------------------------------------------------------

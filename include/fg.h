@@ -186,6 +186,107 @@ FG_API fg_status fg_attention_decode_append(const fg_kv_cache *kv, const fg_half
                                      const int32_t *positions, void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* Paged 4-bit KV cache [G3]: append, attention, eviction                  */
+/* ---------------------------------------------------------------------- */
+/* The 4-bit cache of one layer in pages, so that a sequence holds memory for the tokens it has
+ * and not for max_len of them.  A page holds page_size slots of every head; sequence s's slot p
+ * lies in page page_table[s][p / page_size] at p % page_size, in the form of fg_kv_cache (codes,
+ * fp16 min and scale per group of G = 64 or 128 along head_dim):
+ *   k_codes, v_codes            uint8 [num_pages][num_heads][page_size][head_dim/2]
+ *   k_mins, k_scales, v_...     fp16  [num_pages][num_heads][page_size][head_dim/G]
+ * A cache that tracks its slots (for fg_paged_kv_evict) has two pools more, NULL otherwise:
+ *   weights                     fp32  [num_pages][num_heads][page_size], attention weight received
+ *   tokens                      int32 [num_pages][num_heads][page_size], number of the slot's token
+ * An fg_kv_cache is the case page_size = max_len, num_pages = num_seqs, page_table[s] = {s}.
+ * Device memory, caller-owned; the code, min and scale pools 16-byte aligned, the others 4-byte.
+ * Requirements: page_size a multiple of 16, head_dim in {64, 128, 256} and a multiple of G,
+ * max_pages * page_size <= INT32_MAX.  Table entries that no call below reaches may hold anything.
+ * Sequences may share pages that are only read; pages that a call appends to, accumulates weights
+ * in or evicts from belong to one sequence, once.
+ * An entry that is reached and lies outside [0, num_pages) flags FG_ERR_RANGE (fg_sync_status). */
+typedef struct {
+    uint8_t *k_codes;
+    fg_half *k_mins;
+    fg_half *k_scales;
+    uint8_t *v_codes;
+    fg_half *v_mins;
+    fg_half *v_scales;
+    float *weights;             /* or NULL */
+    int32_t *tokens;            /* or NULL */
+    const int32_t *page_table;  /* [num_seqs][max_pages] */
+    int32_t num_pages;
+    int32_t page_size;
+    int32_t num_seqs;
+    int32_t max_pages;
+    int32_t num_heads;          /* key-value heads */
+    int32_t head_dim;
+    int32_t group;              /* G: 64 or 128 (0 = 64) */
+} fg_paged_kv;
+
+/* Byte sizes of one codes pool, one mins/scales pool and one weights/tokens pool. */
+FG_API fg_status fg_paged_kv_bytes(int num_pages, int num_heads, int head_dim, int page_size, int group,
+                                   size_t *codes_bytes, size_t *meta_bytes, size_t *track_bytes);
+
+/* Quantise and append new k, v rows (fp16 device rows, row r at k + r*ld, num_heads*head_dim
+ * values, head-major; 16-byte aligned, ld % 8 == 0) exactly as fg_kv_append does: the same bits.
+ * Row r is row i = r % rows_per_seq of sequence s = r / rows_per_seq and goes to slot
+ * positions[s] + i.  row_counts (int32 device [num_seqs], or NULL: rows_per_seq each): only the
+ * rows i < row_counts[s] are appended, the padding behind them is not read.  positions[s] = -1:
+ * the sequence takes no part.  A tracked cache's slots get weight 0 and token number
+ * first_tokens[s] + i (int32 device [num_seqs]; NULL: the slot's own number, positions[s] + i).
+ * A slot outside the table's max_pages pages or in a bad page is skipped and flags FG_ERR_RANGE;
+ * so does a position below -1 or a count outside [0, rows_per_seq], whose sequence is left out. */
+FG_API fg_status fg_paged_kv_append(const fg_paged_kv *kv, const fg_half *k, const fg_half *v, int64_t ld, int rows,
+                                    int rows_per_seq, const int32_t *positions, const int32_t *row_counts,
+                                    const int32_t *first_tokens, void *stream);
+
+/* Softmax attention of query rows over the paged cache.  q: fp16 device rows (stride ldq) of
+ * num_q_heads * head_dim values, already scaled by head_dim^-1/2; out: fp16 device rows (stride
+ * ldo); both 16-byte aligned with strides that are multiples of 8.  num_q_heads is a multiple of
+ * num_heads, and the query heads j*R .. j*R + R-1 (R their ratio) read key-value head j.  Row i of
+ * sequence s (r = s * rows_per_seq + i) sees the slots 0 .. positions[s] + i:
+ *   p_t = softmax over them of q . k_t,  out = sum_t p_t v_t,  k_t, v_t = min + code * scale
+ * (not rounded to fp16 in between; fp32 sums and softmax).  accumulate = 1 (needs weights): each
+ * slot's weight grows by the sum over the call's rows and the R query heads of p_t, in a fixed
+ * order: the same bits from run to run.
+ * Rows i >= row_counts[s] and sequences with positions[s] = -1 see nothing: their output is zero.
+ * max_len: a bound on the slots that any row sees, for the launch's plan (0: max_pages *
+ * page_size).  A sequence with a row that would see more, a position below -1 or a bad count flags
+ * FG_ERR_RANGE; its rows are zero and its weights do not grow.  A row that sees a slot in a bad page
+ * flags it too and is zero; the sequence's other rows are zero or as they would be, and its weights
+ * have grown by the rows that are not zero.
+ * workspace: fg_paged_attention_workspace_bytes of device scratch (16-byte aligned), nothing kept
+ * in it between calls; with less the attention is split less, or accumulate is refused
+ * (FG_ERR_WORKSPACE).  Two calls that may run at once need a workspace each. */
+FG_API size_t fg_paged_attention_workspace_bytes(const fg_paged_kv *kv, int num_q_heads, int rows, int rows_per_seq,
+                                                 int max_len, int accumulate);
+FG_API fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q, int64_t ldq, int num_q_heads, fg_half *out,
+                                    int64_t ldo, int rows, int rows_per_seq, const int32_t *positions,
+                                    const int32_t *row_counts, int max_len, int accumulate, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* Evicts slots of a tracked cache by accumulated attention weight, each head its own: of a sequence
+ * whose lengths[s] slots are more than `budget`, every head keeps the slots whose token is one of
+ * the last `recent` ones (token >= next_tokens[s] - recent), then those of the largest weight, ties
+ * to the lower slot, `budget` in all (recent <= budget; a NaN weight ranks below all others, -0 as
+ * 0).  A kept slot below the budget stays where it is; the kept ones at or above it move, in order,
+ * into the holes below it, with their weight and token: attention does not depend on the slots'
+ * order, and what moves is as little as the eviction frees.  new_lengths[s] = min(lengths[s],
+ * budget); the pages behind are the caller's again.  Sequences within the budget are not touched.
+ *   lengths, next_tokens, new_lengths: int32 device [num_seqs] (new_lengths may be lengths);
+ *   next_tokens: the number that the sequence's next token will get.
+ *   weights_out, tokens_out: pools like weights and tokens that receive the kept slots' numbers in
+ *   place of those (every slot below new_lengths[s], moved or not); NULL, or the pool itself: in place.
+ *   max_len: a bound on lengths[s] for the launch's plan (0: max_pages * page_size).
+ * A length above max_len or the table's pages or below -1 (-1: no sequence), or a bad page in it,
+ * flags FG_ERR_RANGE and leaves the sequence as it is, new_lengths[s] = lengths[s].
+ * workspace: fg_paged_kv_evict_workspace_bytes of device scratch (16-byte aligned), nothing kept. */
+FG_API size_t fg_paged_kv_evict_workspace_bytes(const fg_paged_kv *kv, int budget, int max_len);
+FG_API fg_status fg_paged_kv_evict(const fg_paged_kv *kv, const int32_t *lengths, const int32_t *next_tokens, int budget,
+                                   int recent, int max_len, int32_t *new_lengths, float *weights_out,
+                                   int32_t *tokens_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* W4A16 linear layer and LayerNorm                                         */
 /* ---------------------------------------------------------------------- */
 

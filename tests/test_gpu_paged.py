@@ -1,0 +1,696 @@
+"""The paged 4-bit KV cache against plain implementations in 64 bits: append (bit for bit), attention with and without
+the accumulation of its weights, eviction (exact), and a run of them together.
+
+Attention's tolerance, per output value.  The kernel holds scores, softmax and sums in fp32; it rounds twice to fp16:
+the product w = p * scale of each slot and group that multiplies the codes (at most half a step, 2^-11 relative, or
+2^-25 absolute where w is subnormal; the rounding's share that all codes of the group have in common, 7.5 * (w' - w), is
+taken back, so a code's error weighs at most |c - 7.5| <= 7.5), and the output (2^-11).  With q.k = sum_g (min_g sum q +
+scale_g sum q c), each of the <= D + 2 D/G fp32 additions and products of a score is off by 2^-24 of magnitudes below
+A = sum |q| (|min| + 15 scale) in each direction, twice that on a tensor core that truncates; exp2 adds 2^-21 and each of
+the n/128 + 8 chained additions and rescalings of the sums 2^-23.  So
+  |out - ref| <= 2^-11 (|ref| + sum p scale 7.5) + 2 delta sum p (|min| + 15 scale) + n 2^-25 * 7.5 * 4 / l
+  delta = 2 (D + 2 D/G) 2^-23 max A + 2^-21 + (n/128 + 8) 2^-23,  l = sum exp(s - max s)
+(4: the running reference of the exponent may lie 2 binary orders below the maximum).  A slot's weight grows by sums of
+p: delta of the growth, and 2^-23 per addition (one for each row and head) of the total."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import seeded_inputs as si
+
+pytestmark = pytest.mark.gpu
+
+fg = None
+
+
+@pytest.fixture(autouse=True)
+def _bind_library(fg_lib):
+    global fg
+    fg = fg_lib
+
+
+RANGE = 4
+
+
+def flagged(code=RANGE):
+    with pytest.raises(fg.FgError) as e:
+        fg.fg_sync_status()
+    assert e.value.code == code
+
+
+def make_cache(rng, lengths, H, D, G, ps, track=False, extra=3, spread=1.0, poison=True):
+    """A cache of random groups: lengths[s] slots of each sequence hold data, every other slot of every page holds NaN,
+    infinite or huge numbers, and table entries past a sequence's pages hold numbers that are no pages."""
+    S = len(lengths)
+    width = max(1, max(-(-n // ps) for n in lengths)) + 1
+    pages = sum(-(-n // ps) for n in lengths) + extra
+    order = rng.permutation(pages)
+    table = np.full((S, width), -7, np.int32)
+    table[:, 1::2] = 2**31 - 1
+    used, at = np.zeros((pages, ps), bool), 0
+    for s, n in enumerate(lengths):
+        for i in range(-(-n // ps)):
+            table[s, i] = order[at]
+            used[order[at], : min(ps, n - i * ps)] = True
+            at += 1
+    NG = D // G
+    arrays = []
+    for _ in range(2):
+        arrays.append(rng.integers(0, 256, (pages, H, ps, D // 2), dtype=np.uint8))
+        arrays.append((rng.normal(-2.4, 0.4, (pages, H, ps, NG)) * spread).astype(np.float16))
+        arrays.append((np.abs(rng.normal(0.31, 0.05, (pages, H, ps, NG))) * spread).astype(np.float16))
+    if poison:
+        free = ~np.broadcast_to(used[:, None, :, None], (pages, H, ps, NG))
+        bad = np.array([np.nan, np.inf, -np.inf, 65504, -65504], np.float16)
+        for i in (1, 2, 4, 5):
+            arrays[i] = np.where(free, bad[rng.integers(0, 5, free.shape)], arrays[i])
+    dev = [torch.from_numpy(a).cuda() for a in arrays]
+    c = fg.PagedKVCache(pages, H, D, ps, torch.from_numpy(table).cuda(), group=G, arrays=dev, track=track)
+    if track:
+        w = np.exp(rng.normal(-7, 2, (pages, H, ps))).astype(np.float32)
+        c.weights.copy_(torch.from_numpy(w))
+        c.tokens.copy_(torch.from_numpy(rng.integers(0, 1 << 20, (pages, H, ps), dtype=np.int32)))
+    return c
+
+
+def dense(cache, pool, s, n):
+    """Sequence s's first n slots of a pool as numpy [H, n, ...]."""
+    ps = cache.page_size
+    t = cache.page_table[s].cpu().numpy()
+    a = pool.cpu().numpy()
+    if n == 0:
+        return a[:0].reshape((a.shape[1], 0) + a.shape[3:])
+    return np.concatenate([a[t[i]] for i in range(-(-n // ps))], 1)[:, :n]
+
+
+def values(cache, s, n, side):
+    """(values, magnitudes |min| + 15 scale, scales, each [H, n, D] float64) of k or v."""
+    c = dense(cache, getattr(cache, side + "_codes"), s, n)
+    mn = np.repeat(dense(cache, getattr(cache, side + "_mins"), s, n).astype(np.float64), cache.group, -1)
+    sc = np.repeat(dense(cache, getattr(cache, side + "_scales"), s, n).astype(np.float64), cache.group, -1)
+    codes = np.stack((c & 15, c >> 4), -1).reshape(c.shape[:-1] + (-1,)).astype(np.float64)
+    return mn + codes * sc, np.abs(mn) + 15 * sc, sc
+
+
+def ref_attention(cache, q, positions, rows_per_seq, counts=None):
+    """(out, tolerance, {(s): (growth of weights [H, n], its tolerance)}) in float64."""
+    q = q.cpu().numpy().astype(np.float64)
+    rows, D, H = q.shape[0], cache.head_dim, cache.num_heads
+    R = q.shape[1] // D // H
+    q = q.reshape(rows, H, R, D)
+    out, tol, grown = np.zeros_like(q), np.zeros_like(q), {}
+    NG = D // cache.group
+    for s in range(rows // rows_per_seq):
+        count = rows_per_seq if counts is None else counts[s]
+        if positions[s] < 0 or count == 0:
+            continue
+        n = positions[s] + count
+        k, ka, _ = values(cache, s, n, "k")
+        v, va, vs = values(cache, s, n, "v")
+        add, add_tol = np.zeros((H, n)), np.zeros((H, n))
+        for i in range(count):
+            r, m = s * rows_per_seq + i, positions[s] + i + 1
+            sc = np.einsum("hrd,htd->hrt", q[r], k[:, :m])
+            e = np.exp(sc - sc.max(-1, keepdims=True))
+            l = e.sum(-1, keepdims=True)
+            p = e / l
+            A = np.einsum("hrd,htd->hrt", np.abs(q[r]), ka[:, :m]).max(-1, keepdims=True)
+            delta = 2 * (D + 2 * NG) * 2.0**-23 * A + 2.0**-21 + (m / 128 + 8) * 2.0**-23
+            o = np.einsum("hrt,htd->hrd", p, v[:, :m])
+            out[r] = o
+            tol[r] = (2.0**-11 * (np.abs(o) + 7.5 * np.einsum("hrt,htd->hrd", p, vs[:, :m]))
+                      + 2 * delta * np.einsum("hrt,htd->hrd", p, va[:, :m]) + m * 2.0**-25 * 30 / l)
+            add[:, :m] += p.sum(1)
+            add_tol[:, :m] += (2 * delta * p).sum(1)
+        grown[s] = (add, add_tol)
+    return out.reshape(rows, -1), tol.reshape(rows, -1), grown
+
+
+def check_attention(cache, q, positions, rows_per_seq=1, counts=None, max_len=None, accumulate=False, workspace=None):
+    pos = torch.tensor(positions, dtype=torch.int32, device="cuda")
+    cnt = None if counts is None else torch.tensor(counts, dtype=torch.int32, device="cuda")
+    before = cache.weights.clone() if accumulate else None
+    out = fg.fg_paged_attention(cache, q, pos, rows_per_seq=rows_per_seq, row_counts=cnt, max_len=max_len,
+                                accumulate=accumulate, workspace=workspace)
+    fg.fg_sync_status()
+    ref, tol, grown = ref_attention(cache, q, positions, rows_per_seq, counts)
+    err = np.abs(out.cpu().numpy().astype(np.float64) - ref)
+    assert np.all(err <= tol), (err.max(), (err / np.maximum(tol, 1e-30)).max())
+    if accumulate:
+        want, slack = before.cpu().numpy().astype(np.float64), np.zeros(before.shape)
+        per = rows_per_seq * (q.shape[1] // cache.head_dim // cache.num_heads)
+        t = cache.page_table.cpu().numpy()
+        for s, (add, add_tol) in grown.items():
+            for i in range(0, add.shape[1], cache.page_size):
+                a, b = add[:, i:i + cache.page_size], add_tol[:, i:i + cache.page_size]
+                at = (t[s, i // cache.page_size], slice(None), slice(0, a.shape[1]))
+                want[at] += a
+                slack[at] += b + (per + 2) * 2.0**-23 * want[at]
+        got = cache.weights.cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - want) <= slack), (np.abs(got - want) / np.maximum(slack, 1e-30)).max()
+    return out
+
+
+def queries(rng, rows, heads, D, size=1.5):
+    return torch.from_numpy((rng.normal(0, size * D**-0.5, (rows, heads * D))).astype(np.float16)).cuda()
+
+
+# ------------------------------------------------------------------ append ------------
+
+
+@pytest.mark.parametrize("D,G,ps", [(64, 64, 16), (128, 64, 48), (128, 128, 64), (256, 64, 16), (256, 128, 80)])
+@pytest.mark.parametrize("rows,counts,positions", [
+    (1, None, [0, 15, 16, -1, 70]), (5, None, [0, 14, -1, 60, 31]), (40, [40, 0, 1, 17, 33], [0, 3, 47, 48, -1])])
+def test_append_bits(D, G, ps, rows, counts, positions):
+    rng = np.random.default_rng(D + ps + rows)
+    S, H = len(positions), 3
+    cap = 128
+    c = make_cache(rng, [cap] * S, H, D, G, ps, track=True)
+    before = [a.clone() for a in c.arrays() + [c.weights, c.tokens]]
+    qkv = si.normal_f16(3, 5, (S * rows, 3 * H * D), 1.0)
+    qkv[0, H * D:H * D + G] = 0.5                                       # a constant group: scale 0
+    dev = torch.from_numpy(qkv).cuda()
+    k, v = dev[:, H * D:2 * H * D], dev[:, 2 * H * D:]
+    if counts is not None:                                              # the padding may hold anything
+        for s in range(S):
+            dev[s * rows + counts[s]:(s + 1) * rows] = float("nan")
+    first = torch.arange(100, 100 + S, dtype=torch.int32, device="cuda") * 1000
+    i32 = lambda x: None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+    fg.fg_paged_kv_append(c, k, v, i32(positions), rows_per_seq=rows, row_counts=i32(counts), first_tokens=first)
+    fg.fg_sync_status()
+    want = [a.cpu().numpy() for a in before]
+    t = c.page_table.cpu().numpy()
+    for s in range(S):
+        for i in range(rows if counts is None else counts[s]):
+            if positions[s] < 0:
+                continue
+            p = positions[s] + i
+            at = (t[s, p // ps], slice(None), p % ps)
+            for side, x in ((0, k), (3, v)):
+                r = oracle.quantize(x[s * rows + i].cpu().numpy().reshape(H, D), group=G)
+                want[side][at], want[side + 1][at], want[side + 2][at] = r.codes, r.mins, r.scales
+            want[6][at], want[7][at] = 0.0, 100000 + s * 1000 + i
+    for a, w in zip(c.arrays() + [c.weights, c.tokens], want):
+        assert np.array_equal(a.cpu().numpy().view(np.uint8), w.view(np.uint8))
+
+
+def test_append_equals_the_contiguous_cache():
+    S, H, D, L, P = 3, 4, 128, 128, 21
+    a, b = fg.KVCache(S, H, D, L), fg.KVCache(S, H, D, L)
+    k = torch.from_numpy(si.normal_f16(1, 22, (S * P, H * D), 1.0)).cuda()
+    v = torch.from_numpy(si.normal_f16(1, 23, (S * P, H * D), 1.0)).cuda()
+    pos = torch.tensor([0, 40, 107], dtype=torch.int32, device="cuda")
+    fg.fg_kv_append(a, k, v, pos, rows_per_seq=P)
+    c = fg.PagedKVCache.from_cache(b, track=True)
+    fg.fg_paged_kv_append(c, k, v, pos, rows_per_seq=P)
+    fg.fg_sync_status()
+    for x, y in zip(a.arrays(), b.arrays()):
+        assert torch.equal(x, y)
+    assert c.tokens[1, 2, 40:61].tolist() == list(range(40, 61))        # without first_tokens: the slots' own numbers
+
+
+def test_append_flags_bad_slots_and_leaves_the_rest():
+    rng = np.random.default_rng(1)
+    H, D, ps = 2, 128, 16
+    c = make_cache(rng, [48] * 6, H, D, 64, ps, track=True)
+    c.page_table[1, 0] = c.num_pages                                    # a page that is none
+    c.page_table[2, 0] = -1
+    before = [a.clone() for a in c.arrays() + [c.weights, c.tokens]]
+    k = torch.from_numpy(si.normal_f16(2, 22, (12, H * D), 1.0)).cuda()
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    # past the table's pages; two bad pages; below -1; a count above rows_per_seq; a count below 0
+    fg.fg_paged_kv_append(c, k, k, i32([c.max_pages * ps, 3, 15, -2, 0, 0]), rows_per_seq=2, row_counts=i32([2, 2, 1, 2, 3, -1]))
+    flagged()
+    for a, b in zip(c.arrays() + [c.weights, c.tokens], before):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    fg.fg_paged_kv_append(c, k, k, i32([2**31 - 1, -1, -1, -1, -1, 4]), rows_per_seq=2)   # no overflow past int32
+    flagged()
+    r = oracle.quantize(k[11].cpu().numpy().reshape(H, D))
+    page = int(c.page_table[5, 0])
+    assert np.array_equal(c.v_codes[page, :, 5].cpu().numpy(), r.codes)
+    fg.fg_sync_status()                                                 # and the flag is gone
+
+
+# ------------------------------------------------------------------ attention ---------
+
+SHAPES = [  # D, G, page, kv heads, ratio
+    (64, 64, 16, 2, 1), (64, 64, 64, 3, 4), (128, 64, 48, 2, 1), (128, 64, 16, 1, 8), (128, 128, 64, 2, 3),
+    (256, 64, 80, 1, 5), (256, 128, 32, 2, 1), (128, 64, 128, 4, 9), (256, 64, 16, 1, 17), (64, 64, 32, 1, 2),
+]
+
+
+@pytest.mark.parametrize("accumulate", [False, True], ids=["plain", "tracked"])
+@pytest.mark.parametrize("D,G,ps,H,R", SHAPES)
+def test_attention_one_new_token(D, G, ps, H, R, accumulate):
+    rng = np.random.default_rng(D * 7 + ps + R)
+    lengths = [1, 2, 15, 16, 17, 31, 33, 64, 65, 127, 128, 129, 300, 511]
+    c = make_cache(rng, lengths, H, D, G, ps, track=accumulate)
+    q = queries(rng, len(lengths), H * R, D)
+    check_attention(c, q, [n - 1 for n in lengths], accumulate=accumulate)
+
+
+@pytest.mark.parametrize("accumulate", [False, True], ids=["plain", "tracked"])
+@pytest.mark.parametrize("D,G,ps,H,R", SHAPES)
+def test_attention_rows_counts_and_inactive_sequences(D, G, ps, H, R, accumulate):
+    rng = np.random.default_rng(D + ps * 5 + R)
+    rows = 6
+    counts = [6, 0, 1, 5, 6, 3]
+    positions = [0, 9, 200, 31, -1, 16 * 9 - 2]
+    c = make_cache(rng, [max(0, p) + n if p >= 0 else 0 for p, n in zip(positions, counts)], H, D, G, ps, track=accumulate)
+    q = queries(rng, len(counts) * rows, H * R, D)
+    for s, n in enumerate(counts):                                      # the padding's queries may hold anything
+        q[s * rows + n:(s + 1) * rows] = float("nan")
+    q.view(len(counts), rows, -1)[4] = float("inf")
+    zeros = torch.zeros_like(q)
+    qz = torch.where(torch.isfinite(q), q, zeros)
+    pos = torch.tensor(positions, dtype=torch.int32, device="cuda")
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    out = fg.fg_paged_attention(c, q, pos, rows_per_seq=rows, row_counts=cnt)
+    fg.fg_sync_status()
+    for s, n in enumerate(counts):
+        dead = out.view(len(counts), rows, -1)[s, (n if positions[s] >= 0 else 0):]
+        assert torch.count_nonzero(dead) == 0 and torch.isfinite(dead).all()
+    assert torch.equal(out, check_attention(c, qz, positions, rows, counts, accumulate=accumulate))
+
+
+@pytest.mark.parametrize("accumulate", [False, True], ids=["plain", "tracked"])
+@pytest.mark.parametrize("D,G,ps,H,R,lengths", [
+    (128, 64, 64, 2, 1, [20011]), (128, 128, 16, 1, 8, [9000, 1, 4097]), (64, 64, 48, 1, 1, [30000, 12]),
+    (256, 64, 128, 1, 4, [5000, 2049])])
+def test_attention_split_over_long_sequences(D, G, ps, H, R, lengths, accumulate):
+    rng = np.random.default_rng(D + R)
+    c = make_cache(rng, lengths, H, D, G, ps, track=accumulate)
+    q = queries(rng, len(lengths), H * R, D, 3.0)
+    out = check_attention(c, q, [n - 1 for n in lengths], max_len=max(lengths), accumulate=accumulate)
+    if not accumulate:                                                  # less scratch, or none: split less
+        need = fg.fg_paged_attention_workspace_bytes(c, H * R, len(lengths), 1, max(lengths))
+        for nbytes in (need // 3, 0):
+            check_attention(c, q, [n - 1 for n in lengths], max_len=max(lengths),
+                            workspace=torch.empty(nbytes, dtype=torch.uint8, device="cuda"))
+    else:
+        need = fg.fg_paged_attention_workspace_bytes(c, H * R, len(lengths), 1, max(lengths), True)
+        if need:
+            with pytest.raises(fg.FgError, match="WORKSPACE"):
+                fg.fg_paged_attention(c, q, torch.tensor([n - 1 for n in lengths], dtype=torch.int32, device="cuda"),
+                                      max_len=max(lengths), accumulate=True,
+                                      workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    assert out.shape == q.shape
+
+
+@pytest.mark.parametrize("rows,R", [(33, 1), (20, 5)])
+def test_attention_prompt_rows(rows, R):
+    rng = np.random.default_rng(rows)
+    H, D = 2, 128
+    positions = [0, 100]
+    c = make_cache(rng, [p + rows for p in positions], H, D, 64, 32, track=True)
+    check_attention(c, queries(rng, 2 * rows, H * R, D), positions, rows, accumulate=True)
+
+
+@pytest.mark.parametrize("size,spread", [(40.0, 1.0), (1.5, 2000.0), (0.0, 1.0), (300.0, 30.0)])
+def test_attention_extreme_scores_and_scales(size, spread):
+    """One-hot softmaxes, scales near fp16's largest, equal scores."""
+    rng = np.random.default_rng(int(size))
+    H, D, lengths = 2, 128, [1, 77, 700]
+    c = make_cache(rng, lengths, H, D, 64, 64, track=True, spread=spread)
+    check_attention(c, queries(rng, 3, 2 * H, D, size if spread == 1.0 else size / spread), [n - 1 for n in lengths],
+                    accumulate=True)
+
+
+def test_attention_rising_scores():
+    """Scores that grow along the sequence: the running maximum moves all the way."""
+    rng = np.random.default_rng(5)
+    H, D, n = 1, 64, 900
+    c = make_cache(rng, [n], H, D, 64, 64, track=True)
+    t = c.page_table[0].cpu().tolist()
+    for i in range(n):
+        c.k_mins[t[i // 64], :, i % 64] = i * 0.02 - 2.4
+    check_attention(c, torch.full((1, D), 0.05, dtype=torch.float16, device="cuda"), [n - 1], accumulate=True)
+
+
+def test_attention_strides_and_untouched_rows():
+    rng = np.random.default_rng(8)
+    H, R, D, lengths = 2, 2, 128, [70, 5, 200]
+    c = make_cache(rng, lengths, H, D, 64, 16)
+    q = queries(rng, 5, H * R, D)
+    wide = torch.full((5, 3 * H * R * D + 8), float("nan"), dtype=torch.float16, device="cuda")
+    wide[:, 8:8 + H * R * D] = q
+    big = torch.full((6, H * R * D + 64), 7.0, dtype=torch.float16, device="cuda")
+    pos = torch.tensor([n - 1 for n in lengths], dtype=torch.int32, device="cuda")
+    fg.fg_paged_attention(c, wide[:3, 8:8 + H * R * D], pos, out=big[:3, :H * R * D])
+    fg.fg_sync_status()
+    assert torch.equal(big[:3, :H * R * D], check_attention(c, q[:3].contiguous(), [n - 1 for n in lengths]))
+    assert (big[3:] == 7.0).all() and (big[:, H * R * D:] == 7.0).all()
+
+
+def test_attention_flags_bad_sequences_only():
+    rng = np.random.default_rng(9)
+    H, D, ps = 2, 128, 16
+    lengths = [40, 40, 40, 40, 40, 40, 40]
+    c = make_cache(rng, lengths, H, D, 64, ps, track=True)
+    c.page_table[0, 1] = c.num_pages
+    c.page_table[1, 2] = -1
+    before = c.weights.clone()
+    q = queries(rng, 7, H, D)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    # bad pages, past max_len, below -1, bad counts, and one good sequence
+    out = fg.fg_paged_attention(c, q, i32([39, 39, 40, -2, 39, 39, 39]), row_counts=i32([1, 1, 1, 1, 2, -1, 1]), max_len=40,
+                                accumulate=True)
+    flagged()
+    assert torch.count_nonzero(out[:6]) == 0
+    got = c.weights.clone()
+    mine = c.page_table[6, :3].long()
+    assert torch.count_nonzero(got[mine] - before[mine]) > 0
+    got[mine] = before[mine]
+    assert torch.equal(got, before)
+    c.weights.copy_(before)
+    good = fg.fg_paged_attention(c, q, i32([-1] * 6 + [39]), accumulate=True)
+    fg.fg_sync_status()
+    assert torch.equal(good, out)
+
+
+def test_attention_equals_the_contiguous_caches():
+    """Over one cache, the paged call and the contiguous one agree to the sum of their roundings."""
+    S, H, D, L = 4, 4, 128, 320
+    cache = fg.KVCache(S, H, D, L)
+    k = torch.from_numpy(si.normal_f16(1, 22, (S * L, H * D), 1.0)).cuda()
+    v = torch.from_numpy(si.normal_f16(1, 23, (S * L, H * D), 1.0)).cuda()
+    fg.fg_kv_append(cache, k, v, torch.zeros(S, dtype=torch.int32, device="cuda"), rows_per_seq=L)
+    q = torch.from_numpy(si.normal_f16(1, 24, (S, H * D), D**-0.5)).cuda()
+    pos = [3, 100, 319, 256]
+    c = fg.PagedKVCache.from_cache(cache)
+    out = check_attention(c, q, pos)
+    old = fg.fg_attention_decode(cache, q, torch.tensor(pos, dtype=torch.int32, device="cuda"))
+    # the contiguous kernel's bound is 2e-3 of the largest output (tests of the individual kernels)
+    assert (out.float() - old.float()).abs().max() <= 4e-3 * old.float().abs().max()
+
+
+def test_attention_is_deterministic():
+    rng = np.random.default_rng(3)
+    c = make_cache(rng, [5000, 3, 777], 2, 128, 64, 64, track=True)
+    q = queries(rng, 3, 8, 128)
+    pos = torch.tensor([4999, 2, 776], dtype=torch.int32, device="cuda")
+    w0, got = c.weights.clone(), []
+    for _ in range(5):
+        c.weights.copy_(w0)
+        got.append((fg.fg_paged_attention(c, q, pos, accumulate=True).clone(), c.weights.clone()))
+    for o, w in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(w, got[0][1])
+
+
+# ------------------------------------------------------------------ eviction ----------
+
+
+def ref_evict(cache, lengths, nxt, budget, recent):
+    """Per sequence and head, the slot that each kept place is filled from."""
+    src = {}
+    for s, n in enumerate(lengths):
+        if n <= budget:
+            continue
+        w, t = dense(cache, cache.weights, s, n), dense(cache, cache.tokens, s, n)
+        for h in range(cache.num_heads):
+            rank = lambda i: (0, 0.0, i) if t[h, i] >= nxt[s] - recent else (2, 0.0, i) if np.isnan(w[h, i]) else (1, -float(w[h, i]), i)
+            keep = set(sorted(range(n), key=rank)[:budget])
+            above = iter(sorted(i for i in keep if i >= budget))
+            src[s, h] = [i if i in keep else next(above) for i in range(budget)]
+    return src
+
+
+def check_evict(cache, lengths, nxt, budget, recent, in_place=True, max_len=None, same_lengths=False):
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    pools = cache.arrays() + [cache.weights, cache.tokens]
+    src = ref_evict(cache, lengths, nxt, budget, recent)
+    want = [a.cpu().numpy().copy() for a in pools]
+    t, ps = cache.page_table.cpu().numpy(), cache.page_size
+    old = [w.copy() for w in want]
+    wout = tout = None
+    if not in_place:
+        wout, tout = torch.full_like(cache.weights, -1.0), torch.full_like(cache.tokens, -1)
+        want += [wout.cpu().numpy(), tout.cpu().numpy()]
+    for s, n in enumerate(lengths):
+        for h in range(cache.num_heads):
+            m = np.array(src.get((s, h), range(max(0, n))), np.int64)
+            i = np.arange(len(m))
+            to, fr = (t[s, i // ps], h, i % ps), (t[s, m // ps], h, m % ps)
+            for x in range(6 if not in_place else 8):
+                want[x][to] = old[x][fr]
+            if not in_place:
+                want[8][to], want[9][to] = old[6][fr], old[7][fr]
+    ln = i32(lengths)
+    new = fg.fg_paged_kv_evict(cache, ln, i32(nxt), budget, recent, weights_out=wout, tokens_out=tout, max_len=max_len,
+                               new_lengths=ln if same_lengths else None)
+    fg.fg_sync_status()
+    assert new.tolist() == [min(n, budget) for n in lengths]
+    for a, w in zip(pools + ([] if in_place else [wout, tout]), want):
+        assert np.array_equal(a.cpu().numpy().view(np.uint8), w.view(np.uint8))
+
+
+def tokens_in_order(cache, lengths):
+    t, ps = cache.page_table.cpu(), cache.page_size
+    for s, n in enumerate(lengths):
+        for i in range(0, max(0, n), ps):
+            cache.tokens[t[s, i // ps], :, :min(ps, n - i)] = torch.arange(i, min(n, i + ps), dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("in_place", [True, False], ids=["in_place", "apart"])
+@pytest.mark.parametrize("D,G,ps,H,budget,recent", [
+    (64, 64, 16, 3, 32, 8), (128, 64, 48, 2, 100, 0), (128, 128, 64, 1, 64, 64), (256, 64, 16, 2, 257, 100),
+    (256, 128, 80, 1, 1, 0), (128, 64, 64, 2, 512, 1), (64, 64, 32, 1, 16, 16)])
+def test_evict_exact(D, G, ps, H, budget, recent, in_place):
+    rng = np.random.default_rng(budget + ps)
+    lengths = [0, 1, budget - 1, budget, budget + 1, budget + 2, budget + ps, 2 * budget + 3, 3 * budget + 700, -1]
+    c = make_cache(rng, [max(0, n) for n in lengths], H, D, G, ps, track=True)
+    tokens_in_order(c, lengths)
+    check_evict(c, lengths, lengths, budget, recent, in_place)
+
+
+@pytest.mark.parametrize("what", ["ties", "zeros", "nan", "inf", "negative", "protected_in_holes", "all_protected", "sorted", "reversed"])
+def test_evict_ranks(what):
+    rng = np.random.default_rng(len(what))
+    H, budget, lengths = 2, 96, [97, 400, 1000]
+    c = make_cache(rng, lengths, H, 128, 64, 32, track=True)
+    tokens_in_order(c, lengths)
+    nxt = list(lengths)
+    if what == "ties":
+        c.weights.copy_(torch.from_numpy(rng.integers(0, 3, c.weights.shape)))
+    elif what == "zeros":
+        c.weights.copy_(torch.from_numpy(np.where(rng.random(c.weights.shape) < 0.5, 0.0, -0.0)))
+    elif what == "nan":
+        c.weights[torch.rand(c.weights.shape, device="cuda") < 0.95] = float("nan")
+    elif what == "inf":
+        c.weights[torch.rand(c.weights.shape, device="cuda") < 0.5] = float("inf")
+    elif what == "negative":
+        c.weights.neg_()
+    elif what == "protected_in_holes":                                  # tokens of any age in any slot
+        c.tokens.copy_(torch.from_numpy(rng.permutation(c.tokens.numel()).reshape(c.tokens.shape).astype(np.int32) % 2000))
+        nxt = [2000] * 3
+    elif what == "all_protected":                                       # more protected slots than the budget
+        c.tokens.fill_(2**31 - 1)
+        nxt = [2**31 - 1] * 3
+    else:
+        t, ps = c.page_table.cpu(), c.page_size
+        for s, n in enumerate(lengths):
+            for i in range(n):
+                c.weights[t[s, i // ps], :, i % ps] = i if what == "sorted" else n - i
+    check_evict(c, lengths, nxt, budget, 24)
+
+
+@pytest.mark.parametrize("n,budget", [(20000, 1024), (9000, 8000), (40000, 39999), (5000, 16)])
+def test_evict_long(n, budget):
+    rng = np.random.default_rng(n)
+    c = make_cache(rng, [n, 100], 1, 64, 64, 64, track=True)
+    tokens_in_order(c, [n, 100])
+    c.weights.copy_(torch.round(c.weights * 2000))                      # many ties
+    check_evict(c, [n, 100], [n, 100], budget, min(budget, 128), max_len=n)
+
+
+def test_evict_writes_lengths_in_place():
+    rng = np.random.default_rng(4)
+    lengths = [300, 20, 64, -1, 0]
+    c = make_cache(rng, [300, 20, 64, 0, 0], 2, 64, 64, 16, track=True)
+    tokens_in_order(c, lengths)
+    check_evict(c, lengths, lengths, 48, 4, same_lengths=True)
+
+
+def test_evict_flags_bad_sequences_only():
+    rng = np.random.default_rng(6)
+    lengths = [100, 100, 100, 100, 100]
+    c = make_cache(rng, lengths, 2, 64, 64, 16, track=True)
+    tokens_in_order(c, lengths)
+    c.page_table[0, 6] = -3
+    c.page_table[1, 0] = c.num_pages
+    before = [a.clone() for a in c.arrays() + [c.weights, c.tokens]]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    new = fg.fg_paged_kv_evict(c, i32([100, 100, c.max_pages * 16 + 1, -2, 16]), i32(lengths), 50, 10)
+    flagged()
+    assert new.tolist() == [100, 100, c.max_pages * 16 + 1, -2, 16]
+    new = fg.fg_paged_kv_evict(c, i32([-1, -1, 100, -1, -1]), i32(lengths), 100, 10, max_len=99)
+    flagged()
+    assert new.tolist() == [-1, -1, 100, -1, -1]
+    for a, b in zip(c.arrays() + [c.weights, c.tokens], before):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ together ----------
+
+
+def step(c, qkv, H, R, D, pos, first, out, ws, stream=None):
+    hq = H * R * D
+    fg.fg_paged_kv_append(c, qkv[:, hq:hq + H * D], qkv[:, hq + H * D:], pos, first_tokens=first, stream=stream)
+    fg.fg_paged_attention(c, qkv[:, :hq], pos, accumulate=True, out=out, workspace=ws, stream=stream)
+
+
+def test_generation_at_a_budget():
+    """Prompts into pages, then decode steps; whenever a sequence has filled a page beyond the budget its heads evict
+    back to it and it goes on.  Every step's attention and weights are checked over the cache as it stands, every
+    eviction against its rule, and no kept token's codes ever change."""
+    rng = np.random.default_rng(12)
+    S, H, R, D, G, ps, budget, recent = 3, 2, 2, 128, 64, 16, 64, 24
+    width = budget // ps + 2
+    table = torch.from_numpy(rng.permutation(S * width + 2)[:S * width].reshape(S, width).astype(np.int32)).cuda()
+    c = fg.PagedKVCache(S * width + 2, H, D, ps, table, group=G, track=True)
+    prompts, P = [70, 9, 80], 80
+    data = {}                                                           # token -> (k, v) rows of a sequence
+    rows = lambda n: (torch.from_numpy(rng.normal(0, 1, (n, H * D)).astype(np.float16)).cuda() for _ in range(2))
+    k, v = rows(S * P)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    fg.fg_paged_kv_append(c, k, v, i32([0] * S), rows_per_seq=P, row_counts=i32(prompts))
+    for s in range(S):
+        for i in range(prompts[s]):
+            data[s, i] = (k[s * P + i], v[s * P + i])
+    lengths, seen = list(prompts), list(prompts)
+    evictions = 0
+    for it in range(40):
+        if max(lengths) >= budget + ps:
+            check_evict(c, lengths, seen, budget, recent, max_len=width * ps)
+            lengths = [min(n, budget) for n in lengths]
+            evictions += 1
+        k, v = rows(S)
+        fg.fg_paged_kv_append(c, k, v, i32(lengths), first_tokens=i32(seen))
+        for s in range(S):
+            data[s, seen[s]] = (k[s], v[s])
+        lengths, seen = [n + 1 for n in lengths], [n + 1 for n in seen]
+        check_attention(c, queries(rng, S, H * R, D), [n - 1 for n in lengths], max_len=width * ps, accumulate=True)
+    assert evictions >= 2
+    for s in range(S):
+        tok = dense(c, c.tokens, s, lengths[s])
+        codes = dense(c, c.v_codes, s, lengths[s])
+        for h in range(H):
+            assert len(set(tok[h])) == lengths[s] and set(range(seen[s] - recent, seen[s])) <= set(tok[h])
+            for i in range(lengths[s]):
+                r = oracle.quantize(data[s, int(tok[h, i])][1].cpu().numpy().reshape(H, D), group=G)
+                assert np.array_equal(codes[h, i], r.codes[h])
+
+
+def test_prefilled_contiguous_cache_goes_on_in_paged_calls():
+    h, H, F, S, P = 256, 4, 512, 3, 20
+    D = h // H
+    cfg = fg.LayerConfig(h, H, F)
+    lw = fg.LayerWeights.from_fp16(cfg, si.layer_weights_f16(0, h, F, std=0.05, bias_std=0.05, ln_random=True))
+    cache = fg.KVCache(S, H, D, 64)
+    x = torch.from_numpy(si.hidden_block(0, si.STREAM["prompt"], S, P, h)).cuda()
+    fg.fg_layer_prefill(cfg, lw, cache, x, torch.zeros(S, dtype=torch.int32, device="cuda"))
+    c = fg.PagedKVCache.from_cache(cache, track=True)
+    rng = np.random.default_rng(2)
+    check_attention(c, queries(rng, S, H, D), [P - 1] * S, accumulate=True)
+    tokens_in_order(c, [P] * S)
+    check_evict(c, [P] * S, [P] * S, 16, 4)
+
+
+def test_side_stream_and_graph_replay():
+    """One step captured once and replayed, two graphs that share a workspace, and calls on a stream of their own."""
+    rng = np.random.default_rng(21)
+    S, H, R, D, ps, L0 = 3, 2, 4, 128, 64, 3000
+    mk = lambda: make_cache(np.random.default_rng(5), [L0 + 8] * S, H, D, 64, ps, track=True)
+    a, b = mk(), mk()
+    xs = [queries(rng, S, H * R + 2 * H, D, 3.0) for _ in range(4)]
+    need = fg.fg_paged_attention_workspace_bytes(a, H * R, S, 1, None, True)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out_a = torch.empty((S, H * R * D), dtype=torch.float16, device="cuda")
+    pos_a = torch.full((S,), L0, dtype=torch.int32, device="cuda")
+    x = torch.empty_like(xs[0])
+    side = torch.cuda.Stream()
+    x.copy_(xs[0])
+    torch.cuda.synchronize()
+    want = []
+    for i, q in enumerate(xs):                                          # eager, on a side stream
+        pos = torch.full((S,), L0 + i, dtype=torch.int32, device="cuda")
+        out = torch.empty_like(out_a)
+        torch.cuda.synchronize()
+        step(b, q, H, R, D, pos, None, out, None, stream=side)
+        side.synchronize()
+        want.append((out, b.weights.clone()))
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(a, x, H, R, D, pos_a, None, out_a, ws)
+        graphs.append(g)
+    ws.fill_(0xFF)                                                      # nothing in the workspace is relied on
+    for i, q in enumerate(xs):
+        x.copy_(q)
+        pos_a.fill_(L0 + i)
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out_a, want[i][0]) and torch.equal(a.weights, want[i][1])
+    fg.fg_sync_status()
+
+
+def test_evict_in_a_graph():
+    rng = np.random.default_rng(31)
+    lengths = [400, 90, 399]
+    mk = lambda: make_cache(np.random.default_rng(7), lengths, 2, 64, 64, 16, track=True)
+    a, b = mk(), mk()
+    for c in (a, b):
+        tokens_in_order(c, lengths)
+    ln = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    new = torch.empty_like(ln)
+    need = fg.fg_paged_kv_evict_workspace_bytes(a, 128)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fg.fg_paged_kv_evict(a, ln, ln, 128, 32, new_lengths=new, workspace=ws)
+    ws.fill_(0xFF)
+    g.replay()
+    fg.fg_paged_kv_evict(b, ln, ln, 128, 32)
+    fg.fg_sync_status()
+    assert new.tolist() == [128, 90, 128]
+    for x, y in zip(a.arrays() + [a.weights, a.tokens], b.arrays() + [b.weights, b.tokens]):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    new2 = torch.empty_like(ln)
+    fg.fg_paged_kv_evict(a, new, ln, 128, 32, new_lengths=new2)         # within the budget: nothing moves
+    fg.fg_sync_status()
+    for x, y in zip(a.arrays(), b.arrays()):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_binding_refuses_what_it_can_see():
+    rng = np.random.default_rng(1)
+    c = make_cache(rng, [40, 40], 2, 128, 64, 16, track=True)
+    q = queries(rng, 2, 2, 128)
+    pos = torch.tensor([39, 39], dtype=torch.int32, device="cuda")
+    for bad in (dict(q=q.float()), dict(q=q[:, :200]), dict(q=q.cpu()), dict(q=q[:, ::2]), dict(positions=pos.long()),
+                dict(positions=pos[:1]), dict(positions=pos.cpu()), dict(out=q[:1]), dict(out=q[:, :128]),
+                dict(row_counts=pos.float()), dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            fg.fg_paged_attention(**(dict(cache=c, q=q, positions=pos) | bad))
+    with pytest.raises(fg.FgError, match="SHAPE"):
+        fg.fg_paged_attention(c, q[:, :128], pos)                       # one query head for two key-value heads
+    with pytest.raises(ValueError):
+        fg.fg_paged_kv_append(c, q, q[:1], pos)
+    with pytest.raises(ValueError):
+        fg.fg_paged_kv_evict(c, pos, pos, 16, 4, weights_out=c.weights[:1])
+    with pytest.raises(ValueError):
+        fg.PagedKVCache(4, 2, 128, 16, c.page_table, arrays=c.arrays()[:5] + [c.v_scales[:1]])
+    with pytest.raises(fg.FgError, match="SHAPE"):
+        fg.PagedKVCache(4, 2, 128, 40, c.page_table)
+    plain = fg.PagedKVCache(c.num_pages, 2, 128, 16, c.page_table, arrays=c.arrays())
+    with pytest.raises(fg.FgError, match="INVALID"):
+        fg.fg_paged_attention(plain, q, pos, accumulate=True)
+    with pytest.raises(fg.FgError, match="INVALID"):
+        fg.fg_paged_kv_evict(plain, pos, pos, 16, 4)
+    none = fg.fg_paged_attention(c, q[:0], pos)                         # no rows: nothing to do
+    assert none.shape == (0, 256)
+    fg.fg_sync_status()
