@@ -1,12 +1,48 @@
-// fg_paged_attention.cu -- softmax attention of query rows over the paged 4-bit KV cache, and the
-// accumulation of its probabilities in the slots' weights.
+// fg_paged_attention.cu -- softmax attention of query rows over the paged 4-bit KV cache, split
+// over the cache's length and joined, and the accumulation of its probabilities in the slots'
+// weights.
+//
+// "FlexGen Guide: High-Throughput LLM Offloading on One GPU", section 3: the KV cache is held as
+// 4-bit groups and dequantised on the fly for the attention dot products.
+//
+// The query rows of a sequence that share a key-value head -- its new tokens' rows times the query
+// heads of the head's group -- are columns of one product.  A tile is 8 of them, the width of an
+// mma.sync n8 operand: with more than one live column the codes are read and unpacked once for all.
+// A CTA takes one (sequence, key-value head, column tile) over C slots of the sequence; its four
+// warps take 32-slot blocks in turn, each with a pipeline of its own: kStages blocks of codes and
+// group numbers in flight by bulk copies (cp.async.bulk), an mbarrier per stage, and no barrier of
+// the CTA before the end.  A block lies in one or two pages (page_size % 16 == 0), six copies each,
+// issued by as many lanes; the lanes look the table up for 32 blocks at a time.
+//
+// Both products run on the tensor cores straight from the codes (the group decomposition):
+//     q . k_t = sum_g ( min_tg * sum_{d in g} q_d  +  scale_tg * sum_{d in g} q_d c_td )
+//     o_d     = sum_t p_t (min_tg + 7.5 scale_tg)  +  sum_t w_tg c_td  -  7.5 sum_t w_tg
+// with w_tg = p_t scale_tg rounded to fp16, the operand's type.  The last term, one more MMA per
+// group with an operand of ones, takes back what the rounding of w has in common for all codes, so
+// that an error of w weighs |c - 7.5| instead of c.  A nibble left in bits 0-3 of a 16-bit half is
+// the fp16 subnormal c * 2^-24, one in bits 4-7 is c * 2^-20, both exact: an AND per pair of codes
+// unpacks them, and the fp32 results are rescaled by the power of two.  Scores, softmax state and
+// sums are fp32.
+//   scores: A = codes of 16 slots x 16 dims of one group, B = q (16 dims x 8 columns)
+//   output: A = codes of 16 dims x 16 slots, B = w of the dims' group (16 slots x 8 columns), which
+//           is the score tile's layout transposed (movmatrix)
+// Both score and output fragments give a lane the columns 2c, 2c+1 (c = lane % 4), so the softmax
+// state of a column never leaves its lanes.
 #include <math.h>
 
 #include "fg_paged.cuh"
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kBlock = 32;              // slots per warp step
+constexpr int kCta = kWarps * kBlock;   // slots per CTA step
+constexpr int kCols = 8;                // columns per tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 2.0f;
+constexpr uint32_t kLoNib = 0x000F000Fu;  // bits 0-3 of both halves: c * 2^-24
+constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves: c * 2^-20
+constexpr uint32_t kOnes = 0x3C003C00u;   // fp16 {1, 1}
 
 struct PagedAttnArgs {
   PagedArgs kv;
@@ -14,121 +50,592 @@ struct PagedAttnArgs {
   int64_t ldq;
   __half *out;
   int64_t ldo;
-  int R, rows_per_seq, limit, accumulate;
+  int R, rows_per_seq, limit;
+  int tile0, tiles;    // column tiles of this launch: tile0 .. tile0 + tiles - 1
+  int split, nsplit;   // slots per split (a multiple of kCta), splits
   const int32_t *positions, *counts;
+  float2 *ml;          // [items][nsplit][8]: running maximum (log2 units) and sum; sum < 0: a bad page
+  float *po;           // [items][nsplit][8][D] unnormalised outputs (nsplit > 1)
+  float *scores;       // [items][8][score_ld] (accumulate)
+  int64_t score_ld;
 };
 
-__device__ __forceinline__ float block_max(float v, float *red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = red[0];
-  for (int w = 1; w < kThreads / 32; w++) t = fmaxf(t, red[w]);
-  return t;
-}
+// One (sequence, key-value head, column tile): items are numbered tile-fastest.
+struct Item {
+  int s, h, n0, ncols;  // columns n0 .. n0 + ncols - 1 of the head (column n: row n / R, query head n % R)
+  int pos, live;        // first new slot; rows of the sequence that see anything
+  __device__ __forceinline__ int len(int n, int R) const {  // slots that column n sees
+    const int i = n / R;
+    return i < live ? pos + i + 1 : 0;
+  }
+};
 
-__device__ __forceinline__ float block_sum(float v, float *red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = red[0];
-  for (int w = 1; w < kThreads / 32; w++) t += red[w];
-  return t;
-}
-
-// One CTA per (sequence, key-value head); its rows and query heads one after the other.  A thread
-// takes a slot's score, then a head dim's sum; the running maximum and sum follow 128-slot chunks.
-template <int D, int G>
-__global__ void __launch_bounds__(kThreads) paged_attn_kernel(const PagedAttnArgs a) {
-  constexpr int NG = D / G;
-  __shared__ float q[D], p[kThreads], red[kThreads / 32];
-  __shared__ int64_t slots[kThreads];
-  __shared__ int bad;
-  const int s = blockIdx.x / a.kv.H, h = blockIdx.x % a.kv.H, tid = threadIdx.x;
-  const int pos = a.positions[s], count = a.counts ? a.counts[s] : a.rows_per_seq;
+__device__ __forceinline__ Item load_item(const PagedAttnArgs &a, int item, bool flag) {
+  Item it;
+  const int sh = item / a.tiles, tile = a.tile0 + item % a.tiles;
+  it.s = sh / a.kv.H;
+  it.h = sh % a.kv.H;
+  it.n0 = tile * kCols;
+  it.ncols = min(kCols, a.rows_per_seq * a.R - it.n0);
+  const int pos = a.positions[it.s], count = a.counts ? a.counts[it.s] : a.rows_per_seq;
   const bool range = pos < -1 || count < 0 || count > a.rows_per_seq ||
                      (pos >= 0 && static_cast<int64_t>(pos) + count > a.limit);
-  if (range && tid == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
-  const int live = range || pos < 0 ? 0 : count;
+  if (range && flag) atomicOr(a.kv.err, FG_DEVERR_RANGE);
+  it.pos = pos;
+  it.live = range || pos < 0 ? 0 : count;
+  return it;
+}
 
-  auto score = [&](int64_t slot) {
-    float t = 0.f;
-    for (int g = 0; g < NG; g++) {
-      float dot = 0.f, sum = 0.f;
-      for (int i = 0; i < G / 2; i++) {
-        const uint32_t b = a.kv.kc[slot * (D / 2) + g * (G / 2) + i];
-        dot += q[g * G + 2 * i] * static_cast<float>(b & 15u) + q[g * G + 2 * i + 1] * static_cast<float>(b >> 4);
-        sum += q[g * G + 2 * i] + q[g * G + 2 * i + 1];
-      }
-      t += __half2float(a.kv.km[slot * NG + g]) * sum + __half2float(a.kv.ks[slot * NG + g]) * dot;
-    }
-    return t;
-  };
+template <int D, int G>
+struct Shape {
+  static constexpr int NG = D / G;
+  static constexpr int RB = D / 2;                 // code bytes per slot
+  static constexpr int KW = G / 32;                // K code words per lane, slot and group
+  static constexpr int VW = G / 64;                // V code words per lane, slot and group
+  static constexpr int CODE_B = kBlock * RB, META_B = kBlock * NG * 2;
+  static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
+  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 4 : 2;
+  static constexpr int WARP_B = kStages * STAGE_B;  // >= 8 * D * 4, the warp's outputs at the end
+  static constexpr int SMEM = kWarps * WARP_B;
+  static constexpr int kCtas = 3;
+};
 
-  for (int i = 0; i < a.rows_per_seq; i++) {
-    for (int j = 0; j < a.R; j++) {
-      const int64_t r = static_cast<int64_t>(s) * a.rows_per_seq + i;
-      const int hq = h * a.R + j;
-      __half *out = a.out + r * a.ldo + hq * D;
-      __syncthreads();
-      if (tid == 0) bad = 0;
-      for (int d = tid; d < D; d += kThreads) q[d] = __half2float(a.q[r * a.ldq + hq * D + d]);
-      __syncthreads();
-      const int L = i < live ? pos + i + 1 : 0;
-      float m = -INFINITY, l = 0.f, o[(D + kThreads - 1) / kThreads] = {0.f};
-      for (int t0 = 0; t0 < L; t0 += kThreads) {
-        const int t = t0 + tid, n = min(kThreads, L - t0);
-        float sc = -INFINITY;
-        if (t < L) {
-          slots[tid] = paged_slot(a.kv, s, h, t);
-          if (slots[tid] < 0) bad = 1;
-          else sc = score(slots[tid]);
-        }
-        const float mc = block_max(sc, red);  // (its barriers also publish slots and bad)
-        if (bad) break;
-        const float mn = fmaxf(m, mc), alpha = expf(m - mn);
-        p[tid] = t < L ? expf(sc - mn) : 0.f;
-        l = l * alpha + block_sum(p[tid], red);
-        m = mn;
-        for (int e = 0; e * kThreads + tid < D; e++) {
-          const int d = e * kThreads + tid;
-          float acc = o[e] * alpha;
-          for (int x = 0; x < n; x++) {
-            const uint32_t b = a.kv.vc[slots[x] * (D / 2) + d / 2];
-            const float c = static_cast<float>(d & 1 ? b >> 4 : b & 15u);
-            acc += p[x] * (__half2float(a.kv.vm[slots[x] * NG + d / G]) + c * __half2float(a.kv.vs[slots[x] * NG + d / G]));
-          }
-          o[e] = acc;
-        }
-        __syncthreads();
-      }
-      if (bad && tid == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
-      for (int e = 0; e * kThreads + tid < D; e++)
-        out[e * kThreads + tid] = __float2half_rn(L > 0 && !bad ? o[e] / l : 0.f);
-      if (a.accumulate && !bad)
-        for (int t = tid; t < L; t += kThreads) {
-          const int64_t slot = paged_slot(a.kv, s, h, t);
-          a.kv.weights[slot] += expf(score(slot) - m) / l;
-        }
-    }
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_h2(__half lo, __half hi) {
+  const __half2 h = __halves2half2(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
   }
 }
 
 template <int D, int G>
-fg_status launch(const PagedAttnArgs &a, int seqs, cudaStream_t st) {
-  paged_attn_kernel<D, G><<<static_cast<unsigned>(seqs) * a.kv.H, kThreads, 0, st>>>(a);
-  return fg_launch_check();
+__global__ void __launch_bounds__(kWarps * 32, Shape<D, G>::kCtas) paged_attn_kernel(const PagedAttnArgs a) {
+  using S = Shape<D, G>;
+  constexpr int NG = S::NG, RB = S::RB, KW = S::KW, VW = S::VW, ST = S::kStages;
+  constexpr float kS24 = 16777216.0f, kS20 = 1048576.0f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full_bar[kWarps][ST];
+  __shared__ float red_m[kWarps][kCols], red_l[kWarps][kCols];
+  __shared__ int bad_page;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, c = lane & 3;
+  const int item = blockIdx.x / a.nsplit, sp = blockIdx.x % a.nsplit;
+  const Item it = load_item(a, item, sp == 0 && tid == 0);
+  // live columns' lengths: rows ascend with the column, so the last live one sees most
+  int lmin = 0, lmax = 0;
+  {
+    const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
+    if (last >= it.n0) {
+      lmin = it.len(it.n0, a.R);
+      lmax = it.len(last, a.R);
+    }
+  }
+  const int t_begin = sp * a.split, t_end = min(lmax, t_begin + a.split);
+  if (t_begin >= t_end && (sp > 0 || a.nsplit > 1)) return;  // (the join zeroes rows that see nothing)
+  const int nblk = t_end > t_begin ? (t_end - t_begin + kBlock - 1) / kBlock : 0;
+  const int steps = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;
+
+  if (tid == 0) bad_page = 0;
+  if (lane == 0) {
+    for (int i = 0; i < ST; i++) mbar_init(smem_u32(&full_bar[warp][i]), 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+
+  uint8_t *const wbase = smem + warp * S::WARP_B;
+  // pool slots of the first and second 16 slots of block `lane` of the current 32 steps
+  int64_t slot_a = 0, slot_b = 0;
+  bool bad = false;
+  auto issue = [&](int k) {  // every lane; step k of this warp into stage k % ST
+    const int t = t_begin + (k * kWarps + warp) * kBlock;
+    if ((k & 31) == 0) {
+      const int tl = t + lane * kCta;
+      slot_a = tl < t_end ? paged_slot(a.kv, it.s, it.h, tl) : 0;
+      slot_b = tl + 16 < t_end ? paged_slot(a.kv, it.s, it.h, tl + 16) : 0;
+      // a bad page: flagged below, its slots read from the pool's first instead
+      if (slot_a < 0 || slot_b < 0) bad = true;
+      slot_a = slot_a < 0 ? 0 : slot_a;
+      slot_b = slot_b < 0 ? 0 : slot_b;
+    }
+    const int64_t sa = __shfl_sync(0xffffffffu, slot_a, k & 31), sb = __shfl_sync(0xffffffffu, slot_b, k & 31);
+    const bool second = t + 16 < t_end, joined = second && sb == sa + 16;
+    const uint32_t bar = smem_u32(&full_bar[warp][k % ST]);
+    if (lane == 0) mbar_arrive_expect_tx(bar, (second ? 32 : 16) * (2 * RB + 8 * NG));
+    __syncwarp();
+    const int arr = lane & 7, run = lane >> 3;  // lanes 0-5: first run, 8-13: second
+    if (arr < 6 && (run == 0 || (run == 1 && second && !joined))) {
+      const bool codes = arr < 2;
+      const int per = codes ? RB : NG * 2;
+      const uint8_t *pool = arr == 0   ? a.kv.kc
+                            : arr == 1 ? a.kv.vc
+                            : arr == 2 ? reinterpret_cast<const uint8_t *>(a.kv.km)
+                            : arr == 3 ? reinterpret_cast<const uint8_t *>(a.kv.ks)
+                            : arr == 4 ? reinterpret_cast<const uint8_t *>(a.kv.vm)
+                                       : reinterpret_cast<const uint8_t *>(a.kv.vs);
+      const int off = (k % ST) * S::STAGE_B + (codes ? arr * S::CODE_B : 2 * S::CODE_B + (arr - 2) * S::META_B);
+      bulk_g2s(smem_u32(wbase + off + run * 16 * per), pool + (run ? sb : sa) * per, (joined ? 32 : 16) * per, bar);
+    }
+  };
+  for (int k = 0; k < min(ST, steps); k++) issue(k);
+
+  // ---- q of column n0 + gid as the B operand of the score MMAs ----
+  // Word j of group g of lane class c: dims 2o .. 2o+7, o = g*G/2 + c*G/8 + 4j.  Low-nibble MMA
+  // (bits 0-3 of w and of w >> 8): k slots (2c, 2c+1) = dims (2o, 2o+4), (2c+8, 2c+9) = (2o+2,
+  // 2o+6); high-nibble MMA: the same + 1.
+  uint32_t qf[NG][KW][4];
+  float qsum[2][NG];  // columns 2c, 2c+1: sum of q over the group, times log2(e)
+  {
+    const bool on = gid < it.ncols && it.len(it.n0 + gid, a.R) > 0;
+    const int n = it.n0 + gid;
+    const __half *qrow = a.q + (static_cast<int64_t>(it.s) * a.rows_per_seq + n / a.R) * a.ldq +
+                         (static_cast<int64_t>(it.h) * a.R + n % a.R) * D;
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < KW; j++) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (on) v = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
+        const __half *e = reinterpret_cast<const __half *>(&v);
+        qf[g][j][0] = pack_h2(e[0], e[4]);
+        qf[g][j][1] = pack_h2(e[2], e[6]);
+        qf[g][j][2] = pack_h2(e[1], e[5]);
+        qf[g][j][3] = pack_h2(e[3], e[7]);
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      qsum[0][g] = __shfl_sync(0xffffffffu, sum, 8 * c) * kLog2e;
+      qsum[1][g] = __shfl_sync(0xffffffffu, sum, 8 * c + 4) * kLog2e;
+    }
+  }
+  int len[2];
+#pragma unroll
+  for (int e = 0; e < 2; e++) len[e] = 2 * c + e < it.ncols ? it.len(it.n0 + 2 * c + e, a.R) : 0;
+  float *srow[2] = {nullptr, nullptr};
+  if (a.scores)
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+      if (len[e] > 0) srow[e] = a.scores + (static_cast<int64_t>(item) * kCols + 2 * c + e) * a.score_ld;
+
+  const int tok = (gid >> 1) + 4 * (gid & 1);  // slot of score row gid in its 16 (row gid + 8: 8 further)
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float vacc[2][NG];      // sum of p (min + 7.5 scale) over this lane's slots
+  float ov[NG][VW][4][4]; // tile 2h + x of word w: dims + 4h + 2x (row gid) and + 1 (row gid + 8)
+  float wacc[NG][4];      // every row: sum of w
+#pragma unroll
+  for (int g = 0; g < NG; g++) {
+    vacc[0][g] = vacc[1][g] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; e++) wacc[g][e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < VW; w++)
+#pragma unroll
+      for (int x = 0; x < 4; x++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) ov[g][w][x][e] = 0.f;
+  }
+
+  bool ok = true;
+  for (int k = 0; k < steps; k++) {
+    const int t = t_begin + (k * kWarps + warp) * kBlock;
+    if (!mbar_wait_bounded(smem_u32(&full_bar[warp][k % ST]), (k / ST) & 1, nullptr, a.kv.err)) {
+      ok = false;  // gave up: the copies in flight land (or time out) before the stages are written again
+      for (int i = k + 1; i < min(k + ST, steps); i++)
+        mbar_wait_bounded(smem_u32(&full_bar[warp][i % ST]), (i / ST) & 1, nullptr, a.kv.err);
+      break;
+    }
+    const uint8_t *Kc = wbase + (k % ST) * S::STAGE_B, *Vc = Kc + S::CODE_B;
+    const __half *Km = reinterpret_cast<const __half *>(Kc + 2 * S::CODE_B);
+    const __half *Ks = Km + kBlock * NG, *Vm = Ks + kBlock * NG, *Vs = Vm + kBlock * NG;
+    const int ntile = t + 16 < t_end ? 2 : 1;  // (a second tile that was not copied is masked out)
+
+    // ---- scores (log2 units) of slots t + 16u + tok + 8x, columns 2c + e ----
+    float sc[2][2][2];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+#pragma unroll
+      for (int x = 0; x < 2; x++) sc[u][x][0] = sc[u][x][1] = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+        uint32_t k0[KW], k1[KW];
+        load_words<KW>(Kc + (16 * u + tok) * RB + g * (G / 2) + c * (G / 8), k0);
+        load_words<KW>(Kc + (16 * u + tok + 8) * RB + g * (G / 2) + c * (G / 8), k1);
+        float lo[4] = {0.f, 0.f, 0.f, 0.f}, hi[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < KW; j++) {
+          const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
+          mma_f16(lo, x0 & kLoNib, x1 & kLoNib, y0 & kLoNib, y1 & kLoNib, qf[g][j][0], qf[g][j][1]);
+          mma_f16(hi, x0 & kHiNib, x1 & kHiNib, y0 & kHiNib, y1 & kHiNib, qf[g][j][2], qf[g][j][3]);
+        }
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+          const float mn = __half2float(Km[(16 * u + tok + 8 * x) * NG + g]);
+          const float s24 = __half2float(Ks[(16 * u + tok + 8 * x) * NG + g]) * (kS24 * kLog2e);
+#pragma unroll
+          for (int e = 0; e < 2; e++)
+            sc[u][x][e] += mn * qsum[e][g] + s24 * (lo[2 * x + e] + hi[2 * x + e] * 0.0625f);
+        }
+      }
+    }
+    const bool edge = t + kBlock > lmin;  // warp-uniform: some live column does not see all 32 slots
+    if (edge) {
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+          for (int e = 0; e < 2; e++)
+            if (t + 16 * u + tok + 8 * x >= len[e] || u >= ntile) sc[u][x][e] = -INFINITY;
+    }
+    if (a.scores) {
+#pragma unroll
+      for (int e = 0; e < 2; e++)
+        if (srow[e])
+#pragma unroll
+          for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+              if (t + 16 * u + tok + 8 * x < len[e]) srow[e][t + 16 * u + tok + 8 * x] = sc[u][x][e];
+    }
+    // ---- running maximum: moves only when a score exceeds it by more than kSlack, so that
+    //      p = 2^(s - m) <= 2^kSlack and w = p * scale stays inside fp16 ----
+    float cmax[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      cmax[e] = fmaxf(fmaxf(sc[0][0][e], sc[0][1][e]), fmaxf(sc[1][0][e], sc[1][1][e]));
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) cmax[e] = fmaxf(cmax[e], __shfl_xor_sync(0xffffffffu, cmax[e], o));
+    }
+    if (__any_sync(0xffffffffu, cmax[0] > m[0] + kSlack || cmax[1] > m[1] + kSlack)) {
+      float al[2];
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const float mn = fmaxf(m[e], cmax[e]);
+        al[e] = mn == -INFINITY ? 1.f : fast_exp2(m[e] - mn);
+        m[e] = mn;
+        l[e] *= al[e];
+      }
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+        vacc[0][g] *= al[0];
+        vacc[1][g] *= al[1];
+#pragma unroll
+        for (int i = 0; i < 4; i++) wacc[g][i] *= al[i & 1];
+#pragma unroll
+        for (int w = 0; w < VW; w++)
+#pragma unroll
+          for (int x = 0; x < 4; x++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) ov[g][w][x][i] *= al[i & 1];
+      }
+    }
+    // ---- p, the sums, and the output product ----
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      float p[2][2];
+#pragma unroll
+      for (int x = 0; x < 2; x++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          p[x][e] = edge && sc[u][x][e] == -INFINITY ? 0.f : fast_exp2(sc[u][x][e] - m[e]);
+          l[e] += p[x][e];
+        }
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+        uint32_t b[2];
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+          const float vs = __half2float(Vs[(16 * u + tok + 8 * x) * NG + g]);
+          const float vb = __half2float(Vm[(16 * u + tok + 8 * x) * NG + g]) + 7.5f * vs;
+          float w0 = p[x][0] * vs, w1 = p[x][1] * vs, o0 = p[x][0] * vb, o1 = p[x][1] * vb;
+          if (edge) {  // masked slots may hold anything
+            if (p[x][0] == 0.f) w0 = o0 = 0.f;
+            if (p[x][1] == 0.f) w1 = o1 = 0.f;
+          }
+          vacc[0][g] += o0;
+          vacc[1][g] += o1;
+          b[x] = transpose_8x8(pack_h2(w0, w1));
+        }
+        mma_f16(wacc[g], kOnes, kOnes, kOnes, kOnes, b[0], b[1]);
+        // lane (gid, c): code words of slots c, c+4, c+8, c+12 at its dims of the group
+        uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
+        const uint8_t *vrow = Vc + (16 * u + c) * RB + g * (G / 2) + gid * (G / 16);
+        load_words<VW>(vrow, v0);
+        load_words<VW>(vrow + 4 * RB, v1);
+        load_words<VW>(vrow + 8 * RB, v2);
+        load_words<VW>(vrow + 12 * RB, v3);
+#pragma unroll
+        for (int w = 0; w < VW; w++)
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const uint32_t sel = h ? 0x7632u : 0x5410u;
+            const uint32_t P = __byte_perm(v0[w], v1[w], sel), Q = __byte_perm(v2[w], v3[w], sel);
+            const uint32_t Ps = P >> 8, Qs = Q >> 8;
+            mma_f16(ov[g][w][2 * h], P & kLoNib, P & kHiNib, Q & kLoNib, Q & kHiNib, b[0], b[1]);
+            mma_f16(ov[g][w][2 * h + 1], Ps & kLoNib, Ps & kHiNib, Qs & kLoNib, Qs & kHiNib, b[0], b[1]);
+          }
+      }
+    }
+    if (k + ST < steps) {  // every lane has used the stage; its reads come before the copy that refills it
+      fence_proxy_async_smem();
+      __syncwarp();
+      issue(k + ST);
+    }
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0) {
+    atomicOr(a.kv.err, FG_DEVERR_RANGE);
+    bad_page = 1;
+  }
+
+  // ---- this warp's columns into its (drained) stages, then the four warps' joined ----
+#pragma unroll
+  for (int e = 0; e < 2; e++) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], o);
+#pragma unroll
+    for (int g = 0; g < NG; g++)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) vacc[e][g] += __shfl_xor_sync(0xffffffffu, vacc[e][g], o);
+    if (gid == 0) {
+      red_m[warp][2 * c + e] = m[e];
+      red_l[warp][2 * c + e] = l[e];
+    }
+  }
+  float *wo = reinterpret_cast<float *>(wbase);  // [8][D]
+#pragma unroll
+  for (int g = 0; g < NG; g++)
+#pragma unroll
+    for (int w = 0; w < VW; w++)
+#pragma unroll
+      for (int x = 0; x < 4; x++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          const float base = vacc[e][g] - 7.5f * wacc[g][e];
+          *reinterpret_cast<float2 *>(wo + (2 * c + e) * D + g * G + gid * (G / 8) + w * 8 + 2 * x) =
+              make_float2(ov[g][w][x][e] * kS24 + base, ov[g][w][x][2 + e] * kS20 + base);
+        }
+  const bool all_ok = __syncthreads_and(ok) && !bad_page;
+  for (int i = tid; i < kCols * (D / 2); i += kWarps * 32) {
+    const int n = i / (D / 2), d = 2 * (i % (D / 2));
+    if (n >= it.ncols) break;
+    float M = -INFINITY, den = 0.f, o0 = 0.f, o1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) M = fmaxf(M, red_m[w][n]);
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+      const float f = red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M);
+      const float2 o = *reinterpret_cast<const float2 *>(smem + w * S::WARP_B + (n * D + d) * 4);
+      den += f * red_l[w][n];
+      if (f != 0.f) {  // (a warp without slots has nothing written that counts)
+        o0 += f * o.x;
+        o1 += f * o.y;
+      }
+    }
+    const int64_t pi = (static_cast<int64_t>(item) * a.nsplit + sp) * kCols + n;
+    if (a.ml && d == 0) a.ml[pi] = make_float2(M, all_ok ? den : -1.f);
+    if (a.nsplit > 1) {
+      *reinterpret_cast<float2 *>(a.po + pi * D + d) = make_float2(o0, o1);
+    } else {
+      const int cn = it.n0 + n;
+      const bool on = it.len(cn, a.R) > 0 && all_ok;
+      const float inv = 1.0f / den;
+      __half2 *dst = reinterpret_cast<__half2 *>(
+          a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
+          (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + d);
+      *dst = on ? __floats2half2_rn(o0 * inv, o1 * inv) : __floats2half2_rn(0.f, 0.f);
+    }
+  }
+}
+
+// Column n of an item over its splits: maximum and sum; sum 0: nothing seen, or a bad page.
+__device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, const float2 *ml, int n, int used) {
+  float M = -INFINITY, den = 0.f;
+  bool bad = false;
+  for (int j = 0; j < used; j++) {
+    const float2 v = ml[j * kCols + n];
+    bad |= v.y < 0.f;
+    M = fmaxf(M, v.x);
+  }
+  for (int j = 0; j < used; j++) {
+    const float2 v = ml[j * kCols + n];
+    den += v.x == -INFINITY ? 0.f : exp2f(v.x - M) * v.y;
+  }
+  return make_float2(M, bad ? 0.f : den);
+}
+
+constexpr int kJoinThreads = 128;
+
+// blockIdx.x: item; blockIdx.y < out_cols: that column's splits joined into its output row; beyond:
+// a block of kJoinThreads * 4 slots whose weights grow by the columns' probabilities.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnArgs a, int out_cols) {
+  __shared__ float2 col[kCols];
+  const int item = blockIdx.x, tid = threadIdx.x;
+  const Item it = load_item(a, item, false);
+  int lmax = 0;
+  const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
+  if (last >= it.n0) lmax = it.len(last, a.R);
+  const int used = (lmax + a.split - 1) / a.split;
+  const float2 *ml = a.ml + static_cast<int64_t>(item) * a.nsplit * kCols;
+  if (static_cast<int>(blockIdx.y) < out_cols) {
+    const int n = blockIdx.y;
+    if (n >= it.ncols) return;
+    const int cn = it.n0 + n;
+    const float2 t = it.len(cn, a.R) > 0 ? join_ml(a, ml, n, used) : make_float2(0.f, 0.f);
+    __half *dst = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
+                  (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D;
+    const float *po = a.po + static_cast<int64_t>(item) * a.nsplit * kCols * D + n * D;
+    for (int d = tid; d < D; d += kJoinThreads) {
+      float o = 0.f;
+      if (t.y != 0.f)
+        for (int j = 0; j < used; j++) {
+          const float f = exp2f(ml[j * kCols + n].x - t.x);
+          if (f != 0.f) o += f * po[static_cast<int64_t>(j) * kCols * D + d];
+        }
+      dst[d] = __float2half_rn(t.y != 0.f ? o / t.y : 0.f);
+    }
+    return;
+  }
+  const int t0 = (blockIdx.y - out_cols) * kJoinThreads * 4;
+  if (t0 >= lmax) return;
+  if (tid < kCols) col[tid] = tid < it.ncols && it.len(it.n0 + tid, a.R) > 0 ? join_ml(a, ml, tid, used) : make_float2(0.f, 0.f);
+  __syncthreads();
+  const float *sc = a.scores + static_cast<int64_t>(item) * kCols * a.score_ld;
+  for (int e = 0; e < 4; e++) {
+    const int t = t0 + e * kJoinThreads + tid;
+    if (t >= lmax) break;
+    float add = 0.f;
+    for (int n = 0; n < it.ncols; n++)
+      if (col[n].y != 0.f && t < it.len(it.n0 + n, a.R)) add += exp2f(sc[n * a.score_ld + t] - col[n].x) / col[n].y;
+    const int64_t slot = paged_slot(a.kv, it.s, it.h, t);
+    if (slot >= 0) a.kv.weights[slot] += add;
+  }
+}
+
+struct Plan {
+  int tiles, split, nsplit;
+  size_t ml, po, scores, total;  // bytes, each part 256-byte aligned
+  int64_t score_ld;
+};
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+void plan_bytes(Plan *p, int64_t pairs, int D, int limit, bool accumulate) {
+  // accumulating launches take the column tiles one after the other, so that a slot's weight is
+  // grown by one CTA at a time and in a fixed order
+  const int64_t items = pairs * (accumulate ? 1 : p->tiles);
+  const bool parts = p->nsplit > 1;
+  p->score_ld = (static_cast<int64_t>(limit) + 31) / 32 * 32;
+  p->ml = parts || accumulate ? align256(static_cast<size_t>(items) * p->nsplit * kCols * sizeof(float2)) : 0;
+  p->po = parts ? align256(static_cast<size_t>(items) * p->nsplit * kCols * D * sizeof(float)) : 0;
+  p->scores = accumulate ? align256(static_cast<size_t>(items) * kCols * p->score_ld * sizeof(float)) : 0;
+  p->total = p->ml + p->po + p->scores;
+}
+
+// Splits so that the launch is about four waves of resident CTAs, of at least 512 slots each.
+Plan make_plan(int64_t pairs, int cols, int D, int limit, bool accumulate) {
+  Plan p;
+  p.tiles = (cols + kCols - 1) / kCols;
+  const int64_t items = pairs * (accumulate ? 1 : p.tiles), room = 4LL * 3 * fg_sm_count();
+  int64_t c = (items * limit + room - 1) / room;
+  c = c < 512 ? 512 : c;
+  c = (c + kCta - 1) / kCta * kCta;
+  const int64_t most = (static_cast<int64_t>(limit) + kCta - 1) / kCta * kCta;
+  p.split = static_cast<int>(c < most ? c : most);
+  p.nsplit = (limit + p.split - 1) / p.split;
+  plan_bytes(&p, pairs, D, limit, accumulate);
+  return p;
+}
+
+int plan_limit(const fg_paged_kv *kv, int max_len) {
+  const int cap = fg_paged_capacity(kv);
+  return max_len && max_len < cap ? max_len : cap;
+}
+
+template <int D, int G>
+fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int limit, bool accumulate, cudaStream_t st) {
+  using S = Shape<D, G>;
+  static bool attr_set[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+    const fg_status rc = fg_cuda_check(
+        cudaFuncSetAttribute(paged_attn_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM));
+    if (rc != FG_OK) return rc;
+    attr_set[dev] = true;
+  }
+  const int rounds = accumulate ? p.tiles : 1;
+  a.tiles = accumulate ? 1 : p.tiles;
+  const int64_t items = pairs * a.tiles;
+  if (items * p.nsplit > INT32_MAX) return FG_ERR_SHAPE;
+  for (int r = 0; r < rounds; r++) {
+    a.tile0 = r;
+    paged_attn_kernel<D, G><<<static_cast<unsigned>(items * p.nsplit), kWarps * 32, S::SMEM, st>>>(a);
+    fg_status rc = fg_launch_check();
+    if (rc != FG_OK) return rc;
+    if (p.nsplit == 1 && !accumulate) continue;
+    const int left = cols - r * kCols, out_cols = p.nsplit == 1 ? 0 : left < kCols ? left : kCols;
+    const int blocks = accumulate ? (limit + 4 * kJoinThreads - 1) / (4 * kJoinThreads) : 0;
+    if (out_cols + blocks > 65535) return FG_ERR_SHAPE;
+    paged_join_kernel<D><<<dim3(static_cast<unsigned>(items), out_cols + blocks), kJoinThreads, 0, st>>>(a, out_cols);
+    if ((rc = fg_launch_check()) != FG_OK) return rc;
+  }
+  return FG_OK;
 }
 
 }  // namespace
 
 extern "C" size_t fg_paged_attention_workspace_bytes(const fg_paged_kv *kv, int num_q_heads, int rows, int rows_per_seq,
                                                      int max_len, int accumulate) {
-  return 0;
+  if (fg_paged_validate(kv) != FG_OK || rows <= 0 || rows_per_seq < 1 || num_q_heads < 1 || num_q_heads % kv->num_heads ||
+      max_len < 0)
+    return 0;
+  const int64_t cols = static_cast<int64_t>(num_q_heads / kv->num_heads) * rows_per_seq;
+  if (cols > INT32_MAX) return 0;
+  return make_plan(static_cast<int64_t>(rows / rows_per_seq) * kv->num_heads, static_cast<int>(cols), kv->head_dim,
+                   plan_limit(kv, max_len), accumulate != 0).total;
 }
 
 extern "C" fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q, int64_t ldq, int num_q_heads,
@@ -146,8 +653,19 @@ extern "C" fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q,
     return FG_ERR_INVALID;
   const int64_t hD = static_cast<int64_t>(num_q_heads) * kv->head_dim;
   if (ldq < hD || ldo < hD || ldq % 8 || ldo % 8) return FG_ERR_SHAPE;
-  const int seqs = rows / rows_per_seq;
-  if (static_cast<int64_t>(seqs) * kv->num_heads > INT32_MAX) return FG_ERR_SHAPE;
+  const int64_t pairs = static_cast<int64_t>(rows / rows_per_seq) * kv->num_heads;
+  const int64_t cols = static_cast<int64_t>(num_q_heads / kv->num_heads) * rows_per_seq;
+  if (pairs > INT32_MAX || cols > INT32_MAX) return FG_ERR_SHAPE;
+  const int limit = plan_limit(kv, max_len);
+  Plan p = make_plan(pairs, static_cast<int>(cols), kv->head_dim, limit, accumulate != 0);
+  const size_t have = workspace ? workspace_bytes : 0;
+  while (p.total > have && !accumulate && p.nsplit > 1) {  // less scratch: fewer, longer splits
+    p.nsplit = (p.nsplit + 1) / 2;
+    p.split = ((limit + p.nsplit - 1) / p.nsplit + kCta - 1) / kCta * kCta;
+    p.nsplit = (limit + p.split - 1) / p.split;
+    plan_bytes(&p, pairs, kv->head_dim, limit, false);
+  }
+  if (p.total > have) return FG_ERR_WORKSPACE;
   PagedAttnArgs a;
   if (!fg_paged_args(kv, &a.kv)) return FG_ERR_CUDA;
   a.q = reinterpret_cast<const __half *>(q);
@@ -156,22 +674,30 @@ extern "C" fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q,
   a.ldo = ldo;
   a.R = num_q_heads / kv->num_heads;
   a.rows_per_seq = rows_per_seq;
-  a.limit = fg_paged_capacity(kv);
-  if (max_len && max_len < a.limit) a.limit = max_len;
-  a.accumulate = accumulate;
+  a.limit = limit;
+  a.split = p.split;
+  a.nsplit = p.nsplit;
   a.positions = positions;
   a.counts = row_counts;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.ml = p.ml ? reinterpret_cast<float2 *>(ws) : nullptr;
+  a.po = p.po ? reinterpret_cast<float *>(ws + p.ml) : nullptr;
+  a.scores = p.scores ? reinterpret_cast<float *>(ws + p.ml + p.po) : nullptr;
+  a.score_ld = p.score_ld;
+  a.tile0 = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int n = static_cast<int>(cols);
+  const bool acc = accumulate != 0;
   if (fg_kv_group(kv->group) == 64) {
     switch (kv->head_dim) {
-      case 64: return launch<64, 64>(a, seqs, st);
-      case 128: return launch<128, 64>(a, seqs, st);
-      case 256: return launch<256, 64>(a, seqs, st);
+      case 64: return launch<64, 64>(a, p, pairs, n, limit, acc, st);
+      case 128: return launch<128, 64>(a, p, pairs, n, limit, acc, st);
+      case 256: return launch<256, 64>(a, p, pairs, n, limit, acc, st);
     }
   } else {
     switch (kv->head_dim) {
-      case 128: return launch<128, 128>(a, seqs, st);
-      case 256: return launch<256, 128>(a, seqs, st);
+      case 128: return launch<128, 128>(a, p, pairs, n, limit, acc, st);
+      case 256: return launch<256, 128>(a, p, pairs, n, limit, acc, st);
     }
   }
   return FG_ERR_UNSUPPORTED;
