@@ -38,6 +38,10 @@ constexpr int kWarps = 4;
 constexpr int kBlock = 32;              // slots per warp step
 constexpr int kCta = kWarps * kBlock;   // slots per CTA step
 constexpr int kCols = 8;                // columns per tile
+#ifndef FG_ONE_STAGES
+#define FG_ONE_STAGES 3
+#define FG_ONE_CTAS 4
+#endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 2.0f;
 constexpr uint32_t kLoNib = 0x000F000Fu;  // bits 0-3 of both halves: c * 2^-24
@@ -53,10 +57,13 @@ struct PagedAttnArgs {
   int R, rows_per_seq, limit;
   int tile0, tiles;    // column tiles of this launch: tile0 .. tile0 + tiles - 1
   int split, nsplit;   // slots per split (a multiple of kCta), splits
+  int pcols;           // columns per item in ml, po and scores: 1 (single-column launches) or 8
+  int items;
+  bool shared_unit;    // the CTA's warps share a unit (one split of one item), or have one each
   const int32_t *positions, *counts;
-  float2 *ml;          // [items][nsplit][8]: running maximum (log2 units) and sum; sum < 0: a bad page
-  float *po;           // [items][nsplit][8][D] unnormalised outputs (nsplit > 1)
-  float *scores;       // [items][8][score_ld] (accumulate)
+  float2 *ml;          // [items][nsplit][pcols]: running maximum (log2 units) and sum; sum < 0: a bad page
+  float *po;           // [items][nsplit][pcols][D] unnormalised outputs (nsplit > 1)
+  float *scores;       // [items][pcols][score_ld] (accumulate)
   int64_t score_ld;
 };
 
@@ -489,17 +496,372 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G>::kCtas) paged_attn_ke
   }
 }
 
+// ------------------------------------------------------------------------------------------------
+// One column (one new token, a key-value head of its own): the tile's eight columns hold what one
+// column has to offer instead.
+//   scores: column 2c of q is zero outside group c % 2, so that lane (gid, c) finds the dot product
+//           of slot gid + 8 (c / 2) with group c % 2 in its own fragment; the two lanes of a slot
+//           add their groups' shares.
+//   output: lane (gid, c) holds w of that slot and group as two fp16 numbers, w's rounding and the
+//           rest (22 bits together), in columns 2c and 2c+1 of a matrix whose transpose is the B
+//           operand: columns 0-3 for slots 0-7 of the 16, columns 4-7 for slots 8-15.
+// A = V codes transposed comes from ldmatrix.trans on 16-bit elements (4 codes of a slot): a lane
+// gets two slots' codes of dims 4 gid .. 4 gid + 3, in operand order.
+// Units: with many items a warp takes a whole split of one item and no two warps ever meet;
+// otherwise the CTA's four warps share a unit, 32-slot blocks in turn, and join at the end.
+// ------------------------------------------------------------------------------------------------
+template <int D, int G>
+struct One {
+  static constexpr int NG = D / G;  // 1 or 2
+  static constexpr int RB = D / 2;
+  static constexpr int KW = D / 32;  // K code words per lane and slot
+  static constexpr int CH = D / 32;  // 32-dim chunks (16 bytes of codes)
+  static constexpr int CODE_B = kBlock * RB, META_B = kBlock * NG * 2;
+  static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? FG_ONE_STAGES : 2;
+  static constexpr int WARP_B = kStages * STAGE_B;  // >= D * 4, the warp's outputs at the end
+  static constexpr int SMEM = kWarps * WARP_B;
+  static constexpr int kCtas = D <= 128 ? FG_ONE_CTAS : 3;
+};
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_kernel(const PagedAttnArgs a) {
+  using S = One<D, G>;
+  constexpr int NG = S::NG, RB = S::RB, KW = S::KW, CH = S::CH, ST = S::kStages;
+  constexpr float kS24 = 16777216.0f, kS20 = 1048576.0f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full_bar[kWarps][ST];
+  __shared__ float red_m[kWarps], red_l[kWarps];
+  __shared__ int bad_page;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, c = lane & 3;
+  const int64_t unit = a.shared_unit ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  if (!a.shared_unit && unit >= static_cast<int64_t>(a.items) * a.nsplit) return;
+  const int item = static_cast<int>(unit / a.nsplit), sp = static_cast<int>(unit % a.nsplit);
+  const int first = a.shared_unit ? warp : 0, stride = a.shared_unit ? kWarps : 1;  // this warp's blocks
+  const int s = item / a.kv.H, h = item % a.kv.H;
+  const int pos = a.positions[s], count = a.counts ? a.counts[s] : 1;
+  const bool range = pos < -1 || count < 0 || count > 1 || (pos >= 0 && static_cast<int64_t>(pos) + count > a.limit);
+  if (range && sp == 0 && first == 0 && lane == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
+  const int len = range || pos < 0 || count < 1 ? 0 : pos + 1;
+  const int t_begin = sp * a.split, t_end = min(len, t_begin + a.split);
+  if (t_begin >= t_end && (sp > 0 || a.nsplit > 1)) return;  // (the join zeroes rows that see nothing)
+  const int nblk = t_end > t_begin ? (t_end - t_begin + kBlock - 1) / kBlock : 0;
+  const int steps = nblk > first ? (nblk - first + stride - 1) / stride : 0;
+
+  if (lane == 0) {
+    for (int i = 0; i < ST; i++) mbar_init(smem_u32(&full_bar[warp][i]), 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (a.shared_unit) {
+    if (tid == 0) bad_page = 0;
+    __syncthreads();
+  } else {
+    __syncwarp();
+  }
+
+  uint8_t *const wbase = smem + warp * S::WARP_B;
+  int64_t slot_a = 0, slot_b = 0;  // pool slots of the two halves of block `lane` of the current 32 steps
+  bool bad = false;
+  auto issue = [&](int k) {
+    const int t = t_begin + (k * stride + first) * kBlock;
+    if ((k & 31) == 0) {
+      const int tl = t + lane * stride * kBlock;
+      slot_a = tl < t_end ? paged_slot(a.kv, s, h, tl) : 0;
+      slot_b = tl + 16 < t_end ? paged_slot(a.kv, s, h, tl + 16) : 0;
+      if (slot_a < 0 || slot_b < 0) bad = true;  // flagged at the end; the pool's first slots instead
+      slot_a = slot_a < 0 ? 0 : slot_a;
+      slot_b = slot_b < 0 ? 0 : slot_b;
+    }
+    const int64_t sa = __shfl_sync(0xffffffffu, slot_a, k & 31), sb = __shfl_sync(0xffffffffu, slot_b, k & 31);
+    const bool second = t + 16 < t_end, joined = second && sb == sa + 16;
+    const uint32_t bar = smem_u32(&full_bar[warp][k % ST]);
+    if (lane == 0) mbar_arrive_expect_tx(bar, (second ? 32 : 16) * (2 * RB + 8 * NG));
+    __syncwarp();
+    const int arr = lane & 7, run = lane >> 3;
+    if (arr < 6 && (run == 0 || (run == 1 && second && !joined))) {
+      const bool codes = arr < 2;
+      const int per = codes ? RB : NG * 2;
+      const uint8_t *pool = arr == 0   ? a.kv.kc
+                            : arr == 1 ? a.kv.vc
+                            : arr == 2 ? reinterpret_cast<const uint8_t *>(a.kv.km)
+                            : arr == 3 ? reinterpret_cast<const uint8_t *>(a.kv.ks)
+                            : arr == 4 ? reinterpret_cast<const uint8_t *>(a.kv.vm)
+                                       : reinterpret_cast<const uint8_t *>(a.kv.vs);
+      const int off = (k % ST) * S::STAGE_B + (codes ? arr * S::CODE_B : 2 * S::CODE_B + (arr - 2) * S::META_B);
+      bulk_g2s(smem_u32(wbase + off + run * 16 * per), pool + (run ? sb : sa) * per, (joined ? 32 : 16) * per, bar);
+    }
+  };
+  for (int k = 0; k < min(ST, steps); k++) issue(k);
+
+  // ---- q as the B operand; word j of lane class c: dims 2o .. 2o+7 ----
+  const __half *qrow = a.q + static_cast<int64_t>(s) * a.ldq + static_cast<int64_t>(h) * D;
+  uint32_t qf[KW][4];
+  float ql;  // sum of q over this lane's group, times log2(e)
+  const int g = NG == 2 ? c & 1 : 0;
+  {
+    float part[NG];
+#pragma unroll
+    for (int i = 0; i < NG; i++) part[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < KW; j++) {
+      const int o = D == 64 ? 8 * c + 4 * j : 64 * (j >> 2) + 16 * c + 4 * (j & 3);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (len > 0) v = *reinterpret_cast<const uint4 *>(qrow + 2 * o);
+      const __half *e = reinterpret_cast<const __half *>(&v);
+      const int og = o / (G / 2);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
+#pragma unroll
+      for (int i = 0; i < NG; i++) part[i] += og == i ? sum : 0.f;
+      const bool on = !(gid & 1) && (NG == 1 || og == ((gid >> 1) & 1));
+      qf[j][0] = on ? pack_h2(e[0], e[4]) : 0u;
+      qf[j][1] = on ? pack_h2(e[2], e[6]) : 0u;
+      qf[j][2] = on ? pack_h2(e[1], e[5]) : 0u;
+      qf[j][3] = on ? pack_h2(e[3], e[7]) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < NG; i++) {
+      part[i] += __shfl_xor_sync(0xffffffffu, part[i], 1);
+      part[i] += __shfl_xor_sync(0xffffffffu, part[i], 2);
+    }
+    ql = (NG == 2 && g ? part[NG - 1] : part[0]) * kLog2e;
+  }
+  const bool upper = c & 2;               // this lane's slot is gid + 8 of the 16
+  const int tq = gid + (upper ? 8 : 0);
+  float *const srow = a.scores ? a.scores + static_cast<int64_t>(item) * a.score_ld : nullptr;
+  const uint32_t vaddr = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
+
+  float m = -INFINITY, l = 0.f, vacc = 0.f;
+  float ov[CH][2][4];
+#pragma unroll
+  for (int i = 0; i < CH; i++)
+#pragma unroll
+    for (int x = 0; x < 2; x++) ov[i][x][0] = ov[i][x][1] = ov[i][x][2] = ov[i][x][3] = 0.f;
+
+  bool ok = true;
+  for (int k = 0; k < steps; k++) {
+    const int st = k % ST, t = t_begin + (k * stride + first) * kBlock;
+    if (!mbar_wait_bounded(smem_u32(&full_bar[warp][st]), (k / ST) & 1, nullptr, a.kv.err)) {
+      ok = false;  // gave up: the copies in flight land (or time out) before the stages are written again
+      for (int i = k + 1; i < min(k + ST, steps); i++)
+        mbar_wait_bounded(smem_u32(&full_bar[warp][i % ST]), (i / ST) & 1, nullptr, a.kv.err);
+      break;
+    }
+    const uint8_t *Kc = wbase + st * S::STAGE_B;
+    const __half *Km = reinterpret_cast<const __half *>(Kc + 2 * S::CODE_B);
+    const __half *Ks = Km + kBlock * NG, *Vm = Ks + kBlock * NG, *Vs = Vm + kBlock * NG;
+
+    // ---- scores (log2 units) of slots t + 16u + tq ----
+    float sc[2];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      uint32_t k0[KW], k1[KW];
+#pragma unroll
+      for (int j = 0; j < KW; j += (D == 64 ? 2 : 4)) {
+        const uint8_t *p = Kc + (16 * u + gid) * RB + (D == 64 ? 8 * c : 16 * j + 16 * c);
+        if constexpr (D == 64) {
+          const uint2 x = *reinterpret_cast<const uint2 *>(p), y = *reinterpret_cast<const uint2 *>(p + 8 * RB);
+          k0[j] = x.x, k0[j + 1] = x.y, k1[j] = y.x, k1[j + 1] = y.y;
+        } else {
+          const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + 8 * RB);
+          k0[j] = x.x, k0[j + 1] = x.y, k0[j + 2] = x.z, k0[j + 3] = x.w;
+          k1[j] = y.x, k1[j + 1] = y.y, k1[j + 2] = y.z, k1[j + 3] = y.w;
+        }
+      }
+      float lo[4] = {0.f, 0.f, 0.f, 0.f}, hi[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < KW; j++) {
+        const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
+        mma_f16(lo, x0 & kLoNib, x1 & kLoNib, y0 & kLoNib, y1 & kLoNib, qf[j][0], qf[j][1]);
+        mma_f16(hi, x0 & kHiNib, x1 & kHiNib, y0 & kHiNib, y1 & kHiNib, qf[j][2], qf[j][3]);
+      }
+      const float dot = (upper ? lo[2] : lo[0]) + (upper ? hi[2] : hi[0]) * 0.0625f;
+      const int i = (16 * u + tq) * NG + g;
+      float part = __half2float(Km[i]) * ql + __half2float(Ks[i]) * (kS24 * kLog2e) * dot;
+      if constexpr (NG == 2) part += __shfl_xor_sync(0xffffffffu, part, 1);
+      sc[u] = part;
+    }
+    const bool edge = t + kBlock > t_end;  // warp-uniform
+    if (edge) {
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+        if (t + 16 * u + tq >= t_end) sc[u] = -INFINITY;
+    }
+    if (srow && !(c & 1)) {
+#pragma unroll
+      for (int u = 0; u < 2; u++)
+        if (t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u];
+    }
+    float cmax = fmaxf(sc[0], sc[1]);
+#pragma unroll
+    for (int o = 2; o < 32; o <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
+    if (cmax > m + kSlack) {  // the running maximum moves (warp-uniform)
+      const float al = fast_exp2(m - cmax);
+      m = cmax;
+      l *= al;
+      vacc *= al;
+#pragma unroll
+      for (int i = 0; i < CH; i++)
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) ov[i][x][e] *= al;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      const int i = (16 * u + tq) * NG + g;
+      const float p = fast_exp2(sc[u] - m);
+      float w = p * __half2float(Vs[i]), pm = p * __half2float(Vm[i]);
+      if (edge && t + 16 * u + tq >= t_end) w = pm = 0.f;  // masked slots may hold anything (their p is 0)
+      l += p;
+      vacc += pm;
+      // w rounded, and the rest, in columns 2c and 2c+1 of the slot's row
+      const __half wh = __float2half_rn(w);
+      uint32_t wp = pack_h2(wh, __float2half_rn(w - __half2float(wh)));
+      if (NG == 1 && (c & 1)) wp = 0u;
+      const uint32_t wt = transpose_8x8(wp);
+      const uint32_t b0 = gid < 4 ? wt : 0u, b1 = gid < 4 ? 0u : wt;
+#pragma unroll
+      for (int ch = 0; ch < CH; ch += 2) {
+        uint32_t r[4];  // slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
+        ldmatrix_x4_trans(r, vaddr + st * S::STAGE_B + 16 * u * RB + ch * 16);
+#pragma unroll
+        for (int y = 0; y < 2; y++) {
+          const uint32_t P = r[2 * y], Q = r[2 * y + 1], Ps = P >> 8, Qs = Q >> 8;
+          mma_f16(ov[ch + y][0], P & kLoNib, P & kHiNib, Q & kLoNib, Q & kHiNib, b0, b1);
+          mma_f16(ov[ch + y][1], Ps & kLoNib, Ps & kHiNib, Qs & kLoNib, Qs & kHiNib, b0, b1);
+        }
+      }
+    }
+    if (k + ST < steps) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      issue(k + ST);
+    }
+  }
+  const bool any_bad = __any_sync(0xffffffffu, bad);
+  if (any_bad && lane == 0) {
+    atomicOr(a.kv.err, FG_DEVERR_RANGE);
+    if (a.shared_unit) bad_page = 1;
+  }
+
+  // ---- totals of the warp: every slot was counted by two lanes; group i's min sum in lane i ----
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  l *= 0.5f;
+#pragma unroll
+  for (int o = 2; o < 32; o <<= 1) vacc += __shfl_xor_sync(0xffffffffu, vacc, o);
+  float o4[CH / NG][4];  // lanes c = group: dims 4 gid .. 4 gid + 3 of its chunks
+#pragma unroll
+  for (int i = 0; i < CH; i++) {
+    const int cg = i / (CH / NG);
+    float v[4];
+#pragma unroll
+    for (int x = 0; x < 2; x++) {
+      v[2 * x] = (ov[i][x][0] + ov[i][x][1]) * kS24;
+      v[2 * x + 1] = (ov[i][x][2] + ov[i][x][3]) * kS20;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; x++) {
+      v[x] += __shfl_xor_sync(0xffffffffu, v[x], 2);
+      if (NG == 1 || c == cg) o4[i % (CH / NG)][x] = v[x] + vacc;
+    }
+  }
+  const int64_t pi = static_cast<int64_t>(item) * a.nsplit + sp;
+  __half *const orow = a.out + static_cast<int64_t>(s) * a.ldo + static_cast<int64_t>(h) * D;
+  if (!a.shared_unit) {
+    const bool good = ok && !any_bad;
+    if (a.ml && lane == 0) a.ml[pi] = make_float2(m, good ? l : -1.f);
+    const float inv = 1.0f / l;
+    const bool on = len > 0 && good;
+    if (c < NG) {
+#pragma unroll
+      for (int i = 0; i < CH / NG; i++) {
+        const int d = (c * (CH / NG) + i) * 32 + 4 * gid;
+        if (a.nsplit > 1) {
+          *reinterpret_cast<float4 *>(a.po + pi * D + d) = make_float4(o4[i][0], o4[i][1], o4[i][2], o4[i][3]);
+        } else {
+          uint2 r = make_uint2(0u, 0u);
+          if (on) r = make_uint2(pack_h2(o4[i][0] * inv, o4[i][1] * inv), pack_h2(o4[i][2] * inv, o4[i][3] * inv));
+          *reinterpret_cast<uint2 *>(orow + d) = r;
+        }
+      }
+    }
+    if (srow && a.nsplit == 1 && on) {  // this warp saw the whole row: its slots' weights
+      __syncwarp();
+      for (int t = lane; t < t_end; t += 32) {
+        const int64_t slot = paged_slot(a.kv, s, h, t);
+        a.kv.weights[slot] += fast_exp2(srow[t] - m) * inv;
+      }
+    }
+    return;
+  }
+  float *wo = reinterpret_cast<float *>(wbase);
+  if (c < NG)
+#pragma unroll
+    for (int i = 0; i < CH / NG; i++)
+      *reinterpret_cast<float4 *>(wo + (c * (CH / NG) + i) * 32 + 4 * gid) =
+          make_float4(o4[i][0], o4[i][1], o4[i][2], o4[i][3]);
+  if (lane == 0) {
+    red_m[warp] = m;
+    red_l[warp] = l;
+  }
+  const bool good = __syncthreads_and(ok) && !bad_page;
+  float M = -INFINITY, den = 0.f, f[kWarps];
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) M = fmaxf(M, red_m[w]);
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    f[w] = red_m[w] == -INFINITY ? 0.f : exp2f(red_m[w] - M);
+    den += f[w] * red_l[w];
+  }
+  const float inv = 1.0f / den;
+  const bool on = len > 0 && good;
+  if (a.ml && tid == 0) a.ml[pi] = make_float2(M, good ? den : -1.f);
+  for (int d = 2 * tid; d < D; d += 2 * kWarps * 32) {
+    float o0 = 0.f, o1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++)
+      if (f[w] != 0.f) {
+        const float2 v = *reinterpret_cast<const float2 *>(smem + w * S::WARP_B + d * 4);
+        o0 += f[w] * v.x;
+        o1 += f[w] * v.y;
+      }
+    if (a.nsplit > 1) {
+      *reinterpret_cast<float2 *>(a.po + pi * D + d) = make_float2(o0, o1);
+    } else {
+      *reinterpret_cast<__half2 *>(orow + d) = on ? __floats2half2_rn(o0 * inv, o1 * inv) : __floats2half2_rn(0.f, 0.f);
+    }
+  }
+  if (srow && a.nsplit == 1 && on)  // (the CTA's scores were published by the barrier above)
+    for (int t = tid; t < t_end; t += kWarps * 32) {
+      const int64_t slot = paged_slot(a.kv, s, h, t);
+      a.kv.weights[slot] += fast_exp2(srow[t] - M) * inv;
+    }
+}
+
 // Column n of an item over its splits: maximum and sum; sum 0: nothing seen, or a bad page.
 __device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, const float2 *ml, int n, int used) {
   float M = -INFINITY, den = 0.f;
   bool bad = false;
   for (int j = 0; j < used; j++) {
-    const float2 v = ml[j * kCols + n];
+    const float2 v = ml[j * a.pcols + n];
     bad |= v.y < 0.f;
     M = fmaxf(M, v.x);
   }
   for (int j = 0; j < used; j++) {
-    const float2 v = ml[j * kCols + n];
+    const float2 v = ml[j * a.pcols + n];
     den += v.x == -INFINITY ? 0.f : exp2f(v.x - M) * v.y;
   }
   return make_float2(M, bad ? 0.f : den);
@@ -518,7 +880,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
   const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
   if (last >= it.n0) lmax = it.len(last, a.R);
   const int used = (lmax + a.split - 1) / a.split;
-  const float2 *ml = a.ml + static_cast<int64_t>(item) * a.nsplit * kCols;
+  const float2 *ml = a.ml + static_cast<int64_t>(item) * a.nsplit * a.pcols;
   if (static_cast<int>(blockIdx.y) < out_cols) {
     const int n = blockIdx.y;
     if (n >= it.ncols) return;
@@ -526,13 +888,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
     const float2 t = it.len(cn, a.R) > 0 ? join_ml(a, ml, n, used) : make_float2(0.f, 0.f);
     __half *dst = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
                   (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D;
-    const float *po = a.po + static_cast<int64_t>(item) * a.nsplit * kCols * D + n * D;
+    const float *po = a.po + static_cast<int64_t>(item) * a.nsplit * a.pcols * D + n * D;
     for (int d = tid; d < D; d += kJoinThreads) {
       float o = 0.f;
       if (t.y != 0.f)
         for (int j = 0; j < used; j++) {
-          const float f = exp2f(ml[j * kCols + n].x - t.x);
-          if (f != 0.f) o += f * po[static_cast<int64_t>(j) * kCols * D + d];
+          const float f = exp2f(ml[j * a.pcols + n].x - t.x);
+          if (f != 0.f) o += f * po[static_cast<int64_t>(j) * a.pcols * D + d];
         }
       dst[d] = __float2half_rn(t.y != 0.f ? o / t.y : 0.f);
     }
@@ -542,7 +904,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
   if (t0 >= lmax) return;
   if (tid < kCols) col[tid] = tid < it.ncols && it.len(it.n0 + tid, a.R) > 0 ? join_ml(a, ml, tid, used) : make_float2(0.f, 0.f);
   __syncthreads();
-  const float *sc = a.scores + static_cast<int64_t>(item) * kCols * a.score_ld;
+  const float *sc = a.scores + static_cast<int64_t>(item) * a.pcols * a.score_ld;
   for (int e = 0; e < 4; e++) {
     const int t = t0 + e * kJoinThreads + tid;
     if (t >= lmax) break;
@@ -555,7 +917,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAtt
 }
 
 struct Plan {
-  int tiles, split, nsplit;
+  int tiles, split, nsplit, pcols;
+  bool one, shared_unit;
   size_t ml, po, scores, total;  // bytes, each part 256-byte aligned
   int64_t score_ld;
 };
@@ -568,17 +931,23 @@ void plan_bytes(Plan *p, int64_t pairs, int D, int limit, bool accumulate) {
   const int64_t items = pairs * (accumulate ? 1 : p->tiles);
   const bool parts = p->nsplit > 1;
   p->score_ld = (static_cast<int64_t>(limit) + 31) / 32 * 32;
-  p->ml = parts || accumulate ? align256(static_cast<size_t>(items) * p->nsplit * kCols * sizeof(float2)) : 0;
-  p->po = parts ? align256(static_cast<size_t>(items) * p->nsplit * kCols * D * sizeof(float)) : 0;
-  p->scores = accumulate ? align256(static_cast<size_t>(items) * kCols * p->score_ld * sizeof(float)) : 0;
+  p->ml = parts || (accumulate && !p->one)
+              ? align256(static_cast<size_t>(items) * p->nsplit * p->pcols * sizeof(float2)) : 0;
+  p->po = parts ? align256(static_cast<size_t>(items) * p->nsplit * p->pcols * D * sizeof(float)) : 0;
+  p->scores = accumulate ? align256(static_cast<size_t>(items) * p->pcols * p->score_ld * sizeof(float)) : 0;
   p->total = p->ml + p->po + p->scores;
 }
 
 // Splits so that the launch is about four waves of resident CTAs, of at least 512 slots each.
-Plan make_plan(int64_t pairs, int cols, int D, int limit, bool accumulate) {
+// Single-column launches of more than four waves of warps give every warp an item of its own.
+Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate) {
   Plan p;
+  p.one = cols == 1 && D / G <= 2;
+  p.pcols = p.one ? 1 : kCols;
   p.tiles = (cols + kCols - 1) / kCols;
-  const int64_t items = pairs * (accumulate ? 1 : p.tiles), room = 4LL * 3 * fg_sm_count();
+  const int per_sm = p.one && D <= 128 ? FG_ONE_CTAS : 3;
+  const int64_t items = pairs * (accumulate ? 1 : p.tiles), room = 4LL * per_sm * fg_sm_count();
+  p.shared_unit = !p.one || pairs < room * kWarps;
   int64_t c = (items * limit + room - 1) / room;
   c = c < 512 ? 512 : c;
   c = (c + kCta - 1) / kCta * kCta;
@@ -594,30 +963,46 @@ int plan_limit(const fg_paged_kv *kv, int max_len) {
   return max_len && max_len < cap ? max_len : cap;
 }
 
-template <int D, int G>
-fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int limit, bool accumulate, cudaStream_t st) {
-  using S = Shape<D, G>;
-  static bool attr_set[64] = {false};
+template <typename K>
+fg_status set_smem(K kernel, int bytes, bool (&done)[64]) {
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-    const fg_status rc = fg_cuda_check(
-        cudaFuncSetAttribute(paged_attn_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM));
-    if (rc != FG_OK) return rc;
-    attr_set[dev] = true;
-  }
+  if (dev < 0 || dev >= 64 || done[dev]) return FG_OK;
+  const fg_status rc = fg_cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  done[dev] = rc == FG_OK;
+  return rc;
+}
+
+template <int D, int G>
+fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int limit, bool accumulate, cudaStream_t st) {
   const int rounds = accumulate ? p.tiles : 1;
   a.tiles = accumulate ? 1 : p.tiles;
-  const int64_t items = pairs * a.tiles;
-  if (items * p.nsplit > INT32_MAX) return FG_ERR_SHAPE;
+  const int64_t items = pairs * a.tiles, units = items * p.nsplit;
+  if (units > INT32_MAX) return FG_ERR_SHAPE;
+  a.items = static_cast<int>(items);
+  a.pcols = p.pcols;
+  a.shared_unit = p.shared_unit;
   for (int r = 0; r < rounds; r++) {
     a.tile0 = r;
-    paged_attn_kernel<D, G><<<static_cast<unsigned>(items * p.nsplit), kWarps * 32, S::SMEM, st>>>(a);
-    fg_status rc = fg_launch_check();
-    if (rc != FG_OK) return rc;
-    if (p.nsplit == 1 && !accumulate) continue;
+    fg_status rc = FG_OK;
+    if constexpr (D / G <= 2) {
+      if (p.one) {
+        static bool done[64] = {false};
+        if ((rc = set_smem(paged_attn_one_kernel<D, G>, One<D, G>::SMEM, done)) != FG_OK) return rc;
+        const unsigned grid = static_cast<unsigned>(p.shared_unit ? units : (units + kWarps - 1) / kWarps);
+        paged_attn_one_kernel<D, G><<<grid, kWarps * 32, One<D, G>::SMEM, st>>>(a);
+      }
+    }
+    if (!p.one) {
+      static bool done[64] = {false};
+      if ((rc = set_smem(paged_attn_kernel<D, G>, Shape<D, G>::SMEM, done)) != FG_OK) return rc;
+      paged_attn_kernel<D, G><<<static_cast<unsigned>(units), kWarps * 32, Shape<D, G>::SMEM, st>>>(a);
+    }
+    if ((rc = fg_launch_check()) != FG_OK) return rc;
+    const bool weigh = accumulate && !(p.one && p.nsplit == 1);
+    if (p.nsplit == 1 && !weigh) continue;
     const int left = cols - r * kCols, out_cols = p.nsplit == 1 ? 0 : left < kCols ? left : kCols;
-    const int blocks = accumulate ? (limit + 4 * kJoinThreads - 1) / (4 * kJoinThreads) : 0;
+    const int blocks = weigh ? (limit + 4 * kJoinThreads - 1) / (4 * kJoinThreads) : 0;
     if (out_cols + blocks > 65535) return FG_ERR_SHAPE;
     paged_join_kernel<D><<<dim3(static_cast<unsigned>(items), out_cols + blocks), kJoinThreads, 0, st>>>(a, out_cols);
     if ((rc = fg_launch_check()) != FG_OK) return rc;
@@ -635,7 +1020,7 @@ extern "C" size_t fg_paged_attention_workspace_bytes(const fg_paged_kv *kv, int 
   const int64_t cols = static_cast<int64_t>(num_q_heads / kv->num_heads) * rows_per_seq;
   if (cols > INT32_MAX) return 0;
   return make_plan(static_cast<int64_t>(rows / rows_per_seq) * kv->num_heads, static_cast<int>(cols), kv->head_dim,
-                   plan_limit(kv, max_len), accumulate != 0).total;
+                   fg_kv_group(kv->group), plan_limit(kv, max_len), accumulate != 0).total;
 }
 
 extern "C" fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q, int64_t ldq, int num_q_heads,
@@ -657,7 +1042,7 @@ extern "C" fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q,
   const int64_t cols = static_cast<int64_t>(num_q_heads / kv->num_heads) * rows_per_seq;
   if (pairs > INT32_MAX || cols > INT32_MAX) return FG_ERR_SHAPE;
   const int limit = plan_limit(kv, max_len);
-  Plan p = make_plan(pairs, static_cast<int>(cols), kv->head_dim, limit, accumulate != 0);
+  Plan p = make_plan(pairs, static_cast<int>(cols), kv->head_dim, fg_kv_group(kv->group), limit, accumulate != 0);
   const size_t have = workspace ? workspace_bytes : 0;
   while (p.total > have && !accumulate && p.nsplit > 1) {  // less scratch: fewer, longer splits
     p.nsplit = (p.nsplit + 1) / 2;
