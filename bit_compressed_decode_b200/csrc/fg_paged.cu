@@ -16,11 +16,10 @@ fg_status fg_paged_validate(const fg_paged_kv *kv) {
   if (!kv->k_codes || !kv->v_codes || !kv->k_mins || !kv->k_scales || !kv->v_mins || !kv->v_scales || !kv->page_table)
     return FG_ERR_INVALID;
   if (!fg_aligned16(kv->k_codes) || !fg_aligned16(kv->v_codes) || !fg_aligned16(kv->k_mins) ||
-      !fg_aligned16(kv->k_scales) || !fg_aligned16(kv->v_mins) || !fg_aligned16(kv->v_scales))
+      !fg_aligned16(kv->k_scales) || !fg_aligned16(kv->v_mins) || !fg_aligned16(kv->v_scales) ||
+      !fg_aligned16(kv->weights) || !fg_aligned16(kv->tokens))
     return FG_ERR_INVALID;
-  if ((reinterpret_cast<uintptr_t>(kv->weights) | reinterpret_cast<uintptr_t>(kv->tokens) |
-       reinterpret_cast<uintptr_t>(kv->page_table)) & 3u)
-    return FG_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(kv->page_table) & 3u) return FG_ERR_INVALID;
   return FG_OK;
 }
 

@@ -30,6 +30,8 @@
 // state of a column never leaves its lanes.
 #include <math.h>
 
+#include <type_traits>
+
 #include "fg_paged.cuh"
 
 namespace {
@@ -38,14 +40,14 @@ constexpr int kWarps = 4;
 constexpr int kBlock = 32;              // slots per warp step
 constexpr int kCta = kWarps * kBlock;   // slots per CTA step
 constexpr int kCols = 8;                // columns per tile
-#ifndef FG_ONE_STAGES
-#define FG_ONE_STAGES 3
+#ifndef FG_ONE_CTAS
 #define FG_ONE_CTAS 4
 #endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 2.0f;
 constexpr uint32_t kLoNib = 0x000F000Fu;  // bits 0-3 of both halves: c * 2^-24
 constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves: c * 2^-20
+constexpr uint32_t kByte = 0x00FF00FFu;   // both nibbles of the low byte: (lo + 16 hi) * 2^-24
 constexpr uint32_t kOnes = 0x3C003C00u;   // fp16 {1, 1}
 
 struct PagedAttnArgs {
@@ -114,6 +116,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// d = A * B (fresh accumulators)
+__device__ __forceinline__ void mma_f16_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -163,6 +173,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G>::kCtas) paged_attn_ke
   __shared__ float red_m[kWarps][kCols], red_l[kWarps][kCols];
   __shared__ int bad_page;
 
+  griddep_launch();  // the join may be scheduled once every CTA runs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, c = lane & 3;
   const int item = blockIdx.x / a.nsplit, sp = blockIdx.x % a.nsplit;
@@ -518,8 +529,7 @@ struct One {
   static constexpr int CH = D / 32;  // 32-dim chunks (16 bytes of codes)
   static constexpr int CODE_B = kBlock * RB, META_B = kBlock * NG * 2;
   static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
-  static constexpr int kStages = D == 64 ? 4 : D == 128 ? FG_ONE_STAGES : 2;
-  static constexpr int WARP_B = kStages * STAGE_B;  // >= D * 4, the warp's outputs at the end
+  static constexpr int WARP_B = 2 * STAGE_B;  // two stages; >= D * 4, the warp's outputs at the end
   static constexpr int SMEM = kWarps * WARP_B;
   static constexpr int kCtas = D <= 128 ? FG_ONE_CTAS : 3;
 };
@@ -531,34 +541,99 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t add
                : "memory");
 }
 
-template <int D, int G>
+// A warp's copies of its blocks: what never changes for a lane, and the pool places of the next 32
+// blocks, block i's in lane i, in units of 16 slots.
+constexpr uint32_t kNoSecond = 0xFFFFFFFFu, kJoined = 0xFFFFFFFEu;
+
+template <int RB, int NG, int CODE_B, int META_B>
+struct Copies {
+  const uint8_t *pool;  // lanes 0-5 (first 16 slots) and 8-13 (second): the array of lane % 8
+  uint32_t dst, per16;  // shared address in stage 0; bytes of 16 slots
+  uint32_t a16, b16;    // block `lane`: first half; second half, kJoined (it follows) or kNoSecond
+  bool bad;
+
+  __device__ __forceinline__ void init(const PagedAttnArgs &a, uint32_t base, int lane) {
+    const int arr = lane & 7, run = lane >> 3;
+    const bool codes = arr < 2;
+    const void *const ptr = arr == 0   ? static_cast<const void *>(a.kv.kc)
+                            : arr == 1 ? static_cast<const void *>(a.kv.vc)
+                            : arr == 2 ? static_cast<const void *>(a.kv.km)
+                            : arr == 3 ? static_cast<const void *>(a.kv.ks)
+                            : arr == 4 ? static_cast<const void *>(a.kv.vm)
+                                       : static_cast<const void *>(a.kv.vs);
+    pool = arr < 6 && run < 2 ? static_cast<const uint8_t *>(ptr) : nullptr;
+    per16 = 16u * (codes ? RB : NG * 2);
+    dst = base + (codes ? arr * CODE_B : 2 * CODE_B + (arr - 2) * META_B) + (run & 1) * per16;
+    a16 = b16 = 0;
+    bad = false;
+  }
+  // the places of blocks t + lane * step (slots below t_end)
+  __device__ __forceinline__ void look_up(const PagedAttnArgs &a, int s, int h, int t, int step, int t_end, int lane) {
+    const int64_t tl = t + static_cast<int64_t>(lane) * step;
+    int64_t x = 0, y = 0;
+    if (tl < t_end) x = paged_slot(a.kv, s, h, static_cast<int>(tl));
+    if (tl + 16 < t_end) y = paged_slot(a.kv, s, h, static_cast<int>(tl) + 16);
+    bad |= x < 0 || y < 0;  // flagged at the end; the pool's first slots are read instead
+    x = x < 0 ? 0 : x;
+    y = y < 0 ? 0 : y;
+    a16 = static_cast<uint32_t>(x >> 4);
+    b16 = tl + 16 >= t_end ? kNoSecond : y == x + 16 ? kJoined : static_cast<uint32_t>(y >> 4);
+  }
+  // block `i` of the table into the stage at byte offset `off`, completion on `bar`
+  __device__ __forceinline__ void issue(int i, uint32_t off, uint32_t bar, int lane) {
+    const uint32_t x = __shfl_sync(0xffffffffu, a16, i), y = __shfl_sync(0xffffffffu, b16, i);
+    if (lane == 0) mbar_arrive_expect_tx(bar, (y == kNoSecond ? 16 : 32) * (2 * RB + 8 * NG));
+    __syncwarp();
+    const bool run = lane >> 3;
+    if (pool && (!run || y < kJoined))
+      bulk_g2s(dst + off, pool + static_cast<uint64_t>(run ? y : x) * per16, y == kJoined ? 2 * per16 : per16, bar);
+  }
+};
+
+__device__ __forceinline__ void grow4(const PagedAttnArgs &a, int s, int h, int t, int end, float4 add);
+
+// An item's weights, once its maximum and 1 / sum are known, by `n` threads of which this is number i.
+__device__ __forceinline__ void grow_row(const PagedAttnArgs &a, int s, int h, const float *scores, int end, float m,
+                                         float inv, int i, int n) {
+  for (int t = 4 * i; t < end; t += 4 * n) {
+    const float4 v = *reinterpret_cast<const float4 *>(scores + t);  // (behind `end`: anything, not used)
+    grow4(a, s, h, t, end, make_float4(fast_exp2(v.x - m) * inv, fast_exp2(v.y - m) * inv, fast_exp2(v.z - m) * inv,
+                                       fast_exp2(v.w - m) * inv));
+  }
+}
+
+template <int D, int G, bool TRACK>
 __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_kernel(const PagedAttnArgs a) {
   using S = One<D, G>;
-  constexpr int NG = S::NG, RB = S::RB, KW = S::KW, CH = S::CH, ST = S::kStages;
+  constexpr int NG = S::NG, RB = S::RB, KW = S::KW, CH = S::CH;
   constexpr float kS24 = 16777216.0f, kS20 = 1048576.0f;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full_bar[kWarps][ST];
+  __shared__ __align__(8) uint64_t full_bar[kWarps][2];
   __shared__ float red_m[kWarps], red_l[kWarps];
   __shared__ int bad_page;
 
+  griddep_launch();  // the join may be scheduled once every CTA runs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, c = lane & 3;
-  const int64_t unit = a.shared_unit ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  if (!a.shared_unit && unit >= static_cast<int64_t>(a.items) * a.nsplit) return;
-  const int item = static_cast<int>(unit / a.nsplit), sp = static_cast<int>(unit % a.nsplit);
-  const int first = a.shared_unit ? warp : 0, stride = a.shared_unit ? kWarps : 1;  // this warp's blocks
-  const int s = item / a.kv.H, h = item % a.kv.H;
+  const uint32_t unit = a.shared_unit ? blockIdx.x : blockIdx.x * kWarps + warp;
+  if (!a.shared_unit && unit >= static_cast<uint32_t>(a.items) * a.nsplit) return;
+  const int item = unit / a.nsplit, sp = unit - item * a.nsplit;
+  const int first = a.shared_unit ? warp : 0;
+  const int step = a.shared_unit ? kCta : kBlock;  // slots from one of this warp's blocks to the next
+  const int s = item / a.kv.H, h = item - s * a.kv.H;
   const int pos = a.positions[s], count = a.counts ? a.counts[s] : 1;
   const bool range = pos < -1 || count < 0 || count > 1 || (pos >= 0 && static_cast<int64_t>(pos) + count > a.limit);
   if (range && sp == 0 && first == 0 && lane == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
   const int len = range || pos < 0 || count < 1 ? 0 : pos + 1;
   const int t_begin = sp * a.split, t_end = min(len, t_begin + a.split);
   if (t_begin >= t_end && (sp > 0 || a.nsplit > 1)) return;  // (the join zeroes rows that see nothing)
-  const int nblk = t_end > t_begin ? (t_end - t_begin + kBlock - 1) / kBlock : 0;
-  const int steps = nblk > first ? (nblk - first + stride - 1) / stride : 0;
+  const int t_first = t_begin + first * kBlock;
+  const int steps = t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
 
+  const uint32_t bar0 = smem_u32(&full_bar[warp][0]);
   if (lane == 0) {
-    for (int i = 0; i < ST; i++) mbar_init(smem_u32(&full_bar[warp][i]), 1);
+    mbar_init(bar0, 1);
+    mbar_init(bar0 + 8, 1);
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -570,38 +645,13 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   }
 
   uint8_t *const wbase = smem + warp * S::WARP_B;
-  int64_t slot_a = 0, slot_b = 0;  // pool slots of the two halves of block `lane` of the current 32 steps
-  bool bad = false;
-  auto issue = [&](int k) {
-    const int t = t_begin + (k * stride + first) * kBlock;
-    if ((k & 31) == 0) {
-      const int tl = t + lane * stride * kBlock;
-      slot_a = tl < t_end ? paged_slot(a.kv, s, h, tl) : 0;
-      slot_b = tl + 16 < t_end ? paged_slot(a.kv, s, h, tl + 16) : 0;
-      if (slot_a < 0 || slot_b < 0) bad = true;  // flagged at the end; the pool's first slots instead
-      slot_a = slot_a < 0 ? 0 : slot_a;
-      slot_b = slot_b < 0 ? 0 : slot_b;
-    }
-    const int64_t sa = __shfl_sync(0xffffffffu, slot_a, k & 31), sb = __shfl_sync(0xffffffffu, slot_b, k & 31);
-    const bool second = t + 16 < t_end, joined = second && sb == sa + 16;
-    const uint32_t bar = smem_u32(&full_bar[warp][k % ST]);
-    if (lane == 0) mbar_arrive_expect_tx(bar, (second ? 32 : 16) * (2 * RB + 8 * NG));
-    __syncwarp();
-    const int arr = lane & 7, run = lane >> 3;
-    if (arr < 6 && (run == 0 || (run == 1 && second && !joined))) {
-      const bool codes = arr < 2;
-      const int per = codes ? RB : NG * 2;
-      const uint8_t *pool = arr == 0   ? a.kv.kc
-                            : arr == 1 ? a.kv.vc
-                            : arr == 2 ? reinterpret_cast<const uint8_t *>(a.kv.km)
-                            : arr == 3 ? reinterpret_cast<const uint8_t *>(a.kv.ks)
-                            : arr == 4 ? reinterpret_cast<const uint8_t *>(a.kv.vm)
-                                       : reinterpret_cast<const uint8_t *>(a.kv.vs);
-      const int off = (k % ST) * S::STAGE_B + (codes ? arr * S::CODE_B : 2 * S::CODE_B + (arr - 2) * S::META_B);
-      bulk_g2s(smem_u32(wbase + off + run * 16 * per), pool + (run ? sb : sa) * per, (joined ? 32 : 16) * per, bar);
-    }
-  };
-  for (int k = 0; k < min(ST, steps); k++) issue(k);
+  Copies<RB, NG, S::CODE_B, S::META_B> cp;
+  cp.init(a, smem_u32(wbase), lane);
+  if (steps > 0) {
+    cp.look_up(a, s, h, t_first, step, t_end, lane);
+    cp.issue(0, 0, bar0, lane);
+    if (steps > 1) cp.issue(1, S::STAGE_B, bar0 + 8, lane);
+  }
 
   // ---- q as the B operand; word j of lane class c: dims 2o .. 2o+7 ----
   const __half *qrow = a.q + static_cast<int64_t>(s) * a.ldq + static_cast<int64_t>(h) * D;
@@ -625,10 +675,10 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
 #pragma unroll
       for (int i = 0; i < NG; i++) part[i] += og == i ? sum : 0.f;
       const bool on = !(gid & 1) && (NG == 1 || og == ((gid >> 1) & 1));
-      qf[j][0] = on ? pack_h2(e[0], e[4]) : 0u;
-      qf[j][1] = on ? pack_h2(e[2], e[6]) : 0u;
-      qf[j][2] = on ? pack_h2(e[1], e[5]) : 0u;
-      qf[j][3] = on ? pack_h2(e[3], e[7]) : 0u;
+      qf[j][0] = on ? __byte_perm(v.x, v.z, 0x5410) : 0u;  // dims 0, 4
+      qf[j][1] = on ? __byte_perm(v.y, v.w, 0x5410) : 0u;  // dims 2, 6
+      qf[j][2] = on ? __byte_perm(v.x, v.z, 0x7632) : 0u;  // dims 1, 5
+      qf[j][3] = on ? __byte_perm(v.y, v.w, 0x7632) : 0u;  // dims 3, 7
     }
 #pragma unroll
     for (int i = 0; i < NG; i++) {
@@ -637,10 +687,13 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     }
     ql = (NG == 2 && g ? part[NG - 1] : part[0]) * kLog2e;
   }
-  const bool upper = c & 2;               // this lane's slot is gid + 8 of the 16
+  const bool upper = c & 2;  // this lane's slot is gid + 8 of the 16
   const int tq = gid + (upper ? 8 : 0);
-  float *const srow = a.scores ? a.scores + static_cast<int64_t>(item) * a.score_ld : nullptr;
-  const uint32_t vaddr = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
+  float *const srow = TRACK ? a.scores + static_cast<int64_t>(item) * a.score_ld : nullptr;
+  // this lane's places in a stage: K code rows, group numbers, ldmatrix rows of V codes
+  const uint8_t *const kbase = wbase + gid * RB + (D == 64 ? 8 : 16) * c;
+  const __half *const nbase = reinterpret_cast<const __half *>(wbase + 2 * S::CODE_B) + tq * NG + g;
+  const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
 
   float m = -INFINITY, l = 0.f, vacc = 0.f;
   float ov[CH][2][4];
@@ -649,27 +702,17 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
 #pragma unroll
     for (int x = 0; x < 2; x++) ov[i][x][0] = ov[i][x][1] = ov[i][x][2] = ov[i][x][3] = 0.f;
 
-  bool ok = true;
-  for (int k = 0; k < steps; k++) {
-    const int st = k % ST, t = t_begin + (k * stride + first) * kBlock;
-    if (!mbar_wait_bounded(smem_u32(&full_bar[warp][st]), (k / ST) & 1, nullptr, a.kv.err)) {
-      ok = false;  // gave up: the copies in flight land (or time out) before the stages are written again
-      for (int i = k + 1; i < min(k + ST, steps); i++)
-        mbar_wait_bounded(smem_u32(&full_bar[warp][i % ST]), (i / ST) & 1, nullptr, a.kv.err);
-      break;
-    }
-    const uint8_t *Kc = wbase + st * S::STAGE_B;
-    const __half *Km = reinterpret_cast<const __half *>(Kc + 2 * S::CODE_B);
-    const __half *Ks = Km + kBlock * NG, *Vm = Ks + kBlock * NG, *Vs = Vm + kBlock * NG;
-
-    // ---- scores (log2 units) of slots t + 16u + tq ----
+  // one block of 32 slots at t, in stage ST; EDGE: some of them are not seen
+  auto block = [&](auto stage, auto edge, int t) {
+    constexpr int OFF = decltype(stage)::value * S::STAGE_B;
+    constexpr bool EDGE = decltype(edge)::value;
     float sc[2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
       uint32_t k0[KW], k1[KW];
 #pragma unroll
       for (int j = 0; j < KW; j += (D == 64 ? 2 : 4)) {
-        const uint8_t *p = Kc + (16 * u + gid) * RB + (D == 64 ? 8 * c : 16 * j + 16 * c);
+        const uint8_t *p = kbase + OFF + 16 * u * RB + (D == 64 ? 0 : 16 * j);
         if constexpr (D == 64) {
           const uint2 x = *reinterpret_cast<const uint2 *>(p), y = *reinterpret_cast<const uint2 *>(p + 8 * RB);
           k0[j] = x.x, k0[j + 1] = x.y, k1[j] = y.x, k1[j + 1] = y.y;
@@ -679,34 +722,39 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
           k1[j] = y.x, k1[j + 1] = y.y, k1[j + 2] = y.z, k1[j + 3] = y.w;
         }
       }
-      float lo[4] = {0.f, 0.f, 0.f, 0.f}, hi[4] = {0.f, 0.f, 0.f, 0.f};
+      float lo[4], hi[4];
 #pragma unroll
       for (int j = 0; j < KW; j++) {
         const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
-        mma_f16(lo, x0 & kLoNib, x1 & kLoNib, y0 & kLoNib, y1 & kLoNib, qf[j][0], qf[j][1]);
-        mma_f16(hi, x0 & kHiNib, x1 & kHiNib, y0 & kHiNib, y1 & kHiNib, qf[j][2], qf[j][3]);
+        if (j == 0) {
+          mma_f16_z(lo, x0 & kLoNib, x1 & kLoNib, y0 & kLoNib, y1 & kLoNib, qf[j][0], qf[j][1]);
+          mma_f16_z(hi, x0 & kHiNib, x1 & kHiNib, y0 & kHiNib, y1 & kHiNib, qf[j][2], qf[j][3]);
+        } else {
+          mma_f16(lo, x0 & kLoNib, x1 & kLoNib, y0 & kLoNib, y1 & kLoNib, qf[j][0], qf[j][1]);
+          mma_f16(hi, x0 & kHiNib, x1 & kHiNib, y0 & kHiNib, y1 & kHiNib, qf[j][2], qf[j][3]);
+        }
       }
       const float dot = (upper ? lo[2] : lo[0]) + (upper ? hi[2] : hi[0]) * 0.0625f;
-      const int i = (16 * u + tq) * NG + g;
-      float part = __half2float(Km[i]) * ql + __half2float(Ks[i]) * (kS24 * kLog2e) * dot;
+      const __half *n = nbase + OFF / 2 + 16 * u * NG;
+      float part = __half2float(n[0]) * ql + __half2float(n[kBlock * NG]) * (dot * (kS24 * kLog2e));
       if constexpr (NG == 2) part += __shfl_xor_sync(0xffffffffu, part, 1);
       sc[u] = part;
     }
-    const bool edge = t + kBlock > t_end;  // warp-uniform
-    if (edge) {
+    if constexpr (EDGE) {
 #pragma unroll
       for (int u = 0; u < 2; u++)
         if (t + 16 * u + tq >= t_end) sc[u] = -INFINITY;
     }
-    if (srow && !(c & 1)) {
+    if constexpr (TRACK) {
+      if (!(c & 1))
 #pragma unroll
-      for (int u = 0; u < 2; u++)
-        if (t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u];
+        for (int u = 0; u < 2; u++)
+          if (!EDGE || t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u];
     }
     float cmax = fmaxf(sc[0], sc[1]);
+    if (__any_sync(0xffffffffu, cmax > m + kSlack)) {  // the running maximum moves
 #pragma unroll
-    for (int o = 2; o < 32; o <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
-    if (cmax > m + kSlack) {  // the running maximum moves (warp-uniform)
+      for (int o = 2; o < 32; o <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
       const float al = fast_exp2(m - cmax);
       m = cmax;
       l *= al;
@@ -720,37 +768,61 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     }
 #pragma unroll
     for (int u = 0; u < 2; u++) {
-      const int i = (16 * u + tq) * NG + g;
+      const __half *n = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG;
       const float p = fast_exp2(sc[u] - m);
-      float w = p * __half2float(Vs[i]), pm = p * __half2float(Vm[i]);
-      if (edge && t + 16 * u + tq >= t_end) w = pm = 0.f;  // masked slots may hold anything (their p is 0)
+      float w = p * __half2float(n[kBlock * NG]), pm = p * __half2float(n[0]);
+      if (EDGE && t + 16 * u + tq >= t_end) w = pm = 0.f;  // masked slots may hold anything (their p is 0)
       l += p;
       vacc += pm;
       // w rounded, and the rest, in columns 2c and 2c+1 of the slot's row
-      const __half wh = __float2half_rn(w);
-      uint32_t wp = pack_h2(wh, __float2half_rn(w - __half2float(wh)));
+      uint32_t wp = pack_h2(w, w - __half2float(__float2half_rn(w)));
       if (NG == 1 && (c & 1)) wp = 0u;
       const uint32_t wt = transpose_8x8(wp);
       const uint32_t b0 = gid < 4 ? wt : 0u, b1 = gid < 4 ? 0u : wt;
 #pragma unroll
       for (int ch = 0; ch < CH; ch += 2) {
         uint32_t r[4];  // slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
-        ldmatrix_x4_trans(r, vaddr + st * S::STAGE_B + 16 * u * RB + ch * 16);
+        ldmatrix_x4_trans(r, vbase + OFF + 16 * u * RB + ch * 16);
 #pragma unroll
         for (int y = 0; y < 2; y++) {
-          const uint32_t P = r[2 * y], Q = r[2 * y + 1], Ps = P >> 8, Qs = Q >> 8;
-          mma_f16(ov[ch + y][0], P & kLoNib, P & kHiNib, Q & kLoNib, Q & kHiNib, b0, b1);
-          mma_f16(ov[ch + y][1], Ps & kLoNib, Ps & kHiNib, Qs & kLoNib, Qs & kHiNib, b0, b1);
+          // rows gid take both nibbles of a byte, lo + 16 hi (<= 255, exact), rows gid + 8 the high one
+          const uint32_t P = r[2 * y], Q = r[2 * y + 1];
+          const uint32_t Pb = __byte_perm(P, 0u, 0x4341), Qb = __byte_perm(Q, 0u, 0x4341);
+          mma_f16(ov[ch + y][0], P & kByte, P & kHiNib, Q & kByte, Q & kHiNib, b0, b1);
+          mma_f16(ov[ch + y][1], Pb, Pb & kHiNib, Qb, Qb & kHiNib, b0, b1);
         }
       }
     }
-    if (k + ST < steps) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      issue(k + ST);
+  };
+
+  bool ok = true;
+  int t = t_first;
+  // one step: wait for stage ST, its block, and the copy of the block two steps on
+  auto run = [&](auto stage, int k, uint32_t parity) -> bool {
+    constexpr int ST = decltype(stage)::value;
+    if (!mbar_wait_bounded(bar0 + 8 * ST, parity, nullptr, a.kv.err)) {
+      // gave up: the copy in flight lands (or times out) before the stages are written again
+      if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), ST ? parity ^ 1 : parity, nullptr, a.kv.err);
+      ok = false;
+      return false;
     }
+    if (t + kBlock > t_end) block(stage, std::true_type{}, t);
+    else block(stage, std::false_type{}, t);
+    if (k + 2 < steps) {
+      fence_proxy_async_smem();  // every lane has used the stage before the copy that refills it
+      __syncwarp();
+      if (((k + 2) & 31) == 0) cp.look_up(a, s, h, t + 2 * step, step, t_end, lane);
+      cp.issue((k + 2) & 31, ST * S::STAGE_B, bar0 + 8 * ST, lane);
+    }
+    t += step;
+    return true;
+  };
+  uint32_t parity = 0;
+  for (int k = 0; k < steps; k += 2, parity ^= 1) {
+    if (!run(std::integral_constant<int, 0>{}, k, parity)) break;
+    if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1, parity)) break;
   }
-  const bool any_bad = __any_sync(0xffffffffu, bad);
+  const bool any_bad = __any_sync(0xffffffffu, cp.bad);
   if (any_bad && lane == 0) {
     atomicOr(a.kv.err, FG_DEVERR_RANGE);
     if (a.shared_unit) bad_page = 1;
@@ -769,8 +841,8 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     float v[4];
 #pragma unroll
     for (int x = 0; x < 2; x++) {
-      v[2 * x] = (ov[i][x][0] + ov[i][x][1]) * kS24;
       v[2 * x + 1] = (ov[i][x][2] + ov[i][x][3]) * kS20;
+      v[2 * x] = (ov[i][x][0] + ov[i][x][1]) * kS24 - 16.f * v[2 * x + 1];
     }
 #pragma unroll
     for (int x = 0; x < 4; x++) {
@@ -798,12 +870,9 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
         }
       }
     }
-    if (srow && a.nsplit == 1 && on) {  // this warp saw the whole row: its slots' weights
+    if (TRACK && a.nsplit == 1 && on) {  // this warp saw the whole row: its slots' weights
       __syncwarp();
-      for (int t = lane; t < t_end; t += 32) {
-        const int64_t slot = paged_slot(a.kv, s, h, t);
-        a.kv.weights[slot] += fast_exp2(srow[t] - m) * inv;
-      }
+      grow_row(a, s, h, srow, t_end, m, inv, lane, 32);
     }
     return;
   }
@@ -844,76 +913,132 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
       *reinterpret_cast<__half2 *>(orow + d) = on ? __floats2half2_rn(o0 * inv, o1 * inv) : __floats2half2_rn(0.f, 0.f);
     }
   }
-  if (srow && a.nsplit == 1 && on)  // (the CTA's scores were published by the barrier above)
-    for (int t = tid; t < t_end; t += kWarps * 32) {
-      const int64_t slot = paged_slot(a.kv, s, h, t);
-      a.kv.weights[slot] += fast_exp2(srow[t] - M) * inv;
-    }
+  if (TRACK && a.nsplit == 1 && on)  // (the CTA's scores were published by the barrier above)
+    grow_row(a, s, h, srow, t_end, M, inv, tid, kWarps * 32);
 }
 
-// Column n of an item over its splits: maximum and sum; sum 0: nothing seen, or a bad page.
+// Column n of an item over its splits, by one warp: maximum and sum; sum 0: nothing seen, or a bad
+// page.
 __device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, const float2 *ml, int n, int used) {
+  const int lane = threadIdx.x & 31;
   float M = -INFINITY, den = 0.f;
   bool bad = false;
-  for (int j = 0; j < used; j++) {
+  for (int j = lane; j < used; j += 32) {
     const float2 v = ml[j * a.pcols + n];
     bad |= v.y < 0.f;
-    M = fmaxf(M, v.x);
+    const float mx = fmaxf(M, v.x);
+    if (v.x != -INFINITY) den = (M == -INFINITY ? 0.f : den * exp2f(M - mx)) + v.y * exp2f(v.x - mx);
+    M = mx;
   }
-  for (int j = 0; j < used; j++) {
-    const float2 v = ml[j * a.pcols + n];
-    den += v.x == -INFINITY ? 0.f : exp2f(v.x - M) * v.y;
-  }
-  return make_float2(M, bad ? 0.f : den);
+  float top = M;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  den = M == -INFINITY ? 0.f : den * exp2f(M - top);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  return make_float2(top, __any_sync(0xffffffffu, bad) ? 0.f : den);
 }
 
-constexpr int kJoinThreads = 128;
+// The weights of the 4 slots t .. t + 3 (t % 4 == 0, so that they lie in one page), of which those
+// below `end` grow.
+__device__ __forceinline__ void grow4(const PagedAttnArgs &a, int s, int h, int t, int end, float4 add) {
+  const int64_t slot = paged_slot(a.kv, s, h, t);
+  if (slot < 0) return;
+  float *w = a.kv.weights + slot;
+  float4 v = *reinterpret_cast<float4 *>(w);
+  v.x += add.x;
+  v.y += t + 1 < end ? add.y : 0.f;
+  v.z += t + 2 < end ? add.z : 0.f;
+  v.w += t + 3 < end ? add.w : 0.f;
+  if (t + 3 < end) {
+    *reinterpret_cast<float4 *>(w) = v;
+  } else {  // the slots behind stay as they are
+    w[0] = v.x;
+    if (t + 1 < end) w[1] = v.y;
+    if (t + 2 < end) w[2] = v.z;
+  }
+}
 
-// blockIdx.x: item; blockIdx.y < out_cols: that column's splits joined into its output row; beyond:
-// a block of kJoinThreads * 4 slots whose weights grow by the columns' probabilities.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinSlots = kJoinWarps * 32 * 4;  // slots of a block that grows weights
+
+// blockIdx.x: item; blockIdx.y < out_cols: that column's splits joined into its output row, every
+// kJoinWarps-th split by a warp; beyond: kJoinSlots slots whose weights grow by the columns'
+// probabilities.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedAttnArgs a, int out_cols) {
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnArgs a, int out_cols) {
+  constexpr int V = D / 32;  // dims per lane
   __shared__ float2 col[kCols];
-  const int item = blockIdx.x, tid = threadIdx.x;
+  __shared__ float part[kJoinWarps][D];
+  const int item = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Item it = load_item(a, item, false);
   int lmax = 0;
   const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
   if (last >= it.n0) lmax = it.len(last, a.R);
   const int used = (lmax + a.split - 1) / a.split;
   const float2 *ml = a.ml + static_cast<int64_t>(item) * a.nsplit * a.pcols;
+  griddep_wait();
   if (static_cast<int>(blockIdx.y) < out_cols) {
     const int n = blockIdx.y;
     if (n >= it.ncols) return;
     const int cn = it.n0 + n;
     const float2 t = it.len(cn, a.R) > 0 ? join_ml(a, ml, n, used) : make_float2(0.f, 0.f);
-    __half *dst = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
-                  (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D;
-    const float *po = a.po + static_cast<int64_t>(item) * a.nsplit * a.pcols * D + n * D;
-    for (int d = tid; d < D; d += kJoinThreads) {
-      float o = 0.f;
-      if (t.y != 0.f)
-        for (int j = 0; j < used; j++) {
-          const float f = exp2f(ml[j * a.pcols + n].x - t.x);
-          if (f != 0.f) o += f * po[static_cast<int64_t>(j) * a.pcols * D + d];
+    float o[V];
+#pragma unroll
+    for (int e = 0; e < V; e++) o[e] = 0.f;
+    if (t.y != 0.f) {
+      const float *po = a.po + (static_cast<int64_t>(item) * a.nsplit * a.pcols + n) * D + lane * V;
+#pragma unroll 4
+      for (int j = warp; j < used; j += kJoinWarps) {
+        const float x = ml[j * a.pcols + n].x;
+        const float f = x == -INFINITY ? 0.f : exp2f(x - t.x);
+        const float *p = po + static_cast<int64_t>(j) * a.pcols * D;
+        float v[V];
+        if constexpr (V == 2) {
+          *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(p + e);
         }
-      dst[d] = __float2half_rn(t.y != 0.f ? o / t.y : 0.f);
+#pragma unroll
+        for (int e = 0; e < V; e++) o[e] += f == 0.f ? 0.f : f * v[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < V; e++) part[warp][lane * V + e] = o[e];
+    __syncthreads();
+    if (tid < D) {
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; w++) sum += part[w][tid];
+      __half *dst = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
+                    (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D;
+      dst[tid] = __float2half_rn(t.y != 0.f ? sum / t.y : 0.f);
     }
     return;
   }
-  const int t0 = (blockIdx.y - out_cols) * kJoinThreads * 4;
+  const int t0 = (blockIdx.y - out_cols) * kJoinSlots;
   if (t0 >= lmax) return;
-  if (tid < kCols) col[tid] = tid < it.ncols && it.len(it.n0 + tid, a.R) > 0 ? join_ml(a, ml, tid, used) : make_float2(0.f, 0.f);
-  __syncthreads();
-  const float *sc = a.scores + static_cast<int64_t>(item) * a.pcols * a.score_ld;
-  for (int e = 0; e < 4; e++) {
-    const int t = t0 + e * kJoinThreads + tid;
-    if (t >= lmax) break;
-    float add = 0.f;
-    for (int n = 0; n < it.ncols; n++)
-      if (col[n].y != 0.f && t < it.len(it.n0 + n, a.R)) add += exp2f(sc[n * a.score_ld + t] - col[n].x) / col[n].y;
-    const int64_t slot = paged_slot(a.kv, it.s, it.h, t);
-    if (slot >= 0) a.kv.weights[slot] += add;
+  if (warp < kCols) {
+    const float2 v = warp < it.ncols && it.len(it.n0 + warp, a.R) > 0 ? join_ml(a, ml, warp, used) : make_float2(0.f, 0.f);
+    if (lane == 0) col[warp] = make_float2(v.x, v.y != 0.f ? 1.0f / v.y : 0.f);
   }
+  __syncthreads();
+  const int t = t0 + tid * 4;
+  if (t >= lmax) return;
+  const float *sc = a.scores + static_cast<int64_t>(item) * a.pcols * a.score_ld + t;
+  float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int n = 0; n < it.ncols; n++) {
+    const int end = it.len(it.n0 + n, a.R);
+    const float2 c = col[n];
+    if (c.y == 0.f || t >= end) continue;
+    const float4 v = *reinterpret_cast<const float4 *>(sc + n * a.score_ld);
+    add.x += exp2f(v.x - c.x) * c.y;  // (scores behind the column's last slot hold anything)
+    add.y += t + 1 < end ? exp2f(v.y - c.x) * c.y : 0.f;
+    add.z += t + 2 < end ? exp2f(v.z - c.x) * c.y : 0.f;
+    add.w += t + 3 < end ? exp2f(v.w - c.x) * c.y : 0.f;
+  }
+  grow4(a, it.s, it.h, t, lmax, add);
 }
 
 struct Plan {
@@ -938,20 +1063,39 @@ void plan_bytes(Plan *p, int64_t pairs, int D, int limit, bool accumulate) {
   p->total = p->ml + p->po + p->scores;
 }
 
-// Splits so that the launch is about four waves of resident CTAs, of at least 512 slots each.
-// Single-column launches of more than four waves of warps give every warp an item of its own.
+#ifndef FG_PLAN_K
+#define FG_PLAN_K 2
+#endif
+#ifndef FG_PLAN_SHARED
+#define FG_PLAN_SHARED 4
+#endif
+// Single-column launches: a warp takes a unit of its own once there are enough ...
 Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate) {
   Plan p;
   p.one = cols == 1 && D / G <= 2;
   p.pcols = p.one ? 1 : kCols;
   p.tiles = (cols + kCols - 1) / kCols;
   const int per_sm = p.one && D <= 128 ? FG_ONE_CTAS : 3;
-  const int64_t items = pairs * (accumulate ? 1 : p.tiles), room = 4LL * per_sm * fg_sm_count();
-  p.shared_unit = !p.one || pairs < room * kWarps;
-  int64_t c = (items * limit + room - 1) / room;
-  c = c < 512 ? 512 : c;
-  c = (c + kCta - 1) / kCta * kCta;
-  const int64_t most = (static_cast<int64_t>(limit) + kCta - 1) / kCta * kCta;
+  const int64_t items = pairs * (accumulate ? 1 : p.tiles);
+  int64_t c, unit;
+  if (p.one) {
+    const int64_t warps = static_cast<int64_t>(per_sm) * kWarps * fg_sm_count();
+    int64_t want = FG_PLAN_K * warps / (items > 0 ? items : 1);  // warps per item
+    const int64_t most = (limit + 255) / 256;
+    want = want > most ? most : want;
+    p.shared_unit = want > 1 && want <= FG_PLAN_SHARED;
+    const int64_t n = want <= FG_PLAN_SHARED ? 1 : want;
+    unit = kBlock;
+    c = (limit + n - 1) / n;
+  } else {
+    p.shared_unit = true;
+    const int64_t room = 4LL * per_sm * fg_sm_count();
+    c = (items * limit + room - 1) / room;
+    c = c < 512 ? 512 : c;
+    unit = kCta;
+  }
+  c = (c + unit - 1) / unit * unit;
+  const int64_t most = (static_cast<int64_t>(limit) + unit - 1) / unit * unit;
   p.split = static_cast<int>(c < most ? c : most);
   p.nsplit = (limit + p.split - 1) / p.split;
   plan_bytes(&p, pairs, D, limit, accumulate);
@@ -987,10 +1131,11 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int li
     fg_status rc = FG_OK;
     if constexpr (D / G <= 2) {
       if (p.one) {
-        static bool done[64] = {false};
-        if ((rc = set_smem(paged_attn_one_kernel<D, G>, One<D, G>::SMEM, done)) != FG_OK) return rc;
+        static bool done[2][64] = {{false}};
+        const auto kernel = accumulate ? paged_attn_one_kernel<D, G, true> : paged_attn_one_kernel<D, G, false>;
+        if ((rc = set_smem(kernel, One<D, G>::SMEM, done[accumulate])) != FG_OK) return rc;
         const unsigned grid = static_cast<unsigned>(p.shared_unit ? units : (units + kWarps - 1) / kWarps);
-        paged_attn_one_kernel<D, G><<<grid, kWarps * 32, One<D, G>::SMEM, st>>>(a);
+        kernel<<<grid, kWarps * 32, One<D, G>::SMEM, st>>>(a);
       }
     }
     if (!p.one) {
@@ -1002,9 +1147,19 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int li
     const bool weigh = accumulate && !(p.one && p.nsplit == 1);
     if (p.nsplit == 1 && !weigh) continue;
     const int left = cols - r * kCols, out_cols = p.nsplit == 1 ? 0 : left < kCols ? left : kCols;
-    const int blocks = weigh ? (limit + 4 * kJoinThreads - 1) / (4 * kJoinThreads) : 0;
+    const int blocks = weigh ? (limit + kJoinSlots - 1) / kJoinSlots : 0;
     if (out_cols + blocks > 65535) return FG_ERR_SHAPE;
-    paged_join_kernel<D><<<dim3(static_cast<unsigned>(items), out_cols + blocks), kJoinThreads, 0, st>>>(a, out_cols);
+    // a programmatic dependent: its blocks start while the last splits run and wait for them
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(static_cast<unsigned>(items), out_cols + blocks);
+    lc.blockDim = dim3(kJoinWarps * 32);
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    if ((rc = fg_cuda_check(cudaLaunchKernelEx(&lc, paged_join_kernel<D>, a, out_cols))) != FG_OK) return rc;
     if ((rc = fg_launch_check()) != FG_OK) return rc;
   }
   return FG_OK;

@@ -193,7 +193,7 @@ extern "C" fg_status fg_paged_kv_evict(const fg_paged_kv *kv, const int32_t *len
   if (budget < 1 || recent < 0 || recent > budget || max_len < 0) return FG_ERR_INVALID;
   if (kv->num_seqs == 0) return FG_OK;
   if (!lengths || !next_tokens || !new_lengths || !fg_aligned16(workspace)) return FG_ERR_INVALID;
-  if ((reinterpret_cast<uintptr_t>(weights_out) | reinterpret_cast<uintptr_t>(tokens_out)) & 3u) return FG_ERR_INVALID;
+  if (!fg_aligned16(weights_out) || !fg_aligned16(tokens_out)) return FG_ERR_INVALID;
   if (static_cast<int64_t>(kv->num_seqs) * kv->num_heads > INT32_MAX) return FG_ERR_SHAPE;
   EvictArgs a;
   if (!fg_paged_args(kv, &a.kv)) return FG_ERR_CUDA;

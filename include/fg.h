@@ -198,7 +198,7 @@ FG_API fg_status fg_attention_decode_append(const fg_kv_cache *kv, const fg_half
  *   weights                     fp32  [num_pages][num_heads][page_size], attention weight received
  *   tokens                      int32 [num_pages][num_heads][page_size], number of the slot's token
  * An fg_kv_cache is the case page_size = max_len, num_pages = num_seqs, page_table[s] = {s}.
- * Device memory, caller-owned; the code, min and scale pools 16-byte aligned, the others 4-byte.
+ * Device memory, caller-owned; the pools 16-byte aligned, the table 4-byte.
  * Requirements: page_size a multiple of 16, head_dim in {64, 128, 256} and a multiple of G,
  * max_pages * page_size <= INT32_MAX.  Table entries that no call below reaches may hold anything.
  * Sequences may share pages that are only read; pages that a call appends to, accumulates weights
