@@ -40,6 +40,12 @@ constexpr int kWarps = 4;
 constexpr int kBlock = 32;              // slots per warp step
 constexpr int kCta = kWarps * kBlock;   // slots per CTA step
 constexpr int kCols = 8;                // columns per tile
+#ifndef FG_CTAS
+#define FG_CTAS 3
+#endif
+#ifndef FG_NT2
+#define FG_NT2 1
+#endif
 #ifndef FG_ONE_CTAS
 #define FG_ONE_CTAS 4
 #endif
@@ -84,8 +90,8 @@ __device__ __forceinline__ Item load_item(const PagedAttnArgs &a, int item, bool
   const int sh = item / a.tiles, tile = a.tile0 + item % a.tiles;
   it.s = sh / a.kv.H;
   it.h = sh % a.kv.H;
-  it.n0 = tile * kCols;
-  it.ncols = min(kCols, a.rows_per_seq * a.R - it.n0);
+  it.n0 = tile * a.pcols;
+  it.ncols = min(a.pcols, a.rows_per_seq * a.R - it.n0);
   const int pos = a.positions[it.s], count = a.counts ? a.counts[it.s] : a.rows_per_seq;
   const bool range = pos < -1 || count < 0 || count > a.rows_per_seq ||
                      (pos >= 0 && static_cast<int64_t>(pos) + count > a.limit);
@@ -95,18 +101,17 @@ __device__ __forceinline__ Item load_item(const PagedAttnArgs &a, int item, bool
   return it;
 }
 
-template <int D, int G>
+template <int D, int G, int NT>  // NT: column tiles of 8 per unit
 struct Shape {
   static constexpr int NG = D / G;
   static constexpr int RB = D / 2;                 // code bytes per slot
   static constexpr int KW = G / 32;                // K code words per lane, slot and group
-  static constexpr int VW = G / 64;                // V code words per lane, slot and group
+  static constexpr int CH = D / 32;                // 32-dim chunks (16 bytes of codes)
   static constexpr int CODE_B = kBlock * RB, META_B = kBlock * NG * 2;
   static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
-  static constexpr int kStages = D == 64 ? 6 : D == 128 ? 4 : 2;
-  static constexpr int WARP_B = kStages * STAGE_B;  // >= 8 * D * 4, the warp's outputs at the end
-  static constexpr int SMEM = kWarps * WARP_B;
-  static constexpr int kCtas = 3;
+  static constexpr int WARP_B = 2 * STAGE_B > NT * kCols * D * 4 ? 2 * STAGE_B : NT * kCols * D * 4;
+  static constexpr int SMEM = kWarps * WARP_B;  // two stages a warp; at the end its outputs
+  static constexpr int kCtas = NT == 1 ? FG_CTAS : 2;
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -141,11 +146,6 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ uint32_t pack_h2(__half lo, __half hi) {
-  const __half2 h = __halves2half2(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
   if constexpr (N == 1) {
@@ -162,377 +162,6 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
     w[3] = v.w;
   }
 }
-
-template <int D, int G>
-__global__ void __launch_bounds__(kWarps * 32, Shape<D, G>::kCtas) paged_attn_kernel(const PagedAttnArgs a) {
-  using S = Shape<D, G>;
-  constexpr int NG = S::NG, RB = S::RB, KW = S::KW, VW = S::VW, ST = S::kStages;
-  constexpr float kS24 = 16777216.0f, kS20 = 1048576.0f;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full_bar[kWarps][ST];
-  __shared__ float red_m[kWarps][kCols], red_l[kWarps][kCols];
-  __shared__ int bad_page;
-
-  griddep_launch();  // the join may be scheduled once every CTA runs
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int gid = lane >> 2, c = lane & 3;
-  const int item = blockIdx.x / a.nsplit, sp = blockIdx.x % a.nsplit;
-  const Item it = load_item(a, item, sp == 0 && tid == 0);
-  // live columns' lengths: rows ascend with the column, so the last live one sees most
-  int lmin = 0, lmax = 0;
-  {
-    const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
-    if (last >= it.n0) {
-      lmin = it.len(it.n0, a.R);
-      lmax = it.len(last, a.R);
-    }
-  }
-  const int t_begin = sp * a.split, t_end = min(lmax, t_begin + a.split);
-  if (t_begin >= t_end && (sp > 0 || a.nsplit > 1)) return;  // (the join zeroes rows that see nothing)
-  const int nblk = t_end > t_begin ? (t_end - t_begin + kBlock - 1) / kBlock : 0;
-  const int steps = nblk > warp ? (nblk - warp + kWarps - 1) / kWarps : 0;
-
-  if (tid == 0) bad_page = 0;
-  if (lane == 0) {
-    for (int i = 0; i < ST; i++) mbar_init(smem_u32(&full_bar[warp][i]), 1);
-    fence_mbar_init();
-    fence_proxy_async_smem();
-  }
-  __syncthreads();
-
-  uint8_t *const wbase = smem + warp * S::WARP_B;
-  // pool slots of the first and second 16 slots of block `lane` of the current 32 steps
-  int64_t slot_a = 0, slot_b = 0;
-  bool bad = false;
-  auto issue = [&](int k) {  // every lane; step k of this warp into stage k % ST
-    const int t = t_begin + (k * kWarps + warp) * kBlock;
-    if ((k & 31) == 0) {
-      const int tl = t + lane * kCta;
-      slot_a = tl < t_end ? paged_slot(a.kv, it.s, it.h, tl) : 0;
-      slot_b = tl + 16 < t_end ? paged_slot(a.kv, it.s, it.h, tl + 16) : 0;
-      // a bad page: flagged below, its slots read from the pool's first instead
-      if (slot_a < 0 || slot_b < 0) bad = true;
-      slot_a = slot_a < 0 ? 0 : slot_a;
-      slot_b = slot_b < 0 ? 0 : slot_b;
-    }
-    const int64_t sa = __shfl_sync(0xffffffffu, slot_a, k & 31), sb = __shfl_sync(0xffffffffu, slot_b, k & 31);
-    const bool second = t + 16 < t_end, joined = second && sb == sa + 16;
-    const uint32_t bar = smem_u32(&full_bar[warp][k % ST]);
-    if (lane == 0) mbar_arrive_expect_tx(bar, (second ? 32 : 16) * (2 * RB + 8 * NG));
-    __syncwarp();
-    const int arr = lane & 7, run = lane >> 3;  // lanes 0-5: first run, 8-13: second
-    if (arr < 6 && (run == 0 || (run == 1 && second && !joined))) {
-      const bool codes = arr < 2;
-      const int per = codes ? RB : NG * 2;
-      const uint8_t *pool = arr == 0   ? a.kv.kc
-                            : arr == 1 ? a.kv.vc
-                            : arr == 2 ? reinterpret_cast<const uint8_t *>(a.kv.km)
-                            : arr == 3 ? reinterpret_cast<const uint8_t *>(a.kv.ks)
-                            : arr == 4 ? reinterpret_cast<const uint8_t *>(a.kv.vm)
-                                       : reinterpret_cast<const uint8_t *>(a.kv.vs);
-      const int off = (k % ST) * S::STAGE_B + (codes ? arr * S::CODE_B : 2 * S::CODE_B + (arr - 2) * S::META_B);
-      bulk_g2s(smem_u32(wbase + off + run * 16 * per), pool + (run ? sb : sa) * per, (joined ? 32 : 16) * per, bar);
-    }
-  };
-  for (int k = 0; k < min(ST, steps); k++) issue(k);
-
-  // ---- q of column n0 + gid as the B operand of the score MMAs ----
-  // Word j of group g of lane class c: dims 2o .. 2o+7, o = g*G/2 + c*G/8 + 4j.  Low-nibble MMA
-  // (bits 0-3 of w and of w >> 8): k slots (2c, 2c+1) = dims (2o, 2o+4), (2c+8, 2c+9) = (2o+2,
-  // 2o+6); high-nibble MMA: the same + 1.
-  uint32_t qf[NG][KW][4];
-  float qsum[2][NG];  // columns 2c, 2c+1: sum of q over the group, times log2(e)
-  {
-    const bool on = gid < it.ncols && it.len(it.n0 + gid, a.R) > 0;
-    const int n = it.n0 + gid;
-    const __half *qrow = a.q + (static_cast<int64_t>(it.s) * a.rows_per_seq + n / a.R) * a.ldq +
-                         (static_cast<int64_t>(it.h) * a.R + n % a.R) * D;
-#pragma unroll
-    for (int g = 0; g < NG; g++) {
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < KW; j++) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (on) v = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
-        const __half *e = reinterpret_cast<const __half *>(&v);
-        qf[g][j][0] = pack_h2(e[0], e[4]);
-        qf[g][j][1] = pack_h2(e[2], e[6]);
-        qf[g][j][2] = pack_h2(e[1], e[5]);
-        qf[g][j][3] = pack_h2(e[3], e[7]);
-#pragma unroll
-        for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      qsum[0][g] = __shfl_sync(0xffffffffu, sum, 8 * c) * kLog2e;
-      qsum[1][g] = __shfl_sync(0xffffffffu, sum, 8 * c + 4) * kLog2e;
-    }
-  }
-  int len[2];
-#pragma unroll
-  for (int e = 0; e < 2; e++) len[e] = 2 * c + e < it.ncols ? it.len(it.n0 + 2 * c + e, a.R) : 0;
-  float *srow[2] = {nullptr, nullptr};
-  if (a.scores)
-#pragma unroll
-    for (int e = 0; e < 2; e++)
-      if (len[e] > 0) srow[e] = a.scores + (static_cast<int64_t>(item) * kCols + 2 * c + e) * a.score_ld;
-
-  const int tok = (gid >> 1) + 4 * (gid & 1);  // slot of score row gid in its 16 (row gid + 8: 8 further)
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float vacc[2][NG];      // sum of p (min + 7.5 scale) over this lane's slots
-  float ov[NG][VW][4][4]; // tile 2h + x of word w: dims + 4h + 2x (row gid) and + 1 (row gid + 8)
-  float wacc[NG][4];      // every row: sum of w
-#pragma unroll
-  for (int g = 0; g < NG; g++) {
-    vacc[0][g] = vacc[1][g] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; e++) wacc[g][e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < VW; w++)
-#pragma unroll
-      for (int x = 0; x < 4; x++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) ov[g][w][x][e] = 0.f;
-  }
-
-  bool ok = true;
-  for (int k = 0; k < steps; k++) {
-    const int t = t_begin + (k * kWarps + warp) * kBlock;
-    if (!mbar_wait_bounded(smem_u32(&full_bar[warp][k % ST]), (k / ST) & 1, nullptr, a.kv.err)) {
-      ok = false;  // gave up: the copies in flight land (or time out) before the stages are written again
-      for (int i = k + 1; i < min(k + ST, steps); i++)
-        mbar_wait_bounded(smem_u32(&full_bar[warp][i % ST]), (i / ST) & 1, nullptr, a.kv.err);
-      break;
-    }
-    const uint8_t *Kc = wbase + (k % ST) * S::STAGE_B, *Vc = Kc + S::CODE_B;
-    const __half *Km = reinterpret_cast<const __half *>(Kc + 2 * S::CODE_B);
-    const __half *Ks = Km + kBlock * NG, *Vm = Ks + kBlock * NG, *Vs = Vm + kBlock * NG;
-    const int ntile = t + 16 < t_end ? 2 : 1;  // (a second tile that was not copied is masked out)
-
-    // ---- scores (log2 units) of slots t + 16u + tok + 8x, columns 2c + e ----
-    float sc[2][2][2];
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-#pragma unroll
-      for (int x = 0; x < 2; x++) sc[u][x][0] = sc[u][x][1] = 0.f;
-#pragma unroll
-      for (int g = 0; g < NG; g++) {
-        uint32_t k0[KW], k1[KW];
-        load_words<KW>(Kc + (16 * u + tok) * RB + g * (G / 2) + c * (G / 8), k0);
-        load_words<KW>(Kc + (16 * u + tok + 8) * RB + g * (G / 2) + c * (G / 8), k1);
-        float lo[4] = {0.f, 0.f, 0.f, 0.f}, hi[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < KW; j++) {
-          const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
-          mma_f16(lo, x0 & kLoNib, x1 & kLoNib, y0 & kLoNib, y1 & kLoNib, qf[g][j][0], qf[g][j][1]);
-          mma_f16(hi, x0 & kHiNib, x1 & kHiNib, y0 & kHiNib, y1 & kHiNib, qf[g][j][2], qf[g][j][3]);
-        }
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-          const float mn = __half2float(Km[(16 * u + tok + 8 * x) * NG + g]);
-          const float s24 = __half2float(Ks[(16 * u + tok + 8 * x) * NG + g]) * (kS24 * kLog2e);
-#pragma unroll
-          for (int e = 0; e < 2; e++)
-            sc[u][x][e] += mn * qsum[e][g] + s24 * (lo[2 * x + e] + hi[2 * x + e] * 0.0625f);
-        }
-      }
-    }
-    const bool edge = t + kBlock > lmin;  // warp-uniform: some live column does not see all 32 slots
-    if (edge) {
-#pragma unroll
-      for (int u = 0; u < 2; u++)
-#pragma unroll
-        for (int x = 0; x < 2; x++)
-#pragma unroll
-          for (int e = 0; e < 2; e++)
-            if (t + 16 * u + tok + 8 * x >= len[e] || u >= ntile) sc[u][x][e] = -INFINITY;
-    }
-    if (a.scores) {
-#pragma unroll
-      for (int e = 0; e < 2; e++)
-        if (srow[e])
-#pragma unroll
-          for (int u = 0; u < 2; u++)
-#pragma unroll
-            for (int x = 0; x < 2; x++)
-              if (t + 16 * u + tok + 8 * x < len[e]) srow[e][t + 16 * u + tok + 8 * x] = sc[u][x][e];
-    }
-    // ---- running maximum: moves only when a score exceeds it by more than kSlack, so that
-    //      p = 2^(s - m) <= 2^kSlack and w = p * scale stays inside fp16 ----
-    float cmax[2];
-#pragma unroll
-    for (int e = 0; e < 2; e++) {
-      cmax[e] = fmaxf(fmaxf(sc[0][0][e], sc[0][1][e]), fmaxf(sc[1][0][e], sc[1][1][e]));
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) cmax[e] = fmaxf(cmax[e], __shfl_xor_sync(0xffffffffu, cmax[e], o));
-    }
-    if (__any_sync(0xffffffffu, cmax[0] > m[0] + kSlack || cmax[1] > m[1] + kSlack)) {
-      float al[2];
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const float mn = fmaxf(m[e], cmax[e]);
-        al[e] = mn == -INFINITY ? 1.f : fast_exp2(m[e] - mn);
-        m[e] = mn;
-        l[e] *= al[e];
-      }
-#pragma unroll
-      for (int g = 0; g < NG; g++) {
-        vacc[0][g] *= al[0];
-        vacc[1][g] *= al[1];
-#pragma unroll
-        for (int i = 0; i < 4; i++) wacc[g][i] *= al[i & 1];
-#pragma unroll
-        for (int w = 0; w < VW; w++)
-#pragma unroll
-          for (int x = 0; x < 4; x++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) ov[g][w][x][i] *= al[i & 1];
-      }
-    }
-    // ---- p, the sums, and the output product ----
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-      float p[2][2];
-#pragma unroll
-      for (int x = 0; x < 2; x++)
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-          p[x][e] = edge && sc[u][x][e] == -INFINITY ? 0.f : fast_exp2(sc[u][x][e] - m[e]);
-          l[e] += p[x][e];
-        }
-#pragma unroll
-      for (int g = 0; g < NG; g++) {
-        uint32_t b[2];
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-          const float vs = __half2float(Vs[(16 * u + tok + 8 * x) * NG + g]);
-          const float vb = __half2float(Vm[(16 * u + tok + 8 * x) * NG + g]) + 7.5f * vs;
-          float w0 = p[x][0] * vs, w1 = p[x][1] * vs, o0 = p[x][0] * vb, o1 = p[x][1] * vb;
-          if (edge) {  // masked slots may hold anything
-            if (p[x][0] == 0.f) w0 = o0 = 0.f;
-            if (p[x][1] == 0.f) w1 = o1 = 0.f;
-          }
-          vacc[0][g] += o0;
-          vacc[1][g] += o1;
-          b[x] = transpose_8x8(pack_h2(w0, w1));
-        }
-        mma_f16(wacc[g], kOnes, kOnes, kOnes, kOnes, b[0], b[1]);
-        // lane (gid, c): code words of slots c, c+4, c+8, c+12 at its dims of the group
-        uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
-        const uint8_t *vrow = Vc + (16 * u + c) * RB + g * (G / 2) + gid * (G / 16);
-        load_words<VW>(vrow, v0);
-        load_words<VW>(vrow + 4 * RB, v1);
-        load_words<VW>(vrow + 8 * RB, v2);
-        load_words<VW>(vrow + 12 * RB, v3);
-#pragma unroll
-        for (int w = 0; w < VW; w++)
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const uint32_t sel = h ? 0x7632u : 0x5410u;
-            const uint32_t P = __byte_perm(v0[w], v1[w], sel), Q = __byte_perm(v2[w], v3[w], sel);
-            const uint32_t Ps = P >> 8, Qs = Q >> 8;
-            mma_f16(ov[g][w][2 * h], P & kLoNib, P & kHiNib, Q & kLoNib, Q & kHiNib, b[0], b[1]);
-            mma_f16(ov[g][w][2 * h + 1], Ps & kLoNib, Ps & kHiNib, Qs & kLoNib, Qs & kHiNib, b[0], b[1]);
-          }
-      }
-    }
-    if (k + ST < steps) {  // every lane has used the stage; its reads come before the copy that refills it
-      fence_proxy_async_smem();
-      __syncwarp();
-      issue(k + ST);
-    }
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) {
-    atomicOr(a.kv.err, FG_DEVERR_RANGE);
-    bad_page = 1;
-  }
-
-  // ---- this warp's columns into its (drained) stages, then the four warps' joined ----
-#pragma unroll
-  for (int e = 0; e < 2; e++) {
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], o);
-#pragma unroll
-    for (int g = 0; g < NG; g++)
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) vacc[e][g] += __shfl_xor_sync(0xffffffffu, vacc[e][g], o);
-    if (gid == 0) {
-      red_m[warp][2 * c + e] = m[e];
-      red_l[warp][2 * c + e] = l[e];
-    }
-  }
-  float *wo = reinterpret_cast<float *>(wbase);  // [8][D]
-#pragma unroll
-  for (int g = 0; g < NG; g++)
-#pragma unroll
-    for (int w = 0; w < VW; w++)
-#pragma unroll
-      for (int x = 0; x < 4; x++)
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-          const float base = vacc[e][g] - 7.5f * wacc[g][e];
-          *reinterpret_cast<float2 *>(wo + (2 * c + e) * D + g * G + gid * (G / 8) + w * 8 + 2 * x) =
-              make_float2(ov[g][w][x][e] * kS24 + base, ov[g][w][x][2 + e] * kS20 + base);
-        }
-  const bool all_ok = __syncthreads_and(ok) && !bad_page;
-  for (int i = tid; i < kCols * (D / 2); i += kWarps * 32) {
-    const int n = i / (D / 2), d = 2 * (i % (D / 2));
-    if (n >= it.ncols) break;
-    float M = -INFINITY, den = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) M = fmaxf(M, red_m[w][n]);
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-      const float f = red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M);
-      const float2 o = *reinterpret_cast<const float2 *>(smem + w * S::WARP_B + (n * D + d) * 4);
-      den += f * red_l[w][n];
-      if (f != 0.f) {  // (a warp without slots has nothing written that counts)
-        o0 += f * o.x;
-        o1 += f * o.y;
-      }
-    }
-    const int64_t pi = (static_cast<int64_t>(item) * a.nsplit + sp) * kCols + n;
-    if (a.ml && d == 0) a.ml[pi] = make_float2(M, all_ok ? den : -1.f);
-    if (a.nsplit > 1) {
-      *reinterpret_cast<float2 *>(a.po + pi * D + d) = make_float2(o0, o1);
-    } else {
-      const int cn = it.n0 + n;
-      const bool on = it.len(cn, a.R) > 0 && all_ok;
-      const float inv = 1.0f / den;
-      __half2 *dst = reinterpret_cast<__half2 *>(
-          a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
-          (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + d);
-      *dst = on ? __floats2half2_rn(o0 * inv, o1 * inv) : __floats2half2_rn(0.f, 0.f);
-    }
-  }
-}
-
-// ------------------------------------------------------------------------------------------------
-// One column (one new token, a key-value head of its own): the tile's eight columns hold what one
-// column has to offer instead.
-//   scores: column 2c of q is zero outside group c % 2, so that lane (gid, c) finds the dot product
-//           of slot gid + 8 (c / 2) with group c % 2 in its own fragment; the two lanes of a slot
-//           add their groups' shares.
-//   output: lane (gid, c) holds w of that slot and group as two fp16 numbers, w's rounding and the
-//           rest (22 bits together), in columns 2c and 2c+1 of a matrix whose transpose is the B
-//           operand: columns 0-3 for slots 0-7 of the 16, columns 4-7 for slots 8-15.
-// A = V codes transposed comes from ldmatrix.trans on 16-bit elements (4 codes of a slot): a lane
-// gets two slots' codes of dims 4 gid .. 4 gid + 3, in operand order.
-// Units: with many items a warp takes a whole split of one item and no two warps ever meet;
-// otherwise the CTA's four warps share a unit, 32-slot blocks in turn, and join at the end.
-// ------------------------------------------------------------------------------------------------
-template <int D, int G>
-struct One {
-  static constexpr int NG = D / G;  // 1 or 2
-  static constexpr int RB = D / 2;
-  static constexpr int KW = D / 32;  // K code words per lane and slot
-  static constexpr int CH = D / 32;  // 32-dim chunks (16 bytes of codes)
-  static constexpr int CODE_B = kBlock * RB, META_B = kBlock * NG * 2;
-  static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
-  static constexpr int WARP_B = 2 * STAGE_B;  // two stages; >= D * 4, the warp's outputs at the end
-  static constexpr int SMEM = kWarps * WARP_B;
-  static constexpr int kCtas = D <= 128 ? FG_ONE_CTAS : 3;
-};
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -590,7 +219,35 @@ struct Copies {
   }
 };
 
-__device__ __forceinline__ void grow4(const PagedAttnArgs &a, int s, int h, int t, int end, float4 add);
+// The weights of the 4 slots t .. t + 3 (t % 4 == 0, so that they lie in one page), of which those
+// below `end` grow.
+__device__ __forceinline__ void grow4(const PagedAttnArgs &a, int s, int h, int t, int end, float4 add) {
+  const int64_t slot = paged_slot(a.kv, s, h, t);
+  if (slot < 0) return;
+  float *w = a.kv.weights + slot;
+  float4 v = *reinterpret_cast<float4 *>(w);
+  v.x += add.x;
+  v.y += t + 1 < end ? add.y : 0.f;
+  v.z += t + 2 < end ? add.z : 0.f;
+  v.w += t + 3 < end ? add.w : 0.f;
+  if (t + 3 < end) {
+    *reinterpret_cast<float4 *>(w) = v;
+  } else {  // the slots behind stay as they are
+    w[0] = v.x;
+    if (t + 1 < end) w[1] = v.y;
+    if (t + 2 < end) w[2] = v.z;
+  }
+}
+
+// A column's probabilities of slots t .. t + 3 (those below its length `end`), added to *add.
+__device__ __forceinline__ void grow_by(float4 *add, const float *scores, int t, int end, float m, float inv) {
+  if (t >= end) return;
+  const float4 v = *reinterpret_cast<const float4 *>(scores + t);  // (behind `end`: anything)
+  add->x += fast_exp2(v.x - m) * inv;
+  add->y += t + 1 < end ? fast_exp2(v.y - m) * inv : 0.f;
+  add->z += t + 2 < end ? fast_exp2(v.z - m) * inv : 0.f;
+  add->w += t + 3 < end ? fast_exp2(v.w - m) * inv : 0.f;
+}
 
 // An item's weights, once its maximum and 1 / sum are known, by `n` threads of which this is number i.
 __device__ __forceinline__ void grow_row(const PagedAttnArgs &a, int s, int h, const float *scores, int end, float m,
@@ -601,6 +258,435 @@ __device__ __forceinline__ void grow_row(const PagedAttnArgs &a, int s, int h, c
                                        fast_exp2(v.w - m) * inv));
   }
 }
+
+template <int D, int G, int NT, bool TRACK>
+__global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_attn_kernel(const PagedAttnArgs a) {
+  using S = Shape<D, G, NT>;
+  constexpr int NG = S::NG, RB = S::RB, KW = S::KW, CH = S::CH, NC = NT * kCols;
+  constexpr float kS24 = 16777216.0f, kS20 = 1048576.0f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full_bar[kWarps][2];
+  __shared__ float red_m[kWarps][NC], red_l[kWarps][NC];
+  __shared__ int bad_page;
+
+  griddep_launch();  // the join may be scheduled once every CTA runs
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, c = lane & 3;
+  const uint32_t unit = a.shared_unit ? blockIdx.x : blockIdx.x * kWarps + warp;
+  if (!a.shared_unit && unit >= static_cast<uint32_t>(a.items) * a.nsplit) return;
+  const int item = unit / a.nsplit, sp = unit - item * a.nsplit;
+  const int first = a.shared_unit ? warp : 0;
+  const int step = a.shared_unit ? kCta : kBlock;  // slots from one of this warp's blocks to the next
+  const Item it = load_item(a, item, sp == 0 && first == 0 && lane == 0);
+  // live columns' lengths: rows ascend with the column, so the last live one sees most
+  int lmin = 0, lmax = 0;
+  {
+    const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
+    if (last >= it.n0) {
+      lmin = it.len(it.n0, a.R);
+      lmax = it.len(last, a.R);
+    }
+  }
+  const int t_begin = sp * a.split, t_end = min(lmax, t_begin + a.split);
+  if (t_begin >= t_end && (sp > 0 || a.nsplit > 1)) return;  // (the join zeroes rows that see nothing)
+  const int t_first = t_begin + first * kBlock;
+  const int steps = t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
+
+  const uint32_t bar0 = smem_u32(&full_bar[warp][0]);
+  if (lane == 0) {
+    mbar_init(bar0, 1);
+    mbar_init(bar0 + 8, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (a.shared_unit) {
+    if (tid == 0) bad_page = 0;
+    __syncthreads();
+  } else {
+    __syncwarp();
+  }
+
+  uint8_t *const wbase = smem + warp * S::WARP_B;
+  Copies<RB, NG, S::CODE_B, S::META_B> cp;
+  cp.init(a, smem_u32(wbase), lane);
+  if (steps > 0) {
+    cp.look_up(a, it.s, it.h, t_first, step, t_end, lane);
+    cp.issue(0, 0, bar0, lane);
+    if (steps > 1) cp.issue(1, S::STAGE_B, bar0 + 8, lane);
+  }
+
+  // ---- q of column n0 + 8 nt + gid as the B operand of the score MMAs ----
+  // Word j of group g of lane class c: dims 2o .. 2o+7, o = g*G/2 + c*G/8 + 4j.  Low-nibble MMA
+  // (bits 0-3 of w and of w >> 8): k slots (2c, 2c+1) = dims (2o, 2o+4), (2c+8, 2c+9) = (2o+2,
+  // 2o+6); high-nibble MMA: the same + 1.
+  uint32_t qf[NT][NG][KW][4];
+  float qsum[NT][2][NG];  // columns 2c, 2c+1: sum of q over the group, times log2(e)
+  int len[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    const int col = nt * kCols + gid, n = it.n0 + col;
+    const bool on = col < it.ncols && it.len(n, a.R) > 0;
+    const __half *qrow = a.q + (static_cast<int64_t>(it.s) * a.rows_per_seq + n / a.R) * a.ldq +
+                         (static_cast<int64_t>(it.h) * a.R + n % a.R) * D;
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < KW; j++) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (on) v = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
+        const __half *e = reinterpret_cast<const __half *>(&v);
+        qf[nt][g][j][0] = __byte_perm(v.x, v.z, 0x5410);  // dims 0, 4
+        qf[nt][g][j][1] = __byte_perm(v.y, v.w, 0x5410);  // dims 2, 6
+        qf[nt][g][j][2] = __byte_perm(v.x, v.z, 0x7632);  // dims 1, 5
+        qf[nt][g][j][3] = __byte_perm(v.y, v.w, 0x7632);  // dims 3, 7
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      qsum[nt][0][g] = __shfl_sync(0xffffffffu, sum, 8 * c) * kLog2e;
+      qsum[nt][1][g] = __shfl_sync(0xffffffffu, sum, 8 * c + 4) * kLog2e;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      const int m = nt * kCols + 2 * c + e;
+      len[nt][e] = m < it.ncols ? it.len(it.n0 + m, a.R) : 0;
+    }
+  }
+  float *const srow = TRACK ? a.scores + static_cast<int64_t>(item) * NC * a.score_ld : nullptr;
+  // this lane's places in a stage: K code rows, group numbers, ldmatrix rows of V codes
+  const uint8_t *const kbase = wbase + gid * RB + c * (G / 8);
+  const __half *const nbase = reinterpret_cast<const __half *>(wbase + 2 * S::CODE_B) + gid * NG;
+  const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
+
+  float m[NT][2], l[NT][2];
+  float vacc[NT][2][NG];   // sum of p (min + 7.5 scale) over this lane's slots
+  float ov[NT][CH][2][4];  // chunk ch, x: dims 32 ch + 4 gid + 2x (row gid, with 16 times the next) and + 1
+  float wacc[NT][NG][4];   // every row: sum of w
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int g = 0; g < NG; g++) {
+      vacc[nt][0][g] = vacc[nt][1][g] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; e++) wacc[nt][g][e] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+#pragma unroll
+      for (int x = 0; x < 2; x++) ov[nt][i][x][0] = ov[nt][i][x][1] = ov[nt][i][x][2] = ov[nt][i][x][3] = 0.f;
+  }
+
+  // one block of 32 slots at t, in stage ST; EDGE: some live column does not see all of them
+  auto block = [&](auto stage, auto edge, int t) {
+    constexpr int OFF = decltype(stage)::value * S::STAGE_B;
+    constexpr bool EDGE = decltype(edge)::value;
+    // ---- scores (log2 units) of slots t + 16u + gid + 8x, columns 2c + e ----
+    float sc[NT][2][2][2];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+        uint32_t k0[KW], k1[KW];
+        load_words<KW>(kbase + OFF + 16 * u * RB + g * (G / 2), k0);
+        load_words<KW>(kbase + OFF + (16 * u + 8) * RB + g * (G / 2), k1);
+        float lo[NT][4], hi[NT][4];
+#pragma unroll
+        for (int j = 0; j < KW; j++) {
+          const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
+          const uint32_t l0 = x0 & kLoNib, l1 = x1 & kLoNib, l2 = y0 & kLoNib, l3 = y1 & kLoNib;
+          const uint32_t h0 = x0 & kHiNib, h1 = x1 & kHiNib, h2 = y0 & kHiNib, h3 = y1 & kHiNib;
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            if (j == 0) {
+              mma_f16_z(lo[nt], l0, l1, l2, l3, qf[nt][g][j][0], qf[nt][g][j][1]);
+              mma_f16_z(hi[nt], h0, h1, h2, h3, qf[nt][g][j][2], qf[nt][g][j][3]);
+            } else {
+              mma_f16(lo[nt], l0, l1, l2, l3, qf[nt][g][j][0], qf[nt][g][j][1]);
+              mma_f16(hi[nt], h0, h1, h2, h3, qf[nt][g][j][2], qf[nt][g][j][3]);
+            }
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+          const __half *n = nbase + OFF / 2 + (16 * u + 8 * x) * NG + g;
+          const float mn = __half2float(n[0]), s24 = __half2float(n[kBlock * NG]) * (kS24 * kLog2e);
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              const float v = mn * qsum[nt][e][g] + s24 * (lo[nt][2 * x + e] + hi[nt][2 * x + e] * 0.0625f);
+              sc[nt][u][x][e] = g == 0 ? v : sc[nt][u][x][e] + v;
+            }
+        }
+      }
+    }
+    if constexpr (EDGE) {
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+          for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+              if (t + 16 * u + gid + 8 * x >= min(len[nt][e], t_end)) sc[nt][u][x][e] = -INFINITY;
+    }
+    if constexpr (TRACK) {
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+          if (len[nt][e] > 0)
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+              for (int x = 0; x < 2; x++) {
+                const int ts = t + 16 * u + gid + 8 * x;
+                if (!EDGE || ts < len[nt][e]) srow[(nt * kCols + 2 * c + e) * a.score_ld + ts] = sc[nt][u][x][e];
+              }
+    }
+    // ---- running maximum: moves only when a score exceeds it by more than kSlack, so that
+    //      p = 2^(s - m) <= 2^kSlack and w = p * scale stays inside fp16 ----
+    float cmax[NT][2];
+    bool moves = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        cmax[nt][e] = fmaxf(fmaxf(sc[nt][0][0][e], sc[nt][0][1][e]), fmaxf(sc[nt][1][0][e], sc[nt][1][1][e]));
+        moves |= cmax[nt][e] > m[nt][e] + kSlack;
+      }
+    if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+        float al[2];
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          float mn = cmax[nt][e];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+          mn = fmaxf(m[nt][e], mn);
+          al[e] = mn == -INFINITY ? 1.f : fast_exp2(m[nt][e] - mn);
+          m[nt][e] = mn;
+          l[nt][e] *= al[e];
+        }
+#pragma unroll
+        for (int g = 0; g < NG; g++) {
+          vacc[nt][0][g] *= al[0];
+          vacc[nt][1][g] *= al[1];
+#pragma unroll
+          for (int i = 0; i < 4; i++) wacc[nt][g][i] *= al[i & 1];
+        }
+#pragma unroll
+        for (int ch = 0; ch < CH; ch++)
+#pragma unroll
+          for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) ov[nt][ch][x][i] *= al[i & 1];
+      }
+    }
+    // ---- p, the sums, and the output product ----
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      float p[NT][2][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            p[nt][x][e] = EDGE && sc[nt][u][x][e] == -INFINITY ? 0.f : fast_exp2(sc[nt][u][x][e] - m[nt][e]);
+            l[nt][e] += p[nt][x][e];
+          }
+      uint32_t b[NT][NG][2];
+#pragma unroll
+      for (int g = 0; g < NG; g++) {
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+          const __half *n = nbase + OFF / 2 + (2 * kBlock + 16 * u + 8 * x) * NG + g;
+          const float vs = __half2float(n[kBlock * NG]), vb = __half2float(n[0]) + 7.5f * vs;
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            float w0 = p[nt][x][0] * vs, w1 = p[nt][x][1] * vs, o0 = p[nt][x][0] * vb, o1 = p[nt][x][1] * vb;
+            if constexpr (EDGE) {  // masked slots may hold anything
+              if (p[nt][x][0] == 0.f) w0 = o0 = 0.f;
+              if (p[nt][x][1] == 0.f) w1 = o1 = 0.f;
+            }
+            vacc[nt][0][g] += o0;
+            vacc[nt][1][g] += o1;
+            b[nt][g][x] = transpose_8x8(pack_h2(w0, w1));
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) mma_f16(wacc[nt][g], kOnes, kOnes, kOnes, kOnes, b[nt][g][0], b[nt][g][1]);
+      }
+#pragma unroll
+      for (int ch = 0; ch < CH; ch += 2) {
+        uint32_t r[4];  // slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
+        ldmatrix_x4_trans(r, vbase + OFF + 16 * u * RB + ch * 16);
+        const int g = ch * 32 / G;
+#pragma unroll
+        for (int y = 0; y < 2; y++) {
+          // rows gid take both nibbles of a byte, lo + 16 hi (<= 255, exact), rows gid + 8 the high one
+          const uint32_t P = r[2 * y], Q = r[2 * y + 1];
+          const uint32_t Pb = __byte_perm(P, 0u, 0x4341), Qb = __byte_perm(Q, 0u, 0x4341);
+          const uint32_t Pl = P & kByte, Ph = P & kHiNib, Ql = Q & kByte, Qh = Q & kHiNib;
+          const uint32_t Pbh = Pb & kHiNib, Qbh = Qb & kHiNib;
+#pragma unroll
+          for (int nt = 0; nt < NT; nt++) {
+            mma_f16(ov[nt][ch + y][0], Pl, Ph, Ql, Qh, b[nt][g][0], b[nt][g][1]);
+            mma_f16(ov[nt][ch + y][1], Pb, Pbh, Qb, Qbh, b[nt][g][0], b[nt][g][1]);
+          }
+        }
+      }
+    }
+  };
+
+  bool ok = true;
+  int t = t_first;
+  // one step: wait for stage ST, its block, and the copy of the block two steps on
+  auto run = [&](auto stage, int k, uint32_t parity) -> bool {
+    constexpr int ST = decltype(stage)::value;
+    if (!mbar_wait_bounded(bar0 + 8 * ST, parity, nullptr, a.kv.err)) {
+      // gave up: the copy in flight lands (or times out) before the stages are written again
+      if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), ST ? parity ^ 1 : parity, nullptr, a.kv.err);
+      ok = false;
+      return false;
+    }
+    if (t + kBlock > min(lmin, t_end)) block(stage, std::true_type{}, t);
+    else block(stage, std::false_type{}, t);
+    if (k + 2 < steps) {
+      fence_proxy_async_smem();  // every lane has used the stage before the copy that refills it
+      __syncwarp();
+      if (((k + 2) & 31) == 0) cp.look_up(a, it.s, it.h, t + 2 * step, step, t_end, lane);
+      cp.issue((k + 2) & 31, ST * S::STAGE_B, bar0 + 8 * ST, lane);
+    }
+    t += step;
+    return true;
+  };
+  uint32_t parity = 0;
+  for (int k = 0; k < steps; k += 2, parity ^= 1) {
+    if (!run(std::integral_constant<int, 0>{}, k, parity)) break;
+    if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1, parity)) break;
+  }
+  const bool any_bad = __any_sync(0xffffffffu, cp.bad);
+  if (any_bad && lane == 0) {
+    atomicOr(a.kv.err, FG_DEVERR_RANGE);
+    if (a.shared_unit) bad_page = 1;
+  }
+
+  // ---- this warp's columns: their totals, and their outputs into its (drained) stages ----
+  float *const wo = reinterpret_cast<float *>(wbase);  // [NC][D]
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+#pragma unroll
+      for (int g = 0; g < NG; g++)
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) vacc[nt][e][g] += __shfl_xor_sync(0xffffffffu, vacc[nt][e][g], o);
+      const int n = nt * kCols + 2 * c + e;
+      if (gid == 0) {
+        red_m[warp][n] = m[nt][e];
+        red_l[warp][n] = l[nt][e];
+      }
+      if (n < it.ncols) {
+#pragma unroll
+        for (int ch = 0; ch < CH; ch++) {
+          const float base = vacc[nt][e][ch * 32 / G] - 7.5f * wacc[nt][ch * 32 / G][e];
+          float v[4];
+#pragma unroll
+          for (int x = 0; x < 2; x++) {
+            v[2 * x + 1] = ov[nt][ch][x][2 + e] * kS20;
+            v[2 * x] = ov[nt][ch][x][e] * kS24 - 16.f * v[2 * x + 1];
+          }
+          *reinterpret_cast<float4 *>(wo + n * D + ch * 32 + 4 * gid) =
+              make_float4(v[0] + base, v[1] + base, v[2] + base, v[3] + base);
+        }
+      }
+    }
+  }
+  // ---- the unit's warps joined: all four of the CTA, or this one ----
+  bool good;
+  if (a.shared_unit) {
+    good = __syncthreads_and(ok) && !bad_page;
+  } else {
+    __syncwarp();
+    good = ok && !any_bad;
+  }
+  const int w0 = a.shared_unit ? 0 : warp, w1 = a.shared_unit ? kWarps : warp + 1;
+  const int me = a.shared_unit ? tid : lane, all = a.shared_unit ? kWarps * 32 : 32;
+  for (int i = me; i < it.ncols * (D / 4); i += all) {
+    const int n = i / (D / 4), d = 4 * (i % (D / 4));
+    float M = -INFINITY, den = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = w0; w < w1; w++) M = fmaxf(M, red_m[w][n]);
+    for (int w = w0; w < w1; w++) {
+      const float f = red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M);
+      const float4 v = *reinterpret_cast<const float4 *>(smem + w * S::WARP_B + (n * D + d) * 4);
+      den += f * red_l[w][n];
+      if (f != 0.f) o = make_float4(o.x + f * v.x, o.y + f * v.y, o.z + f * v.z, o.w + f * v.w);
+    }
+    const int64_t pi = (static_cast<int64_t>(item) * a.nsplit + sp) * NC + n;
+    if (a.nsplit > 1) {
+      if (d == 0) a.ml[pi] = make_float2(M, good ? den : -1.f);
+      *reinterpret_cast<float4 *>(a.po + pi * D + d) = o;
+    } else {
+      const int cn = it.n0 + n;
+      const float inv = 1.0f / den;
+      uint2 r = make_uint2(0u, 0u);
+      if (it.len(cn, a.R) > 0 && good) r = make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
+      *reinterpret_cast<uint2 *>(a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
+                                 (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + d) = r;
+    }
+  }
+  if (TRACK && a.nsplit == 1 && good) {  // the unit saw whole rows: its slots' weights
+    for (int i = 4 * me; i < lmax; i += 4 * all) {
+      float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int n = 0; n < it.ncols; n++) {
+        const int end = it.len(it.n0 + n, a.R);
+        float M = -INFINITY, den = 0.f;
+        for (int w = w0; w < w1; w++) M = fmaxf(M, red_m[w][n]);
+        for (int w = w0; w < w1; w++) den += red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M) * red_l[w][n];
+        grow_by(&add, srow + n * a.score_ld, i, end, M, 1.0f / den);
+      }
+      grow4(a, it.s, it.h, i, lmax, add);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// One column (one new token, a key-value head of its own): the tile's eight columns hold what one
+// column has to offer instead.
+//   scores: column 2c of q is zero outside group c % 2, so that lane (gid, c) finds the dot product
+//           of slot gid + 8 (c / 2) with group c % 2 in its own fragment; the two lanes of a slot
+//           add their groups' shares.
+//   output: lane (gid, c) holds w of that slot and group as two fp16 numbers, w's rounding and the
+//           rest (22 bits together), in columns 2c and 2c+1 of a matrix whose transpose is the B
+//           operand: columns 0-3 for slots 0-7 of the 16, columns 4-7 for slots 8-15.
+// A = V codes transposed comes from ldmatrix.trans on 16-bit elements (4 codes of a slot): a lane
+// gets two slots' codes of dims 4 gid .. 4 gid + 3, in operand order.
+// Units: with many items a warp takes a whole split of one item and no two warps ever meet;
+// otherwise the CTA's four warps share a unit, 32-slot blocks in turn, and join at the end.
+// ------------------------------------------------------------------------------------------------
+template <int D, int G>
+struct One {
+  static constexpr int NG = D / G;  // 1 or 2
+  static constexpr int RB = D / 2;
+  static constexpr int KW = D / 32;  // K code words per lane and slot
+  static constexpr int CH = D / 32;  // 32-dim chunks (16 bytes of codes)
+  static constexpr int CODE_B = kBlock * RB, META_B = kBlock * NG * 2;
+  static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
+  static constexpr int WARP_B = 2 * STAGE_B;  // two stages; >= D * 4, the warp's outputs at the end
+  static constexpr int SMEM = kWarps * WARP_B;
+  static constexpr int kCtas = D <= 128 ? FG_ONE_CTAS : 3;
+};
 
 template <int D, int G, bool TRACK>
 __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_kernel(const PagedAttnArgs a) {
@@ -939,27 +1025,8 @@ __device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, const float2 *
   return make_float2(top, __any_sync(0xffffffffu, bad) ? 0.f : den);
 }
 
-// The weights of the 4 slots t .. t + 3 (t % 4 == 0, so that they lie in one page), of which those
-// below `end` grow.
-__device__ __forceinline__ void grow4(const PagedAttnArgs &a, int s, int h, int t, int end, float4 add) {
-  const int64_t slot = paged_slot(a.kv, s, h, t);
-  if (slot < 0) return;
-  float *w = a.kv.weights + slot;
-  float4 v = *reinterpret_cast<float4 *>(w);
-  v.x += add.x;
-  v.y += t + 1 < end ? add.y : 0.f;
-  v.z += t + 2 < end ? add.z : 0.f;
-  v.w += t + 3 < end ? add.w : 0.f;
-  if (t + 3 < end) {
-    *reinterpret_cast<float4 *>(w) = v;
-  } else {  // the slots behind stay as they are
-    w[0] = v.x;
-    if (t + 1 < end) w[1] = v.y;
-    if (t + 2 < end) w[2] = v.z;
-  }
-}
-
 constexpr int kJoinWarps = 8;
+constexpr int kMaxCols = 16;  // columns per item: at most two tiles
 constexpr int kJoinSlots = kJoinWarps * 32 * 4;  // slots of a block that grows weights
 
 // blockIdx.x: item; blockIdx.y < out_cols: that column's splits joined into its output row, every
@@ -968,7 +1035,7 @@ constexpr int kJoinSlots = kJoinWarps * 32 * 4;  // slots of a block that grows 
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnArgs a, int out_cols) {
   constexpr int V = D / 32;  // dims per lane
-  __shared__ float2 col[kCols];
+  __shared__ float2 col[kMaxCols];
   __shared__ float part[kJoinWarps][D];
   const int item = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const Item it = load_item(a, item, false);
@@ -1019,30 +1086,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
   }
   const int t0 = (blockIdx.y - out_cols) * kJoinSlots;
   if (t0 >= lmax) return;
-  if (warp < kCols) {
-    const float2 v = warp < it.ncols && it.len(it.n0 + warp, a.R) > 0 ? join_ml(a, ml, warp, used) : make_float2(0.f, 0.f);
-    if (lane == 0) col[warp] = make_float2(v.x, v.y != 0.f ? 1.0f / v.y : 0.f);
+  for (int n = warp; n < it.ncols; n += kJoinWarps) {
+    const float2 v = it.len(it.n0 + n, a.R) > 0 ? join_ml(a, ml, n, used) : make_float2(0.f, 0.f);
+    if (lane == 0) col[n] = make_float2(v.x, v.y != 0.f ? 1.0f / v.y : 0.f);
   }
   __syncthreads();
   const int t = t0 + tid * 4;
   if (t >= lmax) return;
-  const float *sc = a.scores + static_cast<int64_t>(item) * a.pcols * a.score_ld + t;
+  const float *sc = a.scores + static_cast<int64_t>(item) * a.pcols * a.score_ld;
   float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int n = 0; n < it.ncols; n++) {
     const int end = it.len(it.n0 + n, a.R);
     const float2 c = col[n];
-    if (c.y == 0.f || t >= end) continue;
-    const float4 v = *reinterpret_cast<const float4 *>(sc + n * a.score_ld);
-    add.x += exp2f(v.x - c.x) * c.y;  // (scores behind the column's last slot hold anything)
-    add.y += t + 1 < end ? exp2f(v.y - c.x) * c.y : 0.f;
-    add.z += t + 2 < end ? exp2f(v.z - c.x) * c.y : 0.f;
-    add.w += t + 3 < end ? exp2f(v.w - c.x) * c.y : 0.f;
+    if (c.y == 0.f) continue;
+    grow_by(&add, sc + n * a.score_ld, t, end, c.x, c.y);
   }
   grow4(a, it.s, it.h, t, lmax, add);
 }
 
 struct Plan {
-  int tiles, split, nsplit, pcols;
+  int tiles, split, nsplit, pcols;  // column tiles of pcols columns
   bool one, shared_unit;
   size_t ml, po, scores, total;  // bytes, each part 256-byte aligned
   int64_t score_ld;
@@ -1056,8 +1119,7 @@ void plan_bytes(Plan *p, int64_t pairs, int D, int limit, bool accumulate) {
   const int64_t items = pairs * (accumulate ? 1 : p->tiles);
   const bool parts = p->nsplit > 1;
   p->score_ld = (static_cast<int64_t>(limit) + 31) / 32 * 32;
-  p->ml = parts || (accumulate && !p->one)
-              ? align256(static_cast<size_t>(items) * p->nsplit * p->pcols * sizeof(float2)) : 0;
+  p->ml = parts ? align256(static_cast<size_t>(items) * p->nsplit * p->pcols * sizeof(float2)) : 0;
   p->po = parts ? align256(static_cast<size_t>(items) * p->nsplit * p->pcols * D * sizeof(float)) : 0;
   p->scores = accumulate ? align256(static_cast<size_t>(items) * p->pcols * p->score_ld * sizeof(float)) : 0;
   p->total = p->ml + p->po + p->scores;
@@ -1069,34 +1131,21 @@ void plan_bytes(Plan *p, int64_t pairs, int D, int limit, bool accumulate) {
 #ifndef FG_PLAN_SHARED
 #define FG_PLAN_SHARED 4
 #endif
-// Single-column launches: a warp takes a unit of its own once there are enough ...
+// A warp takes a unit of its own once there are enough ...
 Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate) {
   Plan p;
   p.one = cols == 1 && D / G <= 2;
-  p.pcols = p.one ? 1 : kCols;
-  p.tiles = (cols + kCols - 1) / kCols;
-  const int per_sm = p.one && D <= 128 ? FG_ONE_CTAS : 3;
+  p.pcols = p.one ? 1 : cols > kCols && D <= 128 && FG_NT2 ? 2 * kCols : kCols;
+  p.tiles = (cols + p.pcols - 1) / p.pcols;
+  const int per_sm = p.one ? (D <= 128 ? FG_ONE_CTAS : 3) : p.pcols > kCols ? 2 : FG_CTAS;
   const int64_t items = pairs * (accumulate ? 1 : p.tiles);
-  int64_t c, unit;
-  if (p.one) {
-    const int64_t warps = static_cast<int64_t>(per_sm) * kWarps * fg_sm_count();
-    int64_t want = FG_PLAN_K * warps / (items > 0 ? items : 1);  // warps per item
-    const int64_t most = (limit + 255) / 256;
-    want = want > most ? most : want;
-    p.shared_unit = want > 1 && want <= FG_PLAN_SHARED;
-    const int64_t n = want <= FG_PLAN_SHARED ? 1 : want;
-    unit = kBlock;
-    c = (limit + n - 1) / n;
-  } else {
-    p.shared_unit = true;
-    const int64_t room = 4LL * per_sm * fg_sm_count();
-    c = (items * limit + room - 1) / room;
-    c = c < 512 ? 512 : c;
-    unit = kCta;
-  }
-  c = (c + unit - 1) / unit * unit;
-  const int64_t most = (static_cast<int64_t>(limit) + unit - 1) / unit * unit;
-  p.split = static_cast<int>(c < most ? c : most);
+  const int64_t warps = static_cast<int64_t>(per_sm) * kWarps * fg_sm_count();
+  int64_t want = FG_PLAN_K * warps / (items > 0 ? items : 1);  // warps per item
+  const int64_t most = (limit + 255) / 256;
+  want = want > most ? most : want;
+  p.shared_unit = want > 1 && want <= FG_PLAN_SHARED;
+  const int64_t n = want <= FG_PLAN_SHARED ? 1 : want;
+  p.split = static_cast<int>(((limit + n - 1) / n + kBlock - 1) / kBlock * kBlock);
   p.nsplit = (limit + p.split - 1) / p.split;
   plan_bytes(&p, pairs, D, limit, accumulate);
   return p;
@@ -1117,6 +1166,17 @@ fg_status set_smem(K kernel, int bytes, bool (&done)[64]) {
   return rc;
 }
 
+template <int D, int G, int NT>
+fg_status launch_tiles(const PagedAttnArgs &a, unsigned grid, bool accumulate, cudaStream_t st) {
+  using S = Shape<D, G, NT>;
+  static bool done[2][64] = {{false}};
+  const auto kernel = accumulate ? paged_attn_kernel<D, G, NT, true> : paged_attn_kernel<D, G, NT, false>;
+  const fg_status rc = set_smem(kernel, S::SMEM, done[accumulate]);
+  if (rc != FG_OK) return rc;
+  kernel<<<grid, kWarps * 32, S::SMEM, st>>>(a);
+  return FG_OK;
+}
+
 template <int D, int G>
 fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int limit, bool accumulate, cudaStream_t st) {
   const int rounds = accumulate ? p.tiles : 1;
@@ -1126,6 +1186,7 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int li
   a.items = static_cast<int>(items);
   a.pcols = p.pcols;
   a.shared_unit = p.shared_unit;
+  const unsigned grid = static_cast<unsigned>(p.shared_unit ? units : (units + kWarps - 1) / kWarps);
   for (int r = 0; r < rounds; r++) {
     a.tile0 = r;
     fg_status rc = FG_OK;
@@ -1134,20 +1195,17 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int li
         static bool done[2][64] = {{false}};
         const auto kernel = accumulate ? paged_attn_one_kernel<D, G, true> : paged_attn_one_kernel<D, G, false>;
         if ((rc = set_smem(kernel, One<D, G>::SMEM, done[accumulate])) != FG_OK) return rc;
-        const unsigned grid = static_cast<unsigned>(p.shared_unit ? units : (units + kWarps - 1) / kWarps);
         kernel<<<grid, kWarps * 32, One<D, G>::SMEM, st>>>(a);
       }
     }
-    if (!p.one) {
-      static bool done[64] = {false};
-      if ((rc = set_smem(paged_attn_kernel<D, G>, Shape<D, G>::SMEM, done)) != FG_OK) return rc;
-      paged_attn_kernel<D, G><<<static_cast<unsigned>(units), kWarps * 32, Shape<D, G>::SMEM, st>>>(a);
+    if (!p.one && p.pcols == kCols) rc = launch_tiles<D, G, 1>(a, grid, accumulate, st);
+    if constexpr (D <= 128) {
+      if (!p.one && p.pcols == 2 * kCols) rc = launch_tiles<D, G, 2>(a, grid, accumulate, st);
     }
-    if ((rc = fg_launch_check()) != FG_OK) return rc;
-    const bool weigh = accumulate && !(p.one && p.nsplit == 1);
-    if (p.nsplit == 1 && !weigh) continue;
-    const int left = cols - r * kCols, out_cols = p.nsplit == 1 ? 0 : left < kCols ? left : kCols;
-    const int blocks = weigh ? (limit + kJoinSlots - 1) / kJoinSlots : 0;
+    if (rc != FG_OK || (rc = fg_launch_check()) != FG_OK) return rc;
+    if (p.nsplit == 1) continue;
+    const int left = cols - r * p.pcols, out_cols = left < p.pcols ? left : p.pcols;
+    const int blocks = accumulate ? (limit + kJoinSlots - 1) / kJoinSlots : 0;
     if (out_cols + blocks > 65535) return FG_ERR_SHAPE;
     // a programmatic dependent: its blocks start while the last splits run and wait for them
     cudaLaunchConfig_t lc = {};
@@ -1201,7 +1259,7 @@ extern "C" fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q,
   const size_t have = workspace ? workspace_bytes : 0;
   while (p.total > have && !accumulate && p.nsplit > 1) {  // less scratch: fewer, longer splits
     p.nsplit = (p.nsplit + 1) / 2;
-    p.split = ((limit + p.nsplit - 1) / p.nsplit + kCta - 1) / kCta * kCta;
+    p.split = ((limit + p.nsplit - 1) / p.nsplit + kBlock - 1) / kBlock * kBlock;
     p.nsplit = (limit + p.split - 1) / p.split;
     plan_bytes(&p, pairs, kv->head_dim, limit, false);
   }
