@@ -40,6 +40,9 @@ constexpr int kWarps = 4;
 constexpr int kBlock = 32;              // slots per warp step
 constexpr int kCta = kWarps * kBlock;   // slots per CTA step
 constexpr int kCols = 8;                // columns per tile
+#ifndef FG_MIN_BLOCKS
+#define FG_MIN_BLOCKS 4
+#endif
 #ifndef FG_CTAS
 #define FG_CTAS 3
 #endif
@@ -56,6 +59,10 @@ constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves: c * 2^-20
 constexpr uint32_t kByte = 0x00FF00FFu;   // both nibbles of the low byte: (lo + 16 hi) * 2^-24
 constexpr uint32_t kOnes = 0x3C003C00u;   // fp16 {1, 1}
 
+struct Part {  // a unit's part of a cut item: the units that have it, the part's slots
+  int item, u0, u1, t0, t1;
+};
+
 struct PagedAttnArgs {
   PagedArgs kv;
   const __half *q;
@@ -63,19 +70,22 @@ struct PagedAttnArgs {
   __half *out;
   int64_t ldo;
   int R, rows_per_seq, limit;
-  int tile0, tiles;    // column tiles of this launch: tile0 .. tile0 + tiles - 1
-  int split, nsplit;   // slots per split (a multiple of kCta), splits
-  int pcols;           // columns per item in ml, po and scores: 1 (single-column launches) or 8
-  int items;
-  bool shared_unit;    // the CTA's warps share a unit (one split of one item), or have one each
+  int tile0, tiles;  // column tiles of this launch: tile0 .. tile0 + tiles - 1
+  int pcols;         // columns per item: 1 (single-column launches), 8 or 16
+  int items, seqs;
+  int units;         // partitioned launches: warps that share the blocks of all items; else 0
+  bool shared_unit;  // otherwise: the CTA's warps share an item, or have one each
   const int32_t *positions, *counts;
-  float2 *ml;          // [items][nsplit][pcols]: running maximum (log2 units) and sum; sum < 0: a bad page
-  float *po;           // [items][nsplit][pcols][D] unnormalised outputs (nsplit > 1)
-  float *scores;       // [items][pcols][score_ld] (accumulate)
+  // partitioned launches: per unit two parts of cut items (Walk)
+  float2 *ml;        // [units][2][pcols]: running maximum (log2 units) and sum; sum < 0: a bad page
+  float *po;         // [units][2][pcols][D] unnormalised outputs
+  Part *parts;       // [units][2] (accumulate)
+  int2 *cut;         // [items]: first and last unit of a cut item; first < 0: whole in one unit
+  float *scores;     // [items][pcols][score_ld] (accumulate)
   int64_t score_ld;
 };
 
-// One (sequence, key-value head, column tile): items are numbered tile-fastest.
+// One (sequence, key-value head, column tile); ht = head * tiles + tile, item = s * heads * tiles + ht.
 struct Item {
   int s, h, n0, ncols;  // columns n0 .. n0 + ncols - 1 of the head (column n: row n / R, query head n % R)
   int pos, live;        // first new slot; rows of the sequence that see anything
@@ -85,11 +95,11 @@ struct Item {
   }
 };
 
-__device__ __forceinline__ Item load_item(const PagedAttnArgs &a, int item, bool flag) {
+__device__ __forceinline__ Item load_item(const PagedAttnArgs &a, int s, int ht, bool flag) {
   Item it;
-  const int sh = item / a.tiles, tile = a.tile0 + item % a.tiles;
-  it.s = sh / a.kv.H;
-  it.h = sh % a.kv.H;
+  const int tile = a.tile0 + ht % a.tiles;
+  it.s = s;
+  it.h = ht / a.tiles;
   it.n0 = tile * a.pcols;
   it.ncols = min(a.pcols, a.rows_per_seq * a.R - it.n0);
   const int pos = a.positions[it.s], count = a.counts ? a.counts[it.s] : a.rows_per_seq;
@@ -99,6 +109,121 @@ __device__ __forceinline__ Item load_item(const PagedAttnArgs &a, int item, bool
   it.pos = pos;
   it.live = range || pos < 0 ? 0 : count;
   return it;
+}
+
+// Blocks of 32 slots that a sequence's rows see together.
+__device__ __forceinline__ int seq_blocks(const PagedAttnArgs &a, int s) {
+  const int pos = a.positions[s], count = a.counts ? a.counts[s] : a.rows_per_seq;
+  const bool on = pos >= 0 && count > 0 && count <= a.rows_per_seq && static_cast<int64_t>(pos) + count <= a.limit;
+  return on ? (pos + count + kBlock - 1) / kBlock : 0;
+}
+
+// A warp's way through its share of the work.  Partitioned launches lay the blocks of all items in
+// a row (sequence, then head and tile, then block) and cut it into `units` equal runs, at most one
+// for every kMinBlocks blocks: a run is up to two parts of cut items, the first and the last, with
+// whole items in between.  A part is number 2 * unit + 1 if it begins its item, else 2 * unit.
+constexpr int kMinBlocks = FG_MIN_BLOCKS;
+
+struct Walk {
+  int s, ht, b, nblk;      // at block b of head and tile ht of sequence s, which has nblk blocks
+  int64_t g, end, total;   // place in the row of all blocks
+  int units;
+
+  __device__ __forceinline__ bool begin(const PagedAttnArgs &a, int unit, int lane) {
+    const int HT = a.kv.H * a.tiles;
+    if (!a.units) {
+      if (unit >= a.items) return false;
+      s = unit / HT;
+      ht = unit - s * HT;
+      b = 0;
+      return true;
+    }
+    int64_t sum = 0;
+    for (int i = lane; i < a.seqs; i += 32) sum += seq_blocks(a, i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    total = sum * HT;
+    const int64_t most = (total + kMinBlocks - 1) / kMinBlocks;
+    units = static_cast<int>(most < a.units ? most : a.units);
+    if (unit >= units) return false;
+    g = unit * total / units;
+    end = (unit + 1) * total / units;
+    nblk = 0;
+    int64_t base = 0;  // blocks of one head and tile before the chunk of 32 sequences
+    for (int i = 0; i < a.seqs; i += 32) {
+      const uint32_t n = i + lane < a.seqs ? seq_blocks(a, i + lane) : 0u;
+      uint32_t incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t after = __ballot_sync(0xffffffffu, (base + incl) * HT > g);
+      if (after) {  // the first sequence that ends behind g
+        const int l = __ffs(after) - 1;
+        nblk = __shfl_sync(0xffffffffu, n, l);
+        base += __shfl_sync(0xffffffffu, incl, l) - nblk;
+        s = i + l;
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (nblk == 0) return false;
+    const int64_t rest = g - base * HT;
+    ht = static_cast<int>(rest / nblk);
+    b = static_cast<int>(rest - static_cast<int64_t>(ht) * nblk);
+    return true;
+  }
+  __device__ __forceinline__ int run() const {  // blocks of the segment at b
+    const int64_t left = end - g;
+    return left < nblk - b ? static_cast<int>(left) : nblk - b;
+  }
+  __device__ __forceinline__ bool next(const PagedAttnArgs &a, int ran) {
+    g += ran;
+    if (g >= end) return false;
+    b = 0;
+    if (++ht == a.kv.H * a.tiles) {
+      ht = 0;
+      do {
+        if (++s >= a.seqs) return false;  // (not with blocks left)
+        nblk = seq_blocks(a, s);
+      } while (nblk == 0);
+    }
+    return true;
+  }
+  __device__ __forceinline__ int unit_of(int64_t block) const {
+    return static_cast<int>(((block + 1) * units - 1) / total);
+  }
+};
+
+__device__ __forceinline__ void flag_bad_sequences(const PagedAttnArgs &a, int lane) {
+  bool range = false;
+  for (int i = lane; i < a.seqs; i += 32) {
+    const int pos = a.positions[i], count = a.counts ? a.counts[i] : a.rows_per_seq;
+    range |= pos < -1 || count < 0 || count > a.rows_per_seq ||
+             (pos >= 0 && static_cast<int64_t>(pos) + count > a.limit);
+  }
+  if (range) atomicOr(a.kv.err, FG_DEVERR_RANGE);
+}
+
+// What a segment's outputs are: an item's whole rows, or part `index` of a cut item.
+struct Target {
+  bool whole;
+  int64_t index;
+};
+
+__device__ __forceinline__ Target target_of(const PagedAttnArgs &a, const Walk &w, int unit, int item, int ran,
+                                            bool leader) {
+  Target t;
+  t.whole = !a.units || ran == w.nblk;
+  t.index = 2 * static_cast<int64_t>(unit) + (w.b == 0);
+  if (a.units && leader) {
+    const int64_t g0 = w.g - w.b, g1 = g0 + w.nblk;
+    if (w.b == 0) a.cut[item] = t.whole ? make_int2(-1, -1) : make_int2(unit, w.unit_of(g1 - 1));
+    if (a.scores && !t.whole)
+      a.parts[t.index] = Part{item, w.unit_of(g0), w.unit_of(g1 - 1), w.b * kBlock, (w.b + ran) * kBlock};
+  }
+  return t;
 }
 
 template <int D, int G, int NT>  // NT: column tiles of 8 per unit
@@ -111,7 +236,7 @@ struct Shape {
   static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
   static constexpr int WARP_B = 2 * STAGE_B > NT * kCols * D * 4 ? 2 * STAGE_B : NT * kCols * D * 4;
   static constexpr int SMEM = kWarps * WARP_B;  // two stages a warp; at the end its outputs
-  static constexpr int kCtas = NT == 1 ? FG_CTAS : 2;
+  static constexpr int kCtas = NT == 1 && D <= 128 ? FG_CTAS : 2;
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -272,25 +397,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   griddep_launch();  // the join may be scheduled once every CTA runs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, c = lane & 3;
-  const uint32_t unit = a.shared_unit ? blockIdx.x : blockIdx.x * kWarps + warp;
-  if (!a.shared_unit && unit >= static_cast<uint32_t>(a.items) * a.nsplit) return;
-  const int item = unit / a.nsplit, sp = unit - item * a.nsplit;
+  const int unit = a.shared_unit ? blockIdx.x : blockIdx.x * kWarps + warp;
   const int first = a.shared_unit ? warp : 0;
   const int step = a.shared_unit ? kCta : kBlock;  // slots from one of this warp's blocks to the next
-  const Item it = load_item(a, item, sp == 0 && first == 0 && lane == 0);
-  // live columns' lengths: rows ascend with the column, so the last live one sees most
-  int lmin = 0, lmax = 0;
-  {
-    const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
-    if (last >= it.n0) {
-      lmin = it.len(it.n0, a.R);
-      lmax = it.len(last, a.R);
-    }
-  }
-  const int t_begin = sp * a.split, t_end = min(lmax, t_begin + a.split);
-  if (t_begin >= t_end && (sp > 0 || a.nsplit > 1)) return;  // (the join zeroes rows that see nothing)
-  const int t_first = t_begin + first * kBlock;
-  const int steps = t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
+  if (TRACK && a.units && lane < 2 && unit < a.units) a.parts[2 * unit + lane].item = -1;
+  if (a.units && unit == 0) flag_bad_sequences(a, lane);
+  Walk walk;
+  if (!walk.begin(a, unit, lane)) return;
 
   const uint32_t bar0 = smem_u32(&full_bar[warp][0]);
   if (lane == 0) {
@@ -305,10 +418,31 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   } else {
     __syncwarp();
   }
-
   uint8_t *const wbase = smem + warp * S::WARP_B;
   Copies<RB, NG, S::CODE_B, S::META_B> cp;
   cp.init(a, smem_u32(wbase), lane);
+  bool ok = true;
+  uint32_t phase = 0;  // bit i: the next phase of stage i
+
+  while (true) {  // segments
+  const int ht = walk.ht, item = walk.s * a.kv.H * a.tiles + ht;
+  const Item it = load_item(a, walk.s, ht, !a.units && first == 0 && lane == 0);
+  // live columns' lengths: rows ascend with the column, so the last live one sees most
+  int lmin = 0, lmax = 0;
+  {
+    const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
+    if (last >= it.n0) {
+      lmin = it.len(it.n0, a.R);
+      lmax = it.len(last, a.R);
+    }
+  }
+  const int ran = a.units ? walk.run() : 0;
+  const Target target = target_of(a, walk, unit, item, ran, lane == 0);
+  const int t_begin = a.units ? walk.b * kBlock : 0;
+  const int t_end = a.units ? min(lmax, t_begin + ran * kBlock) : lmax;
+  const int t_first = t_begin + first * kBlock;
+  const int steps = ok && t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
+  cp.bad = false;
   if (steps > 0) {
     cp.look_up(a, it.s, it.h, t_first, step, t_end, lane);
     cp.issue(0, 0, bar0, lane);
@@ -546,17 +680,17 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     }
   };
 
-  bool ok = true;
   int t = t_first;
   // one step: wait for stage ST, its block, and the copy of the block two steps on
-  auto run = [&](auto stage, int k, uint32_t parity) -> bool {
+  auto run = [&](auto stage, int k) -> bool {
     constexpr int ST = decltype(stage)::value;
-    if (!mbar_wait_bounded(bar0 + 8 * ST, parity, nullptr, a.kv.err)) {
+    if (!mbar_wait_bounded(bar0 + 8 * ST, phase >> ST & 1, nullptr, a.kv.err)) {
       // gave up: the copy in flight lands (or times out) before the stages are written again
-      if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), ST ? parity ^ 1 : parity, nullptr, a.kv.err);
+      if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), phase >> (ST ^ 1) & 1, nullptr, a.kv.err);
       ok = false;
       return false;
     }
+    phase ^= 1u << ST;
     if (t + kBlock > min(lmin, t_end)) block(stage, std::true_type{}, t);
     else block(stage, std::false_type{}, t);
     if (k + 2 < steps) {
@@ -568,10 +702,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     t += step;
     return true;
   };
-  uint32_t parity = 0;
-  for (int k = 0; k < steps; k += 2, parity ^= 1) {
-    if (!run(std::integral_constant<int, 0>{}, k, parity)) break;
-    if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1, parity)) break;
+  for (int k = 0; k < steps; k += 2) {
+    if (!run(std::integral_constant<int, 0>{}, k)) break;
+    if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1)) break;
   }
   const bool any_bad = __any_sync(0xffffffffu, cp.bad);
   if (any_bad && lane == 0) {
@@ -633,8 +766,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
       den += f * red_l[w][n];
       if (f != 0.f) o = make_float4(o.x + f * v.x, o.y + f * v.y, o.z + f * v.z, o.w + f * v.w);
     }
-    const int64_t pi = (static_cast<int64_t>(item) * a.nsplit + sp) * NC + n;
-    if (a.nsplit > 1) {
+    const int64_t pi = target.index * NC + n;
+    if (!target.whole) {
       if (d == 0) a.ml[pi] = make_float2(M, good ? den : -1.f);
       *reinterpret_cast<float4 *>(a.po + pi * D + d) = o;
     } else {
@@ -646,7 +779,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
                                  (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + d) = r;
     }
   }
-  if (TRACK && a.nsplit == 1 && good) {  // the unit saw whole rows: its slots' weights
+  if (TRACK && target.whole && good) {  // the unit saw whole rows: its slots' weights
     for (int i = 4 * me; i < lmax; i += 4 * all) {
       float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int n = 0; n < it.ncols; n++) {
@@ -658,6 +791,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
       }
       grow4(a, it.s, it.h, i, lmax, add);
     }
+  }
+  if (!a.units || !walk.next(a, ran)) return;
+  fence_proxy_async_smem();  // the stages' last reads and writes come before the next segment's copies
+  __syncwarp();
   }
 }
 
@@ -701,20 +838,13 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   griddep_launch();  // the join may be scheduled once every CTA runs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, c = lane & 3;
-  const uint32_t unit = a.shared_unit ? blockIdx.x : blockIdx.x * kWarps + warp;
-  if (!a.shared_unit && unit >= static_cast<uint32_t>(a.items) * a.nsplit) return;
-  const int item = unit / a.nsplit, sp = unit - item * a.nsplit;
+  const int unit = a.shared_unit ? blockIdx.x : blockIdx.x * kWarps + warp;
   const int first = a.shared_unit ? warp : 0;
   const int step = a.shared_unit ? kCta : kBlock;  // slots from one of this warp's blocks to the next
-  const int s = item / a.kv.H, h = item - s * a.kv.H;
-  const int pos = a.positions[s], count = a.counts ? a.counts[s] : 1;
-  const bool range = pos < -1 || count < 0 || count > 1 || (pos >= 0 && static_cast<int64_t>(pos) + count > a.limit);
-  if (range && sp == 0 && first == 0 && lane == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
-  const int len = range || pos < 0 || count < 1 ? 0 : pos + 1;
-  const int t_begin = sp * a.split, t_end = min(len, t_begin + a.split);
-  if (t_begin >= t_end && (sp > 0 || a.nsplit > 1)) return;  // (the join zeroes rows that see nothing)
-  const int t_first = t_begin + first * kBlock;
-  const int steps = t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
+  if (TRACK && a.units && lane < 2 && unit < a.units) a.parts[2 * unit + lane].item = -1;
+  if (a.units && unit == 0) flag_bad_sequences(a, lane);
+  Walk walk;
+  if (!walk.begin(a, unit, lane)) return;
 
   const uint32_t bar0 = smem_u32(&full_bar[warp][0]);
   if (lane == 0) {
@@ -729,10 +859,22 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   } else {
     __syncwarp();
   }
-
   uint8_t *const wbase = smem + warp * S::WARP_B;
   Copies<RB, NG, S::CODE_B, S::META_B> cp;
   cp.init(a, smem_u32(wbase), lane);
+  bool ok = true;
+  uint32_t phase = 0;  // bit i: the next phase of stage i
+
+  while (true) {  // segments
+  const int s = walk.s, h = walk.ht, item = s * a.kv.H + h;
+  const int len = load_item(a, s, h, !a.units && first == 0 && lane == 0).len(0, 1);
+  const int ran = a.units ? walk.run() : 0;
+  const Target target = target_of(a, walk, unit, item, ran, lane == 0);
+  const int t_begin = a.units ? walk.b * kBlock : 0;
+  const int t_end = a.units ? min(len, t_begin + ran * kBlock) : len;
+  const int t_first = t_begin + first * kBlock;
+  const int steps = ok && t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
+  cp.bad = false;
   if (steps > 0) {
     cp.look_up(a, s, h, t_first, step, t_end, lane);
     cp.issue(0, 0, bar0, lane);
@@ -881,17 +1023,17 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     }
   };
 
-  bool ok = true;
   int t = t_first;
   // one step: wait for stage ST, its block, and the copy of the block two steps on
-  auto run = [&](auto stage, int k, uint32_t parity) -> bool {
+  auto run = [&](auto stage, int k) -> bool {
     constexpr int ST = decltype(stage)::value;
-    if (!mbar_wait_bounded(bar0 + 8 * ST, parity, nullptr, a.kv.err)) {
+    if (!mbar_wait_bounded(bar0 + 8 * ST, phase >> ST & 1, nullptr, a.kv.err)) {
       // gave up: the copy in flight lands (or times out) before the stages are written again
-      if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), ST ? parity ^ 1 : parity, nullptr, a.kv.err);
+      if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), phase >> (ST ^ 1) & 1, nullptr, a.kv.err);
       ok = false;
       return false;
     }
+    phase ^= 1u << ST;
     if (t + kBlock > t_end) block(stage, std::true_type{}, t);
     else block(stage, std::false_type{}, t);
     if (k + 2 < steps) {
@@ -903,10 +1045,9 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     t += step;
     return true;
   };
-  uint32_t parity = 0;
-  for (int k = 0; k < steps; k += 2, parity ^= 1) {
-    if (!run(std::integral_constant<int, 0>{}, k, parity)) break;
-    if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1, parity)) break;
+  for (int k = 0; k < steps; k += 2) {
+    if (!run(std::integral_constant<int, 0>{}, k)) break;
+    if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1)) break;
   }
   const bool any_bad = __any_sync(0xffffffffu, cp.bad);
   if (any_bad && lane == 0) {
@@ -936,18 +1077,18 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
       if (NG == 1 || c == cg) o4[i % (CH / NG)][x] = v[x] + vacc;
     }
   }
-  const int64_t pi = static_cast<int64_t>(item) * a.nsplit + sp;
+  const int64_t pi = target.index;
   __half *const orow = a.out + static_cast<int64_t>(s) * a.ldo + static_cast<int64_t>(h) * D;
   if (!a.shared_unit) {
     const bool good = ok && !any_bad;
-    if (a.ml && lane == 0) a.ml[pi] = make_float2(m, good ? l : -1.f);
+    if (!target.whole && lane == 0) a.ml[pi] = make_float2(m, good ? l : -1.f);
     const float inv = 1.0f / l;
     const bool on = len > 0 && good;
     if (c < NG) {
 #pragma unroll
       for (int i = 0; i < CH / NG; i++) {
         const int d = (c * (CH / NG) + i) * 32 + 4 * gid;
-        if (a.nsplit > 1) {
+        if (!target.whole) {
           *reinterpret_cast<float4 *>(a.po + pi * D + d) = make_float4(o4[i][0], o4[i][1], o4[i][2], o4[i][3]);
         } else {
           uint2 r = make_uint2(0u, 0u);
@@ -956,11 +1097,14 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
         }
       }
     }
-    if (TRACK && a.nsplit == 1 && on) {  // this warp saw the whole row: its slots' weights
+    if (TRACK && target.whole && on) {  // this warp saw the whole row: its slots' weights
       __syncwarp();
       grow_row(a, s, h, srow, t_end, m, inv, lane, 32);
     }
-    return;
+    if (!a.units || !walk.next(a, ran)) return;
+    fence_proxy_async_smem();  // the stages' last reads come before the next segment's copies
+    __syncwarp();
+    continue;
   }
   float *wo = reinterpret_cast<float *>(wbase);
   if (c < NG)
@@ -983,7 +1127,6 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   }
   const float inv = 1.0f / den;
   const bool on = len > 0 && good;
-  if (a.ml && tid == 0) a.ml[pi] = make_float2(M, good ? den : -1.f);
   for (int d = 2 * tid; d < D; d += 2 * kWarps * 32) {
     float o0 = 0.f, o1 = 0.f;
 #pragma unroll
@@ -993,24 +1136,22 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
         o0 += f[w] * v.x;
         o1 += f[w] * v.y;
       }
-    if (a.nsplit > 1) {
-      *reinterpret_cast<float2 *>(a.po + pi * D + d) = make_float2(o0, o1);
-    } else {
-      *reinterpret_cast<__half2 *>(orow + d) = on ? __floats2half2_rn(o0 * inv, o1 * inv) : __floats2half2_rn(0.f, 0.f);
-    }
+    *reinterpret_cast<__half2 *>(orow + d) = on ? __floats2half2_rn(o0 * inv, o1 * inv) : __floats2half2_rn(0.f, 0.f);
   }
-  if (TRACK && a.nsplit == 1 && on)  // (the CTA's scores were published by the barrier above)
+  if (TRACK && on)  // (the CTA's scores were published by the barrier above)
     grow_row(a, s, h, srow, t_end, M, inv, tid, kWarps * 32);
+  return;
+  }
 }
 
-// Column n of an item over its splits, by one warp: maximum and sum; sum 0: nothing seen, or a bad
-// page.
-__device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, const float2 *ml, int n, int used) {
+// Column n of a cut item over the parts that units u0 .. u1 have of it (the first one's begins the
+// item), by one warp: maximum and sum; sum 0: nothing seen, or a bad page.
+__device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, int n, int u0, int u1) {
   const int lane = threadIdx.x & 31;
   float M = -INFINITY, den = 0.f;
   bool bad = false;
-  for (int j = lane; j < used; j += 32) {
-    const float2 v = ml[j * a.pcols + n];
+  for (int u = u0 + lane; u <= u1; u += 32) {
+    const float2 v = a.ml[(2 * static_cast<int64_t>(u) + (u == u0)) * a.pcols + n];
     bad |= v.y < 0.f;
     const float mx = fmaxf(M, v.x);
     if (v.x != -INFINITY) den = (M == -INFINITY ? 0.f : den * exp2f(M - mx)) + v.y * exp2f(v.x - mx);
@@ -1027,39 +1168,35 @@ __device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, const float2 *
 
 constexpr int kJoinWarps = 8;
 constexpr int kMaxCols = 16;  // columns per item: at most two tiles
-constexpr int kJoinSlots = kJoinWarps * 32 * 4;  // slots of a block that grows weights
 
-// blockIdx.x: item; blockIdx.y < out_cols: that column's splits joined into its output row, every
-// kJoinWarps-th split by a warp; beyond: kJoinSlots slots whose weights grow by the columns'
-// probabilities.
+// The first items * out_cols blocks: a column of an item that was cut, its parts joined into its
+// output row, every kJoinWarps-th by a warp (and zeros for items without blocks, which no unit
+// meets).  Behind them (accumulate) a block per unit: the weights of its parts' slots.
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnArgs a, int out_cols) {
   constexpr int V = D / 32;  // dims per lane
   __shared__ float2 col[kMaxCols];
   __shared__ float part[kJoinWarps][D];
-  const int item = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Item it = load_item(a, item, false);
-  int lmax = 0;
-  const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
-  if (last >= it.n0) lmax = it.len(last, a.R);
-  const int used = (lmax + a.split - 1) / a.split;
-  const float2 *ml = a.ml + static_cast<int64_t>(item) * a.nsplit * a.pcols;
-  griddep_wait();
-  if (static_cast<int>(blockIdx.y) < out_cols) {
-    const int n = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, HT = a.kv.H * a.tiles;
+  if (blockIdx.x < static_cast<unsigned>(a.items) * out_cols) {
+    const int item = blockIdx.x / out_cols, n = blockIdx.x - item * out_cols;
+    const Item it = load_item(a, item / HT, item % HT, false);
     if (n >= it.ncols) return;
+    griddep_wait();
+    const int2 c = it.live ? a.cut[item] : make_int2(0, 0);
+    if (c.x < 0) return;
     const int cn = it.n0 + n;
-    const float2 t = it.len(cn, a.R) > 0 ? join_ml(a, ml, n, used) : make_float2(0.f, 0.f);
+    const float2 t = it.len(cn, a.R) > 0 ? join_ml(a, n, c.x, c.y) : make_float2(0.f, 0.f);
     float o[V];
 #pragma unroll
     for (int e = 0; e < V; e++) o[e] = 0.f;
     if (t.y != 0.f) {
-      const float *po = a.po + (static_cast<int64_t>(item) * a.nsplit * a.pcols + n) * D + lane * V;
 #pragma unroll 4
-      for (int j = warp; j < used; j += kJoinWarps) {
-        const float x = ml[j * a.pcols + n].x;
+      for (int u = c.x + warp; u <= c.y; u += kJoinWarps) {
+        const int64_t pi = (2 * static_cast<int64_t>(u) + (u == c.x)) * a.pcols + n;
+        const float x = a.ml[pi].x;
         const float f = x == -INFINITY ? 0.f : exp2f(x - t.x);
-        const float *p = po + static_cast<int64_t>(j) * a.pcols * D;
+        const float *p = a.po + pi * D + lane * V;
         float v[V];
         if constexpr (V == 2) {
           *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
@@ -1084,70 +1221,70 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     }
     return;
   }
-  const int t0 = (blockIdx.y - out_cols) * kJoinSlots;
-  if (t0 >= lmax) return;
-  for (int n = warp; n < it.ncols; n += kJoinWarps) {
-    const float2 v = it.len(it.n0 + n, a.R) > 0 ? join_ml(a, ml, n, used) : make_float2(0.f, 0.f);
-    if (lane == 0) col[n] = make_float2(v.x, v.y != 0.f ? 1.0f / v.y : 0.f);
+  const int unit = blockIdx.x - a.items * out_cols;
+  griddep_wait();
+  for (int k = 0; k < 2; k++) {
+    const Part p = a.parts[2 * unit + k];
+    if (p.item < 0) continue;
+    const Item it = load_item(a, p.item / HT, p.item % HT, false);
+    __syncthreads();
+    for (int n = warp; n < it.ncols; n += kJoinWarps) {
+      const float2 v = it.len(it.n0 + n, a.R) > 0 ? join_ml(a, n, p.u0, p.u1) : make_float2(0.f, 0.f);
+      if (lane == 0) col[n] = make_float2(v.x, v.y != 0.f ? 1.0f / v.y : 0.f);
+    }
+    __syncthreads();
+    const float *sc = a.scores + static_cast<int64_t>(p.item) * a.pcols * a.score_ld;
+    const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
+    const int end = min(p.t1, last >= it.n0 ? it.len(last, a.R) : 0);
+    for (int t = p.t0 + 4 * tid; t < end; t += 4 * kJoinWarps * 32) {
+      float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int n = 0; n < it.ncols; n++) {
+        const float2 c = col[n];
+        if (c.y != 0.f) grow_by(&add, sc + n * a.score_ld, t, it.len(it.n0 + n, a.R), c.x, c.y);
+      }
+      grow4(a, it.s, it.h, t, end, add);
+    }
   }
-  __syncthreads();
-  const int t = t0 + tid * 4;
-  if (t >= lmax) return;
-  const float *sc = a.scores + static_cast<int64_t>(item) * a.pcols * a.score_ld;
-  float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int n = 0; n < it.ncols; n++) {
-    const int end = it.len(it.n0 + n, a.R);
-    const float2 c = col[n];
-    if (c.y == 0.f) continue;
-    grow_by(&add, sc + n * a.score_ld, t, end, c.x, c.y);
-  }
-  grow4(a, it.s, it.h, t, lmax, add);
 }
 
 struct Plan {
-  int tiles, split, nsplit, pcols;  // column tiles of pcols columns
+  int tiles, pcols;  // column tiles of pcols columns
+  int units;         // of a partitioned launch; 0: an item per warp or CTA
   bool one, shared_unit;
-  size_t ml, po, scores, total;  // bytes, each part 256-byte aligned
+  size_t ml, po, parts, cut, scores, total;  // bytes, each part 256-byte aligned
   int64_t score_ld;
 };
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-void plan_bytes(Plan *p, int64_t pairs, int D, int limit, bool accumulate) {
-  // accumulating launches take the column tiles one after the other, so that a slot's weight is
-  // grown by one CTA at a time and in a fixed order
-  const int64_t items = pairs * (accumulate ? 1 : p->tiles);
-  const bool parts = p->nsplit > 1;
+void plan_bytes(Plan *p, int64_t items, int D, int limit, bool accumulate) {
+  const size_t n = 2 * static_cast<size_t>(p->units);
   p->score_ld = (static_cast<int64_t>(limit) + 31) / 32 * 32;
-  p->ml = parts ? align256(static_cast<size_t>(items) * p->nsplit * p->pcols * sizeof(float2)) : 0;
-  p->po = parts ? align256(static_cast<size_t>(items) * p->nsplit * p->pcols * D * sizeof(float)) : 0;
+  p->ml = align256(n * p->pcols * sizeof(float2));
+  p->po = align256(n * p->pcols * D * sizeof(float));
+  p->parts = accumulate ? align256(n * sizeof(Part)) : 0;
+  p->cut = p->units ? align256(static_cast<size_t>(items) * sizeof(int2)) : 0;
   p->scores = accumulate ? align256(static_cast<size_t>(items) * p->pcols * p->score_ld * sizeof(float)) : 0;
-  p->total = p->ml + p->po + p->scores;
+  p->total = p->ml + p->po + p->parts + p->cut + p->scores;
 }
 
-#ifndef FG_PLAN_K
-#define FG_PLAN_K 2
+#ifndef FG_DIRECT
+#define FG_DIRECT 1024
 #endif
-#ifndef FG_PLAN_SHARED
-#define FG_PLAN_SHARED 4
-#endif
-// A warp takes a unit of its own once there are enough ...
-Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate) {
+// Accumulating launches take the column tiles one after the other, so that a slot's weight is grown
+// by one CTA at a time and in a fixed order.
+Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate, int64_t *items) {
   Plan p;
   p.one = cols == 1 && D / G <= 2;
   p.pcols = p.one ? 1 : cols > kCols && D <= 128 && FG_NT2 ? 2 * kCols : kCols;
   p.tiles = (cols + p.pcols - 1) / p.pcols;
-  const int per_sm = p.one ? (D <= 128 ? FG_ONE_CTAS : 3) : p.pcols > kCols ? 2 : FG_CTAS;
-  const int64_t items = pairs * (accumulate ? 1 : p.tiles);
-  const int64_t warps = static_cast<int64_t>(per_sm) * kWarps * fg_sm_count();
-  int64_t want = FG_PLAN_K * warps / (items > 0 ? items : 1);  // warps per item
-  const int64_t most = (limit + 255) / 256;
-  want = want > most ? most : want;
-  p.shared_unit = want > 1 && want <= FG_PLAN_SHARED;
-  const int64_t n = want <= FG_PLAN_SHARED ? 1 : want;
-  p.split = static_cast<int>(((limit + n - 1) / n + kBlock - 1) / kBlock * kBlock);
-  p.nsplit = (limit + p.split - 1) / p.split;
-  plan_bytes(&p, pairs, D, limit, accumulate);
+  const int per_sm = p.one ? (D <= 128 ? FG_ONE_CTAS : 3) : p.pcols > kCols || D > 128 ? 2 : FG_CTAS;
+  *items = pairs * (accumulate ? 1 : p.tiles);
+  const int warps = per_sm * kWarps * fg_sm_count();
+  const bool many = *items >= 4LL * warps;
+  p.units = limit <= FG_DIRECT || (many && limit <= 4096) ? 0 : warps;
+  p.shared_unit = !p.units && !many;
+  plan_bytes(&p, *items, D, limit, accumulate);
   return p;
 }
 
@@ -1178,15 +1315,11 @@ fg_status launch_tiles(const PagedAttnArgs &a, unsigned grid, bool accumulate, c
 }
 
 template <int D, int G>
-fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int limit, bool accumulate, cudaStream_t st) {
+fg_status launch(PagedAttnArgs a, const Plan &p, int cols, bool accumulate, cudaStream_t st) {
   const int rounds = accumulate ? p.tiles : 1;
-  a.tiles = accumulate ? 1 : p.tiles;
-  const int64_t items = pairs * a.tiles, units = items * p.nsplit;
-  if (units > INT32_MAX) return FG_ERR_SHAPE;
-  a.items = static_cast<int>(items);
-  a.pcols = p.pcols;
-  a.shared_unit = p.shared_unit;
-  const unsigned grid = static_cast<unsigned>(p.shared_unit ? units : (units + kWarps - 1) / kWarps);
+  const unsigned grid = p.units         ? p.units / kWarps
+                        : p.shared_unit ? a.items
+                                        : (static_cast<unsigned>(a.items) + kWarps - 1) / kWarps;
   for (int r = 0; r < rounds; r++) {
     a.tile0 = r;
     fg_status rc = FG_OK;
@@ -1203,13 +1336,11 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int64_t pairs, int cols, int li
       if (!p.one && p.pcols == 2 * kCols) rc = launch_tiles<D, G, 2>(a, grid, accumulate, st);
     }
     if (rc != FG_OK || (rc = fg_launch_check()) != FG_OK) return rc;
-    if (p.nsplit == 1) continue;
+    if (!p.units) continue;
     const int left = cols - r * p.pcols, out_cols = left < p.pcols ? left : p.pcols;
-    const int blocks = accumulate ? (limit + kJoinSlots - 1) / kJoinSlots : 0;
-    if (out_cols + blocks > 65535) return FG_ERR_SHAPE;
-    // a programmatic dependent: its blocks start while the last splits run and wait for them
+    // a programmatic dependent: its blocks start while the last units run and wait for them
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(static_cast<unsigned>(items), out_cols + blocks);
+    lc.gridDim = dim3(static_cast<unsigned>(a.items) * out_cols + (accumulate ? p.units : 0));
     lc.blockDim = dim3(kJoinWarps * 32);
     lc.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1232,8 +1363,9 @@ extern "C" size_t fg_paged_attention_workspace_bytes(const fg_paged_kv *kv, int 
     return 0;
   const int64_t cols = static_cast<int64_t>(num_q_heads / kv->num_heads) * rows_per_seq;
   if (cols > INT32_MAX) return 0;
+  int64_t items;
   return make_plan(static_cast<int64_t>(rows / rows_per_seq) * kv->num_heads, static_cast<int>(cols), kv->head_dim,
-                   fg_kv_group(kv->group), plan_limit(kv, max_len), accumulate != 0).total;
+                   fg_kv_group(kv->group), plan_limit(kv, max_len), accumulate != 0, &items).total;
 }
 
 extern "C" fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q, int64_t ldq, int num_q_heads,
@@ -1255,13 +1387,14 @@ extern "C" fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q,
   const int64_t cols = static_cast<int64_t>(num_q_heads / kv->num_heads) * rows_per_seq;
   if (pairs > INT32_MAX || cols > INT32_MAX) return FG_ERR_SHAPE;
   const int limit = plan_limit(kv, max_len);
-  Plan p = make_plan(pairs, static_cast<int>(cols), kv->head_dim, fg_kv_group(kv->group), limit, accumulate != 0);
+  int64_t items;
+  Plan p = make_plan(pairs, static_cast<int>(cols), kv->head_dim, fg_kv_group(kv->group), limit, accumulate != 0, &items);
+  if (items * p.pcols > INT32_MAX / 2) return FG_ERR_SHAPE;
   const size_t have = workspace ? workspace_bytes : 0;
-  while (p.total > have && !accumulate && p.nsplit > 1) {  // less scratch: fewer, longer splits
-    p.nsplit = (p.nsplit + 1) / 2;
-    p.split = ((limit + p.nsplit - 1) / p.nsplit + kBlock - 1) / kBlock * kBlock;
-    p.nsplit = (limit + p.split - 1) / p.split;
-    plan_bytes(&p, pairs, kv->head_dim, limit, false);
+  if (p.total > have && p.units) {  // less scratch: items stay whole, a CTA each
+    p.units = 0;
+    p.shared_unit = true;
+    plan_bytes(&p, items, kv->head_dim, limit, accumulate != 0);
   }
   if (p.total > have) return FG_ERR_WORKSPACE;
   PagedAttnArgs a;
@@ -1273,29 +1406,35 @@ extern "C" fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q,
   a.R = num_q_heads / kv->num_heads;
   a.rows_per_seq = rows_per_seq;
   a.limit = limit;
-  a.split = p.split;
-  a.nsplit = p.nsplit;
+  a.tiles = accumulate ? 1 : p.tiles;
+  a.tile0 = 0;
+  a.pcols = p.pcols;
+  a.items = static_cast<int>(items);
+  a.seqs = rows / rows_per_seq;
+  a.units = p.units;
+  a.shared_unit = p.shared_unit;
   a.positions = positions;
   a.counts = row_counts;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  a.ml = p.ml ? reinterpret_cast<float2 *>(ws) : nullptr;
-  a.po = p.po ? reinterpret_cast<float *>(ws + p.ml) : nullptr;
-  a.scores = p.scores ? reinterpret_cast<float *>(ws + p.ml + p.po) : nullptr;
+  a.ml = reinterpret_cast<float2 *>(ws);
+  a.po = reinterpret_cast<float *>(ws + p.ml);
+  a.parts = reinterpret_cast<Part *>(ws + p.ml + p.po);
+  a.cut = reinterpret_cast<int2 *>(ws + p.ml + p.po + p.parts);
+  a.scores = accumulate ? reinterpret_cast<float *>(ws + p.ml + p.po + p.parts + p.cut) : nullptr;
   a.score_ld = p.score_ld;
-  a.tile0 = 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int n = static_cast<int>(cols);
   const bool acc = accumulate != 0;
   if (fg_kv_group(kv->group) == 64) {
     switch (kv->head_dim) {
-      case 64: return launch<64, 64>(a, p, pairs, n, limit, acc, st);
-      case 128: return launch<128, 64>(a, p, pairs, n, limit, acc, st);
-      case 256: return launch<256, 64>(a, p, pairs, n, limit, acc, st);
+      case 64: return launch<64, 64>(a, p, n, acc, st);
+      case 128: return launch<128, 64>(a, p, n, acc, st);
+      case 256: return launch<256, 64>(a, p, n, acc, st);
     }
   } else {
     switch (kv->head_dim) {
-      case 128: return launch<128, 128>(a, p, pairs, n, limit, acc, st);
-      case 256: return launch<256, 128>(a, p, pairs, n, limit, acc, st);
+      case 128: return launch<128, 128>(a, p, n, acc, st);
+      case 256: return launch<256, 128>(a, p, n, acc, st);
     }
   }
   return FG_ERR_UNSUPPORTED;
