@@ -196,6 +196,18 @@ struct Walk {
   }
 };
 
+// A warp's walk (in shared memory) one segment on; the stages' last reads and writes come before the
+// next segment's copies.
+__device__ __forceinline__ bool advance(const PagedAttnArgs &a, Walk *shared, int lane) {
+  Walk w = *shared;
+  const bool more = w.next(a, w.run());
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) *shared = w;
+  __syncwarp();
+  return more;
+}
+
 __device__ __forceinline__ void flag_bad_sequences(const PagedAttnArgs &a, int lane) {
   bool range = false;
   for (int i = lane; i < a.seqs; i += 32) {
@@ -235,7 +247,7 @@ struct Shape {
   static constexpr int CODE_B = kBlock * RB, META_B = kBlock * NG * 2;
   static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
   static constexpr int WARP_B = 2 * STAGE_B > NT * kCols * D * 4 ? 2 * STAGE_B : NT * kCols * D * 4;
-  static constexpr int SMEM = kWarps * WARP_B;  // two stages a warp; at the end its outputs
+  static constexpr int SMEM = kWarps * WARP_B;  // a warp's two stages, at the end its outputs
   static constexpr int kCtas = NT == 1 && D <= 128 ? FG_CTAS : 2;
 };
 
@@ -374,13 +386,44 @@ __device__ __forceinline__ void grow_by(float4 *add, const float *scores, int t,
   add->w += t + 3 < end ? fast_exp2(v.w - m) * inv : 0.f;
 }
 
-// An item's weights, once its maximum and 1 / sum are known, by `n` threads of which this is number i.
-__device__ __forceinline__ void grow_row(const PagedAttnArgs &a, int s, int h, const float *scores, int end, float m,
-                                         float inv, int i, int n) {
-  for (int t = 4 * i; t < end; t += 4 * n) {
-    const float4 v = *reinterpret_cast<const float4 *>(scores + t);  // (behind `end`: anything, not used)
-    grow4(a, s, h, t, end, make_float4(fast_exp2(v.x - m) * inv, fast_exp2(v.y - m) * inv, fast_exp2(v.z - m) * inv,
-                                       fast_exp2(v.w - m) * inv));
+// The weights of a single-column item's slots begin .. end - 1, once its maximum and 1 / sum are
+// known, by `n` threads of which this is number i: four slots at a time, four times before any is written, so that the table's and the pools'
+// latencies are paid once for 16 slots.
+__device__ __forceinline__ void grow_row(const PagedAttnArgs &a, int s, int h, const float *scores, int begin, int end,
+                                         float m, float inv, int i, int n) {
+  constexpr int U = 4;
+  for (int t0 = begin + 4 * i; t0 < end; t0 += 4 * U * n) {
+    int64_t slot[U];
+    float4 v[U], w[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int t = t0 + 4 * u * n;
+      slot[u] = -1;
+      if (t < end) {
+        slot[u] = paged_slot(a.kv, s, h, t);
+        v[u] = *reinterpret_cast<const float4 *>(scores + t);  // (behind `end`: anything, not used)
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      if (slot[u] >= 0) w[u] = *reinterpret_cast<const float4 *>(a.kv.weights + slot[u]);
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int t = t0 + 4 * u * n;
+      if (slot[u] < 0) continue;
+      float *dst = a.kv.weights + slot[u];
+      w[u].x += fast_exp2(v[u].x - m) * inv;
+      w[u].y += fast_exp2(v[u].y - m) * inv;
+      w[u].z += fast_exp2(v[u].z - m) * inv;
+      w[u].w += fast_exp2(v[u].w - m) * inv;
+      if (t + 3 < end) {
+        *reinterpret_cast<float4 *>(dst) = w[u];
+      } else {  // the slots behind stay as they are
+        dst[0] = w[u].x;
+        if (t + 1 < end) dst[1] = w[u].y;
+        if (t + 2 < end) dst[2] = w[u].z;
+      }
+    }
   }
 }
 
@@ -402,8 +445,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   const int step = a.shared_unit ? kCta : kBlock;  // slots from one of this warp's blocks to the next
   if (TRACK && a.units && lane < 2 && unit < a.units) a.parts[2 * unit + lane].item = -1;
   if (a.units && unit == 0) flag_bad_sequences(a, lane);
-  Walk walk;
-  if (!walk.begin(a, unit, lane)) return;
+  __shared__ Walk walks[kWarps];  // (out of the registers: used once per segment)
+  {
+    Walk w;
+    if (!w.begin(a, unit, lane)) return;
+    if (lane == 0) walks[warp] = w;
+    __syncwarp();
+  }
 
   const uint32_t bar0 = smem_u32(&full_bar[warp][0]);
   if (lane == 0) {
@@ -422,9 +470,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   Copies<RB, NG, S::CODE_B, S::META_B> cp;
   cp.init(a, smem_u32(wbase), lane);
   bool ok = true;
-  uint32_t phase = 0;  // bit i: the next phase of stage i
+  uint32_t phase = 0;  // bit i: the parity of stage i's next phase
 
   while (true) {  // segments
+  const Walk walk = walks[warp];
   const int ht = walk.ht, item = walk.s * a.kv.H * a.tiles + ht;
   const Item it = load_item(a, walk.s, ht, !a.units && first == 0 && lane == 0);
   // live columns' lengths: rows ascend with the column, so the last live one sees most
@@ -792,9 +841,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
       grow4(a, it.s, it.h, i, lmax, add);
     }
   }
-  if (!a.units || !walk.next(a, ran)) return;
-  fence_proxy_async_smem();  // the stages' last reads and writes come before the next segment's copies
-  __syncwarp();
+  if (!a.units || !advance(a, &walks[warp], lane)) return;
   }
 }
 
@@ -843,8 +890,13 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   const int step = a.shared_unit ? kCta : kBlock;  // slots from one of this warp's blocks to the next
   if (TRACK && a.units && lane < 2 && unit < a.units) a.parts[2 * unit + lane].item = -1;
   if (a.units && unit == 0) flag_bad_sequences(a, lane);
-  Walk walk;
-  if (!walk.begin(a, unit, lane)) return;
+  __shared__ Walk walks[kWarps];  // (out of the registers: used once per segment)
+  {
+    Walk w;
+    if (!w.begin(a, unit, lane)) return;
+    if (lane == 0) walks[warp] = w;
+    __syncwarp();
+  }
 
   const uint32_t bar0 = smem_u32(&full_bar[warp][0]);
   if (lane == 0) {
@@ -863,9 +915,10 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   Copies<RB, NG, S::CODE_B, S::META_B> cp;
   cp.init(a, smem_u32(wbase), lane);
   bool ok = true;
-  uint32_t phase = 0;  // bit i: the next phase of stage i
+  uint32_t phase = 0;  // bit i: the parity of stage i's next phase
 
   while (true) {  // segments
+  const Walk walk = walks[warp];
   const int s = walk.s, h = walk.ht, item = s * a.kv.H + h;
   const int len = load_item(a, s, h, !a.units && first == 0 && lane == 0).len(0, 1);
   const int ran = a.units ? walk.run() : 0;
@@ -1099,11 +1152,9 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     }
     if (TRACK && target.whole && on) {  // this warp saw the whole row: its slots' weights
       __syncwarp();
-      grow_row(a, s, h, srow, t_end, m, inv, lane, 32);
+      grow_row(a, s, h, srow, 0, t_end, m, inv, lane, 32);
     }
-    if (!a.units || !walk.next(a, ran)) return;
-    fence_proxy_async_smem();  // the stages' last reads come before the next segment's copies
-    __syncwarp();
+    if (!a.units || !advance(a, &walks[warp], lane)) return;
     continue;
   }
   float *wo = reinterpret_cast<float *>(wbase);
@@ -1139,7 +1190,7 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     *reinterpret_cast<__half2 *>(orow + d) = on ? __floats2half2_rn(o0 * inv, o1 * inv) : __floats2half2_rn(0.f, 0.f);
   }
   if (TRACK && on)  // (the CTA's scores were published by the barrier above)
-    grow_row(a, s, h, srow, t_end, M, inv, tid, kWarps * 32);
+    grow_row(a, s, h, srow, 0, t_end, M, inv, tid, kWarps * 32);
   return;
   }
 }
@@ -1169,81 +1220,112 @@ __device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, int n, int u0,
 constexpr int kJoinWarps = 8;
 constexpr int kMaxCols = 16;  // columns per item: at most two tiles
 
-// The first items * out_cols blocks: a column of an item that was cut, its parts joined into its
-// output row, every kJoinWarps-th by a warp (and zeros for items without blocks, which no unit
-// meets).  Behind them (accumulate) a block per unit: the weights of its parts' slots.
+// One column's parts joined into its output row by `n` warps, of which this is number w: V dims a
+// lane.  M, inv: the column's maximum and 1 / sum.
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnArgs a, int out_cols) {
+__device__ __forceinline__ void join_parts(const PagedAttnArgs &a, int n, int u0, int u1, float M, int w, int warps,
+                                           float (&o)[D / 32]) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int e = 0; e < V; e++) o[e] = 0.f;
+#pragma unroll 4
+  for (int u = u0 + w; u <= u1; u += warps) {
+    const int64_t pi = (2 * static_cast<int64_t>(u) + (u == u0)) * a.pcols + n;
+    const float x = a.ml[pi].x;
+    const float f = x == -INFINITY ? 0.f : exp2f(x - M);
+    const float *p = a.po + pi * D + lane * V;
+    float v[V];
+    if constexpr (V == 2) {
+      *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(p + e);
+    }
+#pragma unroll
+    for (int e = 0; e < V; e++) o[e] += f == 0.f ? 0.f : f * v[e];
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void store_row(__half *dst, const float (&o)[V], float inv) {
+  uint32_t r[V / 2];
+#pragma unroll
+  for (int e = 0; e < V; e += 2) r[e / 2] = pack_h2(o[e] * inv, o[e + 1] * inv);
+  if constexpr (V == 2) *reinterpret_cast<uint32_t *>(dst) = r[0];
+  else if constexpr (V == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(r[0], r[1]);
+  else *reinterpret_cast<uint4 *>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// The first blocks: a column of an item to a warp, or (wide) to a block: a cut item's parts joined
+// into the column's output row, and zeros for items without blocks, which no unit meets.  Behind
+// them (accumulate) a block per unit: the weights of its parts' slots, half the block to a part.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnArgs a, int out_cols, int out_blocks,
+                                                                     bool wide) {
   constexpr int V = D / 32;  // dims per lane
-  __shared__ float2 col[kMaxCols];
+  __shared__ float2 col[2][kMaxCols];
   __shared__ float part[kJoinWarps][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, HT = a.kv.H * a.tiles;
-  if (blockIdx.x < static_cast<unsigned>(a.items) * out_cols) {
-    const int item = blockIdx.x / out_cols, n = blockIdx.x - item * out_cols;
+  if (static_cast<int>(blockIdx.x) < out_blocks) {
+    const int i = wide ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
+    if (i >= a.items * out_cols) return;
+    const int item = i / out_cols, n = i - item * out_cols;
     const Item it = load_item(a, item / HT, item % HT, false);
     if (n >= it.ncols) return;
+    const int cn = it.n0 + n;
     griddep_wait();
     const int2 c = it.live ? a.cut[item] : make_int2(0, 0);
     if (c.x < 0) return;
-    const int cn = it.n0 + n;
     const float2 t = it.len(cn, a.R) > 0 ? join_ml(a, n, c.x, c.y) : make_float2(0.f, 0.f);
+    const float inv = t.y != 0.f ? 1.0f / t.y : 0.f;
     float o[V];
 #pragma unroll
     for (int e = 0; e < V; e++) o[e] = 0.f;
-    if (t.y != 0.f) {
-#pragma unroll 4
-      for (int u = c.x + warp; u <= c.y; u += kJoinWarps) {
-        const int64_t pi = (2 * static_cast<int64_t>(u) + (u == c.x)) * a.pcols + n;
-        const float x = a.ml[pi].x;
-        const float f = x == -INFINITY ? 0.f : exp2f(x - t.x);
-        const float *p = a.po + pi * D + lane * V;
-        float v[V];
-        if constexpr (V == 2) {
-          *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
-        } else {
+    if (t.y != 0.f) join_parts<D>(a, n, c.x, c.y, t.x, wide ? warp : 0, wide ? kJoinWarps : 1, o);
+    __half *const dst = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
+                        (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D;
+    if (wide) {
 #pragma unroll
-          for (int e = 0; e < V; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(p + e);
-        }
+      for (int e = 0; e < V; e++) part[warp][lane * V + e] = o[e];
+      __syncthreads();
+      if (warp > 0) return;
+      for (int w = 1; w < kJoinWarps; w++)
 #pragma unroll
-        for (int e = 0; e < V; e++) o[e] += f == 0.f ? 0.f : f * v[e];
-      }
+        for (int e = 0; e < V; e++) o[e] += part[w][lane * V + e];
     }
-#pragma unroll
-    for (int e = 0; e < V; e++) part[warp][lane * V + e] = o[e];
-    __syncthreads();
-    if (tid < D) {
-      float sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kJoinWarps; w++) sum += part[w][tid];
-      __half *dst = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
-                    (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D;
-      dst[tid] = __float2half_rn(t.y != 0.f ? sum / t.y : 0.f);
-    }
+    store_row<V>(dst + lane * V, o, inv);
     return;
   }
-  const int unit = blockIdx.x - a.items * out_cols;
+  const int unit = blockIdx.x - out_blocks, k = warp / (kJoinWarps / 2);
   griddep_wait();
-  for (int k = 0; k < 2; k++) {
-    const Part p = a.parts[2 * unit + k];
-    if (p.item < 0) continue;
-    const Item it = load_item(a, p.item / HT, p.item % HT, false);
-    __syncthreads();
-    for (int n = warp; n < it.ncols; n += kJoinWarps) {
+  const Part p = a.parts[2 * unit + k];
+  const int i = tid & (kJoinWarps * 16 - 1), w = warp & (kJoinWarps / 2 - 1);
+  Item it;
+  it.ncols = 0;
+  if (p.item >= 0) {
+    it = load_item(a, p.item / HT, p.item % HT, false);
+    for (int n = w; n < it.ncols; n += kJoinWarps / 2) {
       const float2 v = it.len(it.n0 + n, a.R) > 0 ? join_ml(a, n, p.u0, p.u1) : make_float2(0.f, 0.f);
-      if (lane == 0) col[n] = make_float2(v.x, v.y != 0.f ? 1.0f / v.y : 0.f);
+      if (lane == 0) col[k][n] = make_float2(v.x, v.y != 0.f ? 1.0f / v.y : 0.f);
     }
-    __syncthreads();
-    const float *sc = a.scores + static_cast<int64_t>(p.item) * a.pcols * a.score_ld;
-    const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
-    const int end = min(p.t1, last >= it.n0 ? it.len(last, a.R) : 0);
-    for (int t = p.t0 + 4 * tid; t < end; t += 4 * kJoinWarps * 32) {
-      float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int n = 0; n < it.ncols; n++) {
-        const float2 c = col[n];
-        if (c.y != 0.f) grow_by(&add, sc + n * a.score_ld, t, it.len(it.n0 + n, a.R), c.x, c.y);
-      }
-      grow4(a, it.s, it.h, t, end, add);
+  }
+  __syncthreads();
+  if (p.item < 0) return;
+  const float *sc = a.scores + static_cast<int64_t>(p.item) * a.pcols * a.score_ld;
+  const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
+  const int end = min(p.t1, last >= it.n0 ? it.len(last, a.R) : 0);
+  if (a.pcols == 1) {
+    if (col[k][0].y != 0.f) grow_row(a, it.s, it.h, sc, p.t0, end, col[k][0].x, col[k][0].y, i, kJoinWarps * 16);
+    return;
+  }
+  for (int t = p.t0 + 4 * i; t < end; t += 4 * kJoinWarps * 16) {
+    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int n = 0; n < it.ncols; n++) {
+      const float2 c = col[k][n];
+      if (c.y != 0.f) grow_by(&add, sc + n * a.score_ld, t, it.len(it.n0 + n, a.R), c.x, c.y);
     }
+    grow4(a, it.s, it.h, t, end, add);
   }
 }
 
@@ -1268,6 +1350,9 @@ void plan_bytes(Plan *p, int64_t items, int D, int limit, bool accumulate) {
   p->total = p->ml + p->po + p->parts + p->cut + p->scores;
 }
 
+#ifndef FG_ENOUGH
+#define FG_ENOUGH 2LL
+#endif
 #ifndef FG_DIRECT
 #define FG_DIRECT 1024
 #endif
@@ -1282,7 +1367,7 @@ Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate
   *items = pairs * (accumulate ? 1 : p.tiles);
   const int warps = per_sm * kWarps * fg_sm_count();
   const bool many = *items >= 4LL * warps;
-  p.units = limit <= FG_DIRECT || (many && limit <= 4096) ? 0 : warps;
+  p.units = limit <= FG_DIRECT || (*items >= FG_ENOUGH * (warps / kWarps) && limit <= 4096) ? 0 : warps;
   p.shared_unit = !p.units && !many;
   plan_bytes(&p, *items, D, limit, accumulate);
   return p;
@@ -1340,7 +1425,10 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int cols, bool accumulate, cuda
     const int left = cols - r * p.pcols, out_cols = left < p.pcols ? left : p.pcols;
     // a programmatic dependent: its blocks start while the last units run and wait for them
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(static_cast<unsigned>(a.items) * out_cols + (accumulate ? p.units : 0));
+    // few columns have many parts each
+    const bool wide = a.items * out_cols <= 16 * fg_sm_count();
+    const int out_blocks = wide ? a.items * out_cols : (a.items * out_cols + kJoinWarps - 1) / kJoinWarps;
+    lc.gridDim = dim3(out_blocks + (accumulate ? p.units : 0));
     lc.blockDim = dim3(kJoinWarps * 32);
     lc.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1348,7 +1436,7 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int cols, bool accumulate, cuda
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    if ((rc = fg_cuda_check(cudaLaunchKernelEx(&lc, paged_join_kernel<D>, a, out_cols))) != FG_OK) return rc;
+    if ((rc = fg_cuda_check(cudaLaunchKernelEx(&lc, paged_join_kernel<D>, a, out_cols, out_blocks, wide))) != FG_OK) return rc;
     if ((rc = fg_launch_check()) != FG_OK) return rc;
   }
   return FG_OK;
