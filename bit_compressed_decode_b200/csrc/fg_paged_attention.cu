@@ -301,10 +301,10 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
 }
 
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  // volatile: stays between the wait for its stage and the fence before the stage's next copy
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 
 // A warp's copies of its blocks: what never changes for a lane, and the pool places of the next 32
@@ -427,6 +427,31 @@ __device__ __forceinline__ void grow_row(const PagedAttnArgs &a, int s, int h, c
   }
 }
 
+// The B operands of 8 dims of q (v), for the low and the high nibbles.  A high nibble counts 16 times
+// what a low one does in its place, so the low nibbles' q is taken 16 times (exact), unless a value
+// of the column is too large for that (`big`): then the high nibbles' q a 16th (what that loses of
+// tiny values is far below the rounding of the column's sums).  Sums of products with q then count
+// q_unit(big) each.
+__device__ __forceinline__ float q_unit(bool big) { return big ? 16777216.0f : 1048576.0f; }  // 2^24, 2^20
+
+__device__ __forceinline__ bool q_big(const uint4 &v) {  // some |q| >= 2048
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  return (m & 0xFFFFu) >= 0x6800u || (m >> 16) >= 0x6800u;
+}
+
+__device__ __forceinline__ void q_operands(uint32_t (&f)[4], const uint4 &v, bool big) {
+  f[0] = __byte_perm(v.x, v.z, 0x5410);  // dims 0, 4
+  f[1] = __byte_perm(v.y, v.w, 0x5410);  // dims 2, 6
+  f[2] = __byte_perm(v.x, v.z, 0x7632);  // dims 1, 5
+  f[3] = __byte_perm(v.y, v.w, 0x7632);  // dims 3, 7
+  const __half2 s = big ? __float2half2_rn(0.0625f) : __float2half2_rn(16.0f);
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    __half2 *h = reinterpret_cast<__half2 *>(&f[big ? 2 + i : i]);
+    *h = __hmul2(*h, s);
+  }
+}
+
 template <int D, int G, int NT, bool TRACK>
 __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_attn_kernel(const PagedAttnArgs a) {
   using S = Shape<D, G, NT>;
@@ -503,7 +528,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   // (bits 0-3 of w and of w >> 8): k slots (2c, 2c+1) = dims (2o, 2o+4), (2c+8, 2c+9) = (2o+2,
   // 2o+6); high-nibble MMA: the same + 1.
   uint32_t qf[NT][NG][KW][4];
-  float qsum[NT][2][NG];  // columns 2c, 2c+1: sum of q over the group, times log2(e)
+  float qsum[NT][2][NG];  // columns 2c, 2c+1: sum of q over the group, over the column's unit
+  float qunit[NT][2];     // the unit, times log2(e): what the scores below are multiplied with in the exponent
   int len[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
@@ -511,6 +537,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     const bool on = col < it.ncols && it.len(n, a.R) > 0;
     const __half *qrow = a.q + (static_cast<int64_t>(it.s) * a.rows_per_seq + n / a.R) * a.ldq +
                          (static_cast<int64_t>(it.h) * a.R + n % a.R) * D;
+    bool big = false;
+    if (on)
+#pragma unroll
+      for (int g = 0; g < NG; g++)
+#pragma unroll
+        for (int j = 0; j < KW; j++) big |= q_big(*reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j));
+    big = __ballot_sync(0xffffffffu, big) >> (4 * gid) & 15u;
+    const float unit_of_gid = q_unit(big) * kLog2e;
+    qunit[nt][0] = __shfl_sync(0xffffffffu, unit_of_gid, 8 * c);
+    qunit[nt][1] = __shfl_sync(0xffffffffu, unit_of_gid, 8 * c + 4);
 #pragma unroll
     for (int g = 0; g < NG; g++) {
       float sum = 0.f;
@@ -519,17 +555,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         uint4 v = make_uint4(0, 0, 0, 0);
         if (on) v = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
         const __half *e = reinterpret_cast<const __half *>(&v);
-        qf[nt][g][j][0] = __byte_perm(v.x, v.z, 0x5410);  // dims 0, 4
-        qf[nt][g][j][1] = __byte_perm(v.y, v.w, 0x5410);  // dims 2, 6
-        qf[nt][g][j][2] = __byte_perm(v.x, v.z, 0x7632);  // dims 1, 5
-        qf[nt][g][j][3] = __byte_perm(v.y, v.w, 0x7632);  // dims 3, 7
+        q_operands(qf[nt][g][j], v, big);
 #pragma unroll
         for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      qsum[nt][0][g] = __shfl_sync(0xffffffffu, sum, 8 * c) * kLog2e;
-      qsum[nt][1][g] = __shfl_sync(0xffffffffu, sum, 8 * c + 4) * kLog2e;
+      sum *= 1.0f / q_unit(big);
+      qsum[nt][0][g] = __shfl_sync(0xffffffffu, sum, 8 * c);
+      qsum[nt][1][g] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
     }
 #pragma unroll
     for (int e = 0; e < 2; e++) {
@@ -567,7 +601,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   auto block = [&](auto stage, auto edge, int t) {
     constexpr int OFF = decltype(stage)::value * S::STAGE_B;
     constexpr bool EDGE = decltype(edge)::value;
-    // ---- scores (log2 units) of slots t + 16u + gid + 8x, columns 2c + e ----
+    // ---- scores (over their column's unit) of slots t + 16u + gid + 8x, columns 2c + e ----
     float sc[NT][2][2][2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
@@ -576,7 +610,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         uint32_t k0[KW], k1[KW];
         load_words<KW>(kbase + OFF + 16 * u * RB + g * (G / 2), k0);
         load_words<KW>(kbase + OFF + (16 * u + 8) * RB + g * (G / 2), k1);
-        float lo[NT][4], hi[NT][4];
+        float lo[NT][4], hi[NT][4];  // two chains of MMAs: their latency bounds a warp
 #pragma unroll
         for (int j = 0; j < KW; j++) {
           const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
@@ -596,13 +630,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
 #pragma unroll
         for (int x = 0; x < 2; x++) {
           const __half *n = nbase + OFF / 2 + (16 * u + 8 * x) * NG + g;
-          const float mn = __half2float(n[0]), s24 = __half2float(n[kBlock * NG]) * (kS24 * kLog2e);
+          const float mn = __half2float(n[0]), ks = __half2float(n[kBlock * NG]);
 #pragma unroll
           for (int nt = 0; nt < NT; nt++)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-              const float v = mn * qsum[nt][e][g] + s24 * (lo[nt][2 * x + e] + hi[nt][2 * x + e] * 0.0625f);
-              sc[nt][u][x][e] = g == 0 ? v : sc[nt][u][x][e] + v;
+              const float v = g == 0 ? mn * qsum[nt][e][g] : fmaf(mn, qsum[nt][e][g], sc[nt][u][x][e]);
+              sc[nt][u][x][e] = fmaf(ks, lo[nt][2 * x + e] + hi[nt][2 * x + e], v);
             }
         }
       }
@@ -629,7 +663,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
 #pragma unroll
               for (int x = 0; x < 2; x++) {
                 const int ts = t + 16 * u + gid + 8 * x;
-                if (!EDGE || ts < len[nt][e]) srow[(nt * kCols + 2 * c + e) * a.score_ld + ts] = sc[nt][u][x][e];
+                if (!EDGE || ts < len[nt][e]) srow[(nt * kCols + 2 * c + e) * a.score_ld + ts] = sc[nt][u][x][e] * qunit[nt][e];
               }
     }
     // ---- running maximum: moves only when a score exceeds it by more than kSlack, so that
@@ -640,7 +674,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
       for (int e = 0; e < 2; e++) {
-        cmax[nt][e] = fmaxf(fmaxf(sc[nt][0][0][e], sc[nt][0][1][e]), fmaxf(sc[nt][1][0][e], sc[nt][1][1][e]));
+        cmax[nt][e] =
+            fmaxf(fmaxf(sc[nt][0][0][e], sc[nt][0][1][e]), fmaxf(sc[nt][1][0][e], sc[nt][1][1][e])) * qunit[nt][e];
         moves |= cmax[nt][e] > m[nt][e] + kSlack;
       }
     if (__any_sync(0xffffffffu, moves)) {
@@ -682,7 +717,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         for (int x = 0; x < 2; x++)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
-            p[nt][x][e] = EDGE && sc[nt][u][x][e] == -INFINITY ? 0.f : fast_exp2(sc[nt][u][x][e] - m[nt][e]);
+            p[nt][x][e] = EDGE && sc[nt][u][x][e] == -INFINITY ? 0.f : fast_exp2(fmaf(sc[nt][u][x][e], qunit[nt][e], -m[nt][e]));
             l[nt][e] += p[nt][x][e];
           }
       uint32_t b[NT][NG][2];
@@ -937,36 +972,42 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   // ---- q as the B operand; word j of lane class c: dims 2o .. 2o+7 ----
   const __half *qrow = a.q + static_cast<int64_t>(s) * a.ldq + static_cast<int64_t>(h) * D;
   uint32_t qf[KW][4];
-  float ql;  // sum of q over this lane's group, times log2(e)
+  float ql, qunit;  // sum of q over this lane's group, over the unit; the unit times log2(e)
   const int g = NG == 2 ? c & 1 : 0;
   {
+    uint4 v[KW];
     float part[NG];
+    bool big = false;
 #pragma unroll
     for (int i = 0; i < NG; i++) part[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < KW; j++) {
       const int o = D == 64 ? 8 * c + 4 * j : 64 * (j >> 2) + 16 * c + 4 * (j & 3);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (len > 0) v = *reinterpret_cast<const uint4 *>(qrow + 2 * o);
-      const __half *e = reinterpret_cast<const __half *>(&v);
-      const int og = o / (G / 2);
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (len > 0) v[j] = *reinterpret_cast<const uint4 *>(qrow + 2 * o);
+      big |= q_big(v[j]);
+      const __half *e = reinterpret_cast<const __half *>(&v[j]);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
 #pragma unroll
-      for (int i = 0; i < NG; i++) part[i] += og == i ? sum : 0.f;
-      const bool on = !(gid & 1) && (NG == 1 || og == ((gid >> 1) & 1));
-      qf[j][0] = on ? __byte_perm(v.x, v.z, 0x5410) : 0u;  // dims 0, 4
-      qf[j][1] = on ? __byte_perm(v.y, v.w, 0x5410) : 0u;  // dims 2, 6
-      qf[j][2] = on ? __byte_perm(v.x, v.z, 0x7632) : 0u;  // dims 1, 5
-      qf[j][3] = on ? __byte_perm(v.y, v.w, 0x7632) : 0u;  // dims 3, 7
+      for (int i = 0; i < NG; i++) part[i] += o / (G / 2) == i ? sum : 0.f;
+    }
+    big = __any_sync(0xffffffffu, big);
+#pragma unroll
+    for (int j = 0; j < KW; j++) {
+      const int o = D == 64 ? 8 * c + 4 * j : 64 * (j >> 2) + 16 * c + 4 * (j & 3);
+      const bool on = !(gid & 1) && (NG == 1 || o / (G / 2) == ((gid >> 1) & 1));
+      if (!on) v[j] = make_uint4(0, 0, 0, 0);
+      q_operands(qf[j], v[j], big);
     }
 #pragma unroll
     for (int i = 0; i < NG; i++) {
       part[i] += __shfl_xor_sync(0xffffffffu, part[i], 1);
       part[i] += __shfl_xor_sync(0xffffffffu, part[i], 2);
     }
-    ql = (NG == 2 && g ? part[NG - 1] : part[0]) * kLog2e;
+    ql = (NG == 2 && g ? part[NG - 1] : part[0]) * (1.0f / q_unit(big));
+    qunit = q_unit(big) * kLog2e;
   }
   const bool upper = c & 2;  // this lane's slot is gid + 8 of the 16
   const int tq = gid + (upper ? 8 : 0);
@@ -1003,7 +1044,7 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
           k1[j] = y.x, k1[j + 1] = y.y, k1[j + 2] = y.z, k1[j + 3] = y.w;
         }
       }
-      float lo[4], hi[4];
+      float lo[4], hi[4];  // two chains of MMAs: their latency bounds a warp
 #pragma unroll
       for (int j = 0; j < KW; j++) {
         const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
@@ -1015,9 +1056,8 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
           mma_f16(hi, x0 & kHiNib, x1 & kHiNib, y0 & kHiNib, y1 & kHiNib, qf[j][2], qf[j][3]);
         }
       }
-      const float dot = (upper ? lo[2] : lo[0]) + (upper ? hi[2] : hi[0]) * 0.0625f;
       const __half *n = nbase + OFF / 2 + 16 * u * NG;
-      float part = __half2float(n[0]) * ql + __half2float(n[kBlock * NG]) * (dot * (kS24 * kLog2e));
+      float part = fmaf(__half2float(n[kBlock * NG]), upper ? lo[2] + hi[2] : lo[0] + hi[0], __half2float(n[0]) * ql);
       if constexpr (NG == 2) part += __shfl_xor_sync(0xffffffffu, part, 1);
       sc[u] = part;
     }
@@ -1030,9 +1070,9 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
       if (!(c & 1))
 #pragma unroll
         for (int u = 0; u < 2; u++)
-          if (!EDGE || t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u];
+          if (!EDGE || t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u] * qunit;
     }
-    float cmax = fmaxf(sc[0], sc[1]);
+    float cmax = fmaxf(sc[0], sc[1]) * qunit;  // scores are held over the unit
     if (__any_sync(0xffffffffu, cmax > m + kSlack)) {  // the running maximum moves
 #pragma unroll
       for (int o = 2; o < 32; o <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
@@ -1050,7 +1090,7 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
 #pragma unroll
     for (int u = 0; u < 2; u++) {
       const __half *n = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG;
-      const float p = fast_exp2(sc[u] - m);
+      const float p = fast_exp2(fmaf(sc[u], qunit, -m));
       float w = p * __half2float(n[kBlock * NG]), pm = p * __half2float(n[0]);
       if (EDGE && t + 16 * u + tq >= t_end) w = pm = 0.f;  // masked slots may hold anything (their p is 0)
       l += p;
