@@ -3,13 +3,28 @@
 // Every (sequence, head) ranks its slots by a 32-bit key: the largest for a protected slot (one of
 // the last `recent` tokens), else the weight's bits in an order-preserving form.  The budget-th
 // largest key splits the slots into kept ones (above it), evicted ones (below) and ties, of which
-// the lowest slots are kept.
+// the lowest slots are kept.  Evicted slots below the budget are holes, kept ones at or above it
+// movers; there are as many of the ones as of the others, and mover i goes into hole i.  Sources
+// and destinations are disjoint, so the moves need no order and no second buffer.
+//
+// One CTA per (sequence, head).  Its slots' weights and tokens are read from memory once, 16 bytes
+// of each at a time; the keys stay in shared memory (the `Wide` form, for more slots than fit
+// there, reads them again instead).  The budget-th key is found by a radix selection of 11, 11 and
+// 10 bits; then every warp takes a run of consecutive slots and the ranks of ties, holes and movers
+// come from ballots and one prefix sum over the warps.  What moves is read and written by 16 lanes
+// per slot, 16 bytes of codes a lane.
 #include "fg_paged.cuh"
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
+constexpr int kBins = 2048;
+#ifndef FG_EVICT_SMEM
+#define FG_EVICT_SMEM (200 * 1024)
+#endif
+#ifndef FG_EVICT_LONG
+#define FG_EVICT_LONG 4096
+#endif
 
 struct EvictArgs {
   PagedArgs kv;
@@ -17,7 +32,10 @@ struct EvictArgs {
   int32_t *new_lengths;
   float *wout;
   int32_t *tout;
-  int budget, recent, limit, rb, mb;  // rb, mb: bytes of a slot's codes and of its mins (or scales)
+  int *lists;  // Wide: [items][2][list]
+  int budget, recent, limit;
+  int keys, pages, list;  // capacities: slots (a multiple of 4), pages, holes or movers
+  int code_vecs, meta;    // 16-byte vectors of a slot's codes; bytes of its mins (or scales): 2, 4 or 8
 };
 
 // Unsigned order of the keys = order of the weights; NaN below everything, -0 as +0.
@@ -27,162 +45,274 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t slot_key(const EvictArgs &a, int64_t slot, int64_t since) {
-  return a.kv.tokens[slot] >= since ? kProtected : weight_key(a.kv.weights[slot]);
+__device__ __forceinline__ uint32_t slot_key(float w, int token, int64_t since) {
+  return token >= since ? kProtected : weight_key(w);
 }
 
-__device__ __forceinline__ int block_sum(int v, int *red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int t = 0;
-  for (int w = 0; w < kThreads / 32; w++) t += red[w];
-  return t;
-}
+template <int T, bool Wide>
+__global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
+  constexpr int W = T / 32;
+  extern __shared__ __align__(16) int sm[];
+  int *const hist = sm;
+  uint32_t *const skeys = reinterpret_cast<uint32_t *>(sm + kBins);
+  int *const spages = sm + kBins + (Wide ? 0 : a.keys);
+  int *const holes = Wide ? a.lists + static_cast<int64_t>(blockIdx.x) * 2 * a.list : spages + a.pages;
+  int *const movers = holes + a.list;
+  __shared__ int red[2][W];
+  __shared__ int pick[2];  // the bin that the budget-th key lies in; keys still wanted from it
 
-// Exclusive prefix count of `flag` over the block; *total: the count.
-__device__ __forceinline__ int block_rank(bool flag, int *red, int *total) {
-  const uint32_t b = __ballot_sync(0xffffffffu, flag);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  if (lane == 0) red[warp] = __popc(b);
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < kThreads / 32; w++) {
-    before += w < warp ? red[w] : 0;
-    all += red[w];
-  }
-  *total = all;
-  return before + __popc(b & ((1u << lane) - 1u));
-}
-
-__device__ __forceinline__ void copy_bytes(uint8_t *pool, int64_t dst, int64_t src, int bytes) {
-  for (int i = 0; i < bytes; i += 2)
-    *reinterpret_cast<uint16_t *>(pool + dst * bytes + i) = *reinterpret_cast<const uint16_t *>(pool + src * bytes + i);
-}
-
-// One CTA per (sequence, head).  The budget-th largest key by bisection on its 32 bits; then the
-// holes below the budget and the kept slots at or above it are walked together, hole by hole.
-__global__ void __launch_bounds__(kThreads) paged_evict_kernel(const EvictArgs a) {
-  __shared__ int red[kThreads / 32];
-  const int s = blockIdx.x / a.kv.H, h = blockIdx.x % a.kv.H, tid = threadIdx.x;
+  const int s = blockIdx.x / a.kv.H, h = blockIdx.x % a.kv.H;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.lengths[s];
   const bool range = n < -1 || n > a.limit;
-  int bad = 0;
-  for (int p = tid * a.kv.ps; !range && p < n; p += kThreads * a.kv.ps) bad |= paged_slot(a.kv, s, h, p) < 0;
-  bad = block_sum(bad, red);
-  if ((range || bad) && tid == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
-  const bool skip = range || bad || n <= a.budget;
-  if (h == 0 && tid == 0 && a.new_lengths != a.lengths) a.new_lengths[s] = skip ? n : a.budget;
-  if (range || bad || n < 1) return;
-  if (skip) {
-    if (a.wout != a.kv.weights)
-      for (int p = tid; p < n; p += kThreads) {
-        const int64_t slot = paged_slot(a.kv, s, h, p);
-        a.wout[slot] = a.kv.weights[slot];
-      }
-    if (a.tout != a.kv.tokens)
-      for (int p = tid; p < n; p += kThreads) {
-        const int64_t slot = paged_slot(a.kv, s, h, p);
-        a.tout[slot] = a.kv.tokens[slot];
-      }
-    return;
-  }
-  const int64_t since = static_cast<int64_t>(a.next[s]) - a.recent;
-  // the largest `key` that at least `budget` slots reach
-  uint32_t key = 0;
-  for (int bit = 31; bit >= 0; bit--) {
-    const uint32_t trial = key | (1u << bit);
-    int c = 0;
-    for (int p = tid; p < n; p += kThreads) c += slot_key(a, paged_slot(a.kv, s, h, p), since) >= trial;
-    if (block_sum(c, red) >= a.budget) key = trial;
-  }
-  int c = 0;
-  for (int p = tid; p < n; p += kThreads) c += slot_key(a, paged_slot(a.kv, s, h, p), since) > key;
-  const int ties = a.budget - block_sum(c, red);  // of the slots with this key, the first `ties` are kept
-  int tie_base = 0;
-  __shared__ int mover[kThreads], hole[kThreads];
-  int next_mover = a.budget, movers = 0, used = 0;  // movers found in [budget, next_mover), not yet placed: movers - used
-  int mover_ties = 0;
-  // ties below the budget, needed to know which ties above it are kept
-  for (int p0 = 0; p0 < a.budget; p0 += kThreads) {
-    const int p = p0 + tid;
-    mover_ties += block_sum(p < a.budget && slot_key(a, paged_slot(a.kv, s, h, p), since) == key, red);
-  }
-  for (int p0 = 0; p0 < a.budget; p0 += kThreads) {
-    const int p = p0 + tid;
-    const bool in = p < a.budget;
-    const int64_t slot = in ? paged_slot(a.kv, s, h, p) : 0;
-    const uint32_t k = in ? slot_key(a, slot, since) : 0u;
-    int total;
-    const int rank = tie_base + block_rank(in && k == key, red, &total);
-    tie_base += total;
-    const bool kept = in && (k > key || (k == key && rank < ties));
-    const float w = in ? a.kv.weights[slot] : 0.f;
-    const int32_t tk = in ? a.kv.tokens[slot] : 0;
-    const int hr = block_rank(in && !kept, red, &total);
-    __syncthreads();
-    if (in && !kept) hole[hr] = p;
-    const int holes = total;
-    if (kept) {
-      if (a.wout != a.kv.weights) a.wout[slot] = w;
-      if (a.tout != a.kv.tokens) a.tout[slot] = tk;
+  const int32_t *const table = a.kv.table + static_cast<int64_t>(s) * a.kv.max_pages;
+  bool bad = false;
+  if (!range && n > 0)
+    for (int i = tid; i < (n + a.kv.ps - 1) / a.kv.ps; i += T) {
+      const int page = table[i];
+      bad |= page < 0 || page >= a.kv.num_pages;
+      if (!Wide) spages[i] = page;
     }
-    // fill the chunk's holes with the next kept slots above the budget
-    int filled = 0;
-    while (filled < holes) {
-      if (used == movers) {  // look through the next chunk above the budget
-        if (next_mover >= n) break;  // (as many kept slots above the budget as holes below it)
-        const int q = next_mover + tid;
-        const bool qin = q < n;
-        const uint32_t qk = qin ? slot_key(a, paged_slot(a.kv, s, h, q), since) : 0u;
-        const int qrank = mover_ties + block_rank(qin && qk == key, red, &total);
-        mover_ties += total;
-        const bool qkept = qin && (qk > key || (qk == key && qrank < ties));
-        const int mr = block_rank(qkept, red, &total);
-        __syncthreads();
-        if (qkept) mover[mr] = q;
-        movers = total;
-        used = 0;
-        next_mover += kThreads;
-        __syncthreads();
-        continue;
+  for (int i = tid; i < kBins; i += T) hist[i] = 0;
+  bad = __syncthreads_or(bad);
+  if ((range || bad) && tid == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
+  const bool evicts = !range && !bad && n > a.budget;
+  if (h == 0 && tid == 0 && a.new_lengths != a.lengths) a.new_lengths[s] = evicts ? a.budget : n;
+  if (range || bad || n < 1) return;
+
+  auto pool_slot = [&](int p) -> int64_t {
+    const int i = p / a.kv.ps;
+    const int page = Wide ? table[i] : spages[i];
+    return (static_cast<int64_t>(page) * a.kv.H + h) * a.kv.ps + (p - i * a.kv.ps);
+  };
+  const int64_t since = static_cast<int64_t>(a.next[s]) - a.recent;
+  const int keep = evicts ? a.budget : n;
+  const bool wcopy = a.wout != a.kv.weights, tcopy = a.tout != a.kv.tokens;
+  if (!evicts && !wcopy && !tcopy) return;
+
+  // ---- every slot once: its key, the selection's first histogram, and the numbers of the slots
+  //      below the budget into their new pools (the holes' are written over below) ----
+  for (int p = 4 * tid; p < n; p += 4 * T) {
+    const int64_t slot = pool_slot(p);  // four slots of one page
+    const float4 w = *reinterpret_cast<const float4 *>(a.kv.weights + slot);
+    const int4 t = *reinterpret_cast<const int4 *>(a.kv.tokens + slot);
+    if (evicts) {
+      const uint32_t k[4] = {slot_key(w.x, t.x, since), slot_key(w.y, t.y, since), slot_key(w.z, t.z, since),
+                             slot_key(w.w, t.w, since)};
+      if (!Wide) *reinterpret_cast<uint4 *>(skeys + p) = make_uint4(k[0], k[1], k[2], k[3]);
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (p + e < n) atomicAdd(&hist[k[e] >> 21], 1);
+    }
+    if (p + 3 < keep) {
+      if (wcopy) *reinterpret_cast<float4 *>(a.wout + slot) = w;
+      if (tcopy) *reinterpret_cast<int4 *>(a.tout + slot) = t;
+    } else if (p < keep) {
+      if (wcopy) {
+        a.wout[slot] = w.x;
+        if (p + 1 < keep) a.wout[slot + 1] = w.y;
+        if (p + 2 < keep) a.wout[slot + 2] = w.z;
       }
-      const int take = min(holes - filled, movers - used);
-      __syncthreads();
-      if (tid < take) {
-        const int64_t dst = paged_slot(a.kv, s, h, hole[filled + tid]), src = paged_slot(a.kv, s, h, mover[used + tid]);
-        copy_bytes(a.kv.kc, dst, src, a.rb);
-        copy_bytes(a.kv.vc, dst, src, a.rb);
-        copy_bytes(reinterpret_cast<uint8_t *>(a.kv.km), dst, src, a.mb);
-        copy_bytes(reinterpret_cast<uint8_t *>(a.kv.ks), dst, src, a.mb);
-        copy_bytes(reinterpret_cast<uint8_t *>(a.kv.vm), dst, src, a.mb);
-        copy_bytes(reinterpret_cast<uint8_t *>(a.kv.vs), dst, src, a.mb);
-        a.wout[dst] = a.kv.weights[src];
-        a.tout[dst] = a.kv.tokens[src];
+      if (tcopy) {
+        a.tout[slot] = t.x;
+        if (p + 1 < keep) a.tout[slot + 1] = t.y;
+        if (p + 2 < keep) a.tout[slot + 2] = t.z;
       }
-      filled += take;
-      used += take;
+    }
+  }
+  if (!evicts) return;
+  __syncthreads();
+
+  auto key_of = [&](int p) -> uint32_t {
+    if (!Wide) return skeys[p];
+    const int64_t slot = pool_slot(p);
+    return slot_key(a.kv.weights[slot], a.kv.tokens[slot], since);
+  };
+  // The bin of `bins` from the top that holds the want-th key, into pick; all threads.
+  auto select = [&](int bins, int want) {
+    const int per = bins / T > 0 ? bins / T : 1;  // bins of a thread, from the top
+    int sum = 0;
+    if (tid * per < bins)
+      for (int i = 0; i < per; i++) sum += hist[bins - 1 - tid * per - i];
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) red[0][warp] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int w = 0; w < warp; w++) before += red[0][w];
+    if (before < want && before + sum >= want) {  // (one thread)
+      for (int i = 0; i < per; i++) {
+        const int b = bins - 1 - tid * per - i, c = hist[b];
+        if (before + c >= want) {
+          pick[0] = b;
+          pick[1] = want - before;
+          break;
+        }
+        before += c;
+      }
+    }
+    __syncthreads();
+  };
+  uint32_t prefix = 0;
+  int want = a.budget;
+  select(kBins, want);
+  prefix = static_cast<uint32_t>(pick[0]);
+  want = pick[1];
+#pragma unroll
+  for (int pass = 1; pass < 3; pass++) {
+    const int low = pass == 1 ? 10 : 0, bits = pass == 1 ? 11 : 10;
+    for (int i = tid; i < (1 << bits); i += T) hist[i] = 0;
+    __syncthreads();
+    for (int p = tid; p < n; p += T) {
+      const uint32_t k = key_of(p);
+      if (k >> (low + bits) == prefix) atomicAdd(&hist[(k >> low) & ((1u << bits) - 1u)], 1);
+    }
+    __syncthreads();
+    select(1 << bits, want);
+    prefix = prefix << bits | static_cast<uint32_t>(pick[0]);
+    want = pick[1];
+  }
+  const uint32_t key = prefix;  // of the slots with this key, the first `want` are kept
+
+  // ---- ranks: warp w has the slots w * run .. (w + 1) * run - 1 ----
+  const int run = ((n + W - 1) / W + 31) / 32 * 32;
+  const int p0 = min(n, warp * run), p1 = min(n, p0 + run);
+  const uint32_t below = (1u << lane) - 1u;
+  int ties = 0;
+  for (int p = p0 + lane; p - lane < p1; p += 32)
+    ties += __popc(__ballot_sync(0xffffffffu, p < p1 && key_of(p) == key));
+  if (lane == 0) red[0][warp] = ties;
+  __syncthreads();
+  int tie0 = 0;
+  for (int w = 0; w < warp; w++) tie0 += red[0][w];
+  __syncthreads();
+  auto walk = [&](bool write, int hole, int mover, int *holes_found, int *movers_found) {
+    int tie = tie0;
+    for (int p = p0 + lane; p - lane < p1; p += 32) {
+      const uint32_t k = p < p1 ? key_of(p) : 0u;
+      const bool eq = p < p1 && k == key;
+      const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
+      const bool kept = p < p1 && (k > key || (eq && tie + __popc(eqs & below) < want));
+      tie += __popc(eqs);
+      const uint32_t hs = __ballot_sync(0xffffffffu, p < p1 && !kept && p < a.budget);
+      const uint32_t ms = __ballot_sync(0xffffffffu, kept && p >= a.budget);
+      if (write) {
+        const int hi = hole + __popc(hs & below), mi = mover + __popc(ms & below);
+        if (hs >> lane & 1u && hi < a.list) holes[hi] = p;
+        if (ms >> lane & 1u && mi < a.list) movers[mi] = p;
+      }
+      hole += __popc(hs);
+      mover += __popc(ms);
+    }
+    *holes_found = hole;
+    *movers_found = mover;
+  };
+  int hn, mn;
+  walk(false, 0, 0, &hn, &mn);
+  if (lane == 0) {
+    red[0][warp] = hn;
+    red[1][warp] = mn;
+  }
+  __syncthreads();
+  int h0 = 0, m0 = 0, moves = 0;
+  for (int w = 0; w < W; w++) {
+    h0 += w < warp ? red[0][w] : 0;
+    m0 += w < warp ? red[1][w] : 0;
+    moves += red[0][w];
+  }
+  moves = min(moves, a.list);  // (as many movers as holes)
+  if (moves == 0) return;
+  walk(true, h0, m0, &hn, &mn);
+  __syncthreads();
+
+  // ---- the moves: 16 lanes per slot; lane 0 .. 2 code_vecs - 1 a vector of codes of k or v (twice
+  //      16 of them for head dim 256 in turn), then the four group numbers, the weight, the token ----
+  const int l16 = tid & 15;
+  for (int i = tid / 16; i < moves; i += T / 16) {
+    const int64_t dst = pool_slot(holes[i]), src = pool_slot(movers[i]);
+    const int units = 2 * a.code_vecs + 6;
+    for (int u = l16; u < units; u += 16) {
+      if (u < 2 * a.code_vecs) {
+        const bool v = u >= a.code_vecs;
+        uint4 *const pool = reinterpret_cast<uint4 *>(v ? a.kv.vc : a.kv.kc);
+        const int x = v ? u - a.code_vecs : u;
+        pool[dst * a.code_vecs + x] = pool[src * a.code_vecs + x];
+      } else {
+        const int x = u - 2 * a.code_vecs;
+        if (x < 4) {
+          __half *const pool = x == 0 ? a.kv.km : x == 1 ? a.kv.ks : x == 2 ? a.kv.vm : a.kv.vs;
+          uint8_t *const b = reinterpret_cast<uint8_t *>(pool);
+          if (a.meta == 4) {
+            *reinterpret_cast<uint32_t *>(b + dst * 4) = *reinterpret_cast<const uint32_t *>(b + src * 4);
+          } else if (a.meta == 2) {
+            *reinterpret_cast<uint16_t *>(b + dst * 2) = *reinterpret_cast<const uint16_t *>(b + src * 2);
+          } else {
+            *reinterpret_cast<uint2 *>(b + dst * 8) = *reinterpret_cast<const uint2 *>(b + src * 8);
+          }
+        } else if (x == 4) {
+          a.wout[dst] = a.kv.weights[src];
+        } else {
+          a.tout[dst] = a.kv.tokens[src];
+        }
+      }
     }
   }
 }
 
 // new_lengths given as lengths itself: written once every CTA has read its length.
 __global__ void paged_new_lengths_kernel(int32_t *lengths, int seqs, const EvictArgs a) {
-  const int s = blockIdx.x * blockDim.x + threadIdx.x;
-  if (s >= seqs) return;
-  const int n = lengths[s];
-  if (n <= a.budget || n > a.limit) return;
-  for (int p = 0; p < n; p += a.kv.ps)
-    if (paged_slot(a.kv, s, 0, p) < 0) return;
-  lengths[s] = a.budget;
+  const int s = blockIdx.x, n = lengths[s];
+  bool bad = n <= a.budget || n > a.limit;
+  for (int p = threadIdx.x * a.kv.ps; !bad && p < n; p += blockDim.x * a.kv.ps) bad = paged_slot(a.kv, s, 0, p) < 0;
+  if (!__syncthreads_or(bad) && threadIdx.x == 0) lengths[s] = a.budget;
+}
+
+struct EvictPlan {
+  bool wide;
+  int threads, keys, pages, list;
+  size_t smem, lists;
+};
+
+EvictPlan evict_plan(const fg_paged_kv *kv, int budget, int max_len) {
+  EvictPlan p;
+  const int cap = fg_paged_capacity(kv), limit = max_len && max_len < cap ? max_len : cap;
+  p.keys = (limit + 3) / 4 * 4;
+  p.pages = (limit + kv->page_size - 1) / kv->page_size;
+  const int over = limit > budget ? limit - budget : 0;
+  p.list = over < budget ? over : budget;
+  const size_t need = (static_cast<size_t>(kBins) + p.keys + p.pages + 2 * static_cast<size_t>(p.list)) * 4;
+  p.wide = need > FG_EVICT_SMEM;
+  p.smem = p.wide ? kBins * 4 : need;
+  p.lists = p.wide ? static_cast<size_t>(kv->num_seqs) * kv->num_heads * 2 * p.list * 4 : 0;
+  p.threads = limit > FG_EVICT_LONG ? 1024 : 256;
+  return p;
+}
+
+template <int T, bool Wide>
+fg_status launch(const EvictArgs &a, const EvictPlan &p, unsigned grid, cudaStream_t st) {
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!Wide && dev >= 0 && dev < 64 && !done[dev]) {
+    const fg_status rc = fg_cuda_check(cudaFuncSetAttribute(paged_evict_kernel<T, Wide>,
+                                                            cudaFuncAttributeMaxDynamicSharedMemorySize, FG_EVICT_SMEM));
+    if (rc != FG_OK) return rc;
+    done[dev] = true;
+  }
+  paged_evict_kernel<T, Wide><<<grid, T, p.smem, st>>>(a);
+  return fg_launch_check();
 }
 
 }  // namespace
 
-extern "C" size_t fg_paged_kv_evict_workspace_bytes(const fg_paged_kv *kv, int budget, int max_len) { return 0; }
+extern "C" size_t fg_paged_kv_evict_workspace_bytes(const fg_paged_kv *kv, int budget, int max_len) {
+  if (fg_paged_validate(kv) != FG_OK || budget < 1 || max_len < 0) return 0;
+  return evict_plan(kv, budget, max_len).lists;
+}
 
 extern "C" fg_status fg_paged_kv_evict(const fg_paged_kv *kv, const int32_t *lengths, const int32_t *next_tokens,
                                        int budget, int recent, int max_len, int32_t *new_lengths, float *weights_out,
@@ -195,6 +325,8 @@ extern "C" fg_status fg_paged_kv_evict(const fg_paged_kv *kv, const int32_t *len
   if (!lengths || !next_tokens || !new_lengths || !fg_aligned16(workspace)) return FG_ERR_INVALID;
   if (!fg_aligned16(weights_out) || !fg_aligned16(tokens_out)) return FG_ERR_INVALID;
   if (static_cast<int64_t>(kv->num_seqs) * kv->num_heads > INT32_MAX) return FG_ERR_SHAPE;
+  const EvictPlan p = evict_plan(kv, budget, max_len);
+  if (p.lists > (workspace ? workspace_bytes : 0)) return FG_ERR_WORKSPACE;
   EvictArgs a;
   if (!fg_paged_args(kv, &a.kv)) return FG_ERR_CUDA;
   a.lengths = lengths;
@@ -202,16 +334,22 @@ extern "C" fg_status fg_paged_kv_evict(const fg_paged_kv *kv, const int32_t *len
   a.new_lengths = new_lengths;
   a.wout = weights_out ? weights_out : kv->weights;
   a.tout = tokens_out ? tokens_out : kv->tokens;
+  a.lists = static_cast<int *>(workspace);
   a.budget = budget;
   a.recent = recent;
   a.limit = fg_paged_capacity(kv);
   if (max_len && max_len < a.limit) a.limit = max_len;
-  a.rb = kv->head_dim / 2;
-  a.mb = kv->head_dim / fg_kv_group(kv->group) * 2;
+  a.keys = p.keys;
+  a.pages = p.pages;
+  a.list = p.list;
+  a.code_vecs = kv->head_dim / 32;
+  a.meta = kv->head_dim / fg_kv_group(kv->group) * 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  paged_evict_kernel<<<static_cast<unsigned>(kv->num_seqs) * kv->num_heads, kThreads, 0, st>>>(a);
-  if ((rc = fg_launch_check()) != FG_OK) return rc;
-  if (new_lengths == lengths)
-    paged_new_lengths_kernel<<<(kv->num_seqs + 127) / 128, 128, 0, st>>>(new_lengths, kv->num_seqs, a);
+  const unsigned grid = static_cast<unsigned>(kv->num_seqs) * kv->num_heads;
+  if (p.wide) rc = launch<1024, true>(a, p, grid, st);
+  else if (p.threads == 1024) rc = launch<1024, false>(a, p, grid, st);
+  else rc = launch<256, false>(a, p, grid, st);
+  if (rc != FG_OK || new_lengths != lengths) return rc;
+  paged_new_lengths_kernel<<<kv->num_seqs, 128, 0, st>>>(new_lengths, kv->num_seqs, a);
   return fg_launch_check();
 }
