@@ -35,6 +35,7 @@ bool fg_paged_args(const fg_paged_kv *kv, PagedArgs *a) {
   a->table = kv->page_table;
   a->num_pages = kv->num_pages;
   a->ps = kv->page_size;
+  a->ps_shift = (kv->page_size & (kv->page_size - 1)) ? -1 : __builtin_ctz(kv->page_size);
   a->max_pages = kv->max_pages;
   a->H = kv->num_heads;
   a->err = fg_error_word_ptr();

@@ -9,7 +9,7 @@ struct PagedArgs {
   float *weights;
   int32_t *tokens;
   const int32_t *table;
-  int num_pages, ps, max_pages, H;
+  int num_pages, ps, ps_shift, max_pages, H;  // ps_shift: log2(ps), -1 if ps is no power of two
   unsigned int *err;
 };
 
@@ -20,9 +20,14 @@ bool fg_paged_args(const fg_paged_kv *kv, PagedArgs *a);
 
 static inline int fg_paged_capacity(const fg_paged_kv *kv) { return kv->max_pages * kv->page_size; }
 
+// Page of a sequence that slot `p` lies in.
+__device__ __forceinline__ int paged_index(const PagedArgs &a, int p) {
+  return a.ps_shift >= 0 ? p >> a.ps_shift : p / a.ps;
+}
+
 // Pool index of slot `p` (inside the table's pages) of sequence `s`, head `h`; -1: a bad page.
 __device__ __forceinline__ int64_t paged_slot(const PagedArgs &a, int s, int h, int p) {
-  const int pi = p / a.ps;
+  const int pi = paged_index(a, p);
   const int page = a.table[static_cast<int64_t>(s) * a.max_pages + pi];
   if (page < 0 || page >= a.num_pages) return -1;
   return (static_cast<int64_t>(page) * a.H + h) * a.ps + (p - pi * a.ps);

@@ -10,8 +10,8 @@
 // One CTA per (sequence, head).  Its slots' weights and tokens are read from memory once, 16 bytes
 // of each at a time; the keys stay in shared memory (the `Wide` form, for more slots than fit
 // there, reads them again instead).  The budget-th key is found by a radix selection of 11, 11 and
-// 10 bits; then every warp takes a run of consecutive slots and the ranks of ties, holes and movers
-// come from ballots and one prefix sum over the warps.  What moves is read and written by 16 lanes
+// 10 bits; the ranks of ties, holes and movers come from a bit per slot (ballots) and prefix sums over
+// the words.  What moves is read and written by 16 lanes
 // per slot, 16 bytes of codes a lane.
 #include "fg_paged.cuh"
 
@@ -32,9 +32,9 @@ struct EvictArgs {
   int32_t *new_lengths;
   float *wout;
   int32_t *tout;
-  int *lists;  // Wide: [items][2][list]
+  int *lists;  // Wide: [items][2 * list + 2 * words]
   int budget, recent, limit;
-  int keys, pages, list;  // capacities: slots (a multiple of 4), pages, holes or movers
+  int keys, pages, list, words;  // capacities: slots (a multiple of 4), pages, holes or movers, 32 slots
   int code_vecs, meta;    // 16-byte vectors of a slot's codes; bytes of its mins (or scales): 2, 4 or 8
 };
 
@@ -49,6 +49,20 @@ __device__ __forceinline__ uint32_t slot_key(float w, int token, int64_t since) 
   return token >= since ? kProtected : weight_key(w);
 }
 
+// Sum of the first `warp` of W numbers in shared memory, and of all of them; a whole warp calls it.
+template <int W>
+__device__ __forceinline__ int sum_before(const int *red, int warp, int lane, int *all) {
+  const int v = lane < W ? red[lane] : 0;
+  int before = lane < warp ? v : 0, sum = v;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  *all = sum;
+  return before;
+}
+
 template <int T, bool Wide>
 __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
   constexpr int W = T / 32;
@@ -56,9 +70,11 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
   int *const hist = sm;
   uint32_t *const skeys = reinterpret_cast<uint32_t *>(sm + kBins);
   int *const spages = sm + kBins + (Wide ? 0 : a.keys);
-  int *const holes = Wide ? a.lists + static_cast<int64_t>(blockIdx.x) * 2 * a.list : spages + a.pages;
+  int *const holes = Wide ? a.lists + static_cast<int64_t>(blockIdx.x) * 2 * (a.list + a.words) : spages + a.pages;
   int *const movers = holes + a.list;
-  __shared__ int red[2][W];
+  uint32_t *const above = reinterpret_cast<uint32_t *>(movers + a.list);  // a bit per slot
+  uint32_t *const equal = above + a.words;
+  __shared__ int red[W];
   __shared__ int pick[2];  // the bin that the budget-th key lies in; keys still wanted from it
 
   const int s = blockIdx.x / a.kv.H, h = blockIdx.x % a.kv.H;
@@ -81,7 +97,7 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
   if (range || bad || n < 1) return;
 
   auto pool_slot = [&](int p) -> int64_t {
-    const int i = p / a.kv.ps;
+    const int i = paged_index(a.kv, p);
     const int page = Wide ? table[i] : spages[i];
     return (static_cast<int64_t>(page) * a.kv.H + h) * a.kv.ps + (p - i * a.kv.ps);
   };
@@ -92,31 +108,49 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
 
   // ---- every slot once: its key, the selection's first histogram, and the numbers of the slots
   //      below the budget into their new pools (the holes' are written over below) ----
-  for (int p = 4 * tid; p < n; p += 4 * T) {
-    const int64_t slot = pool_slot(p);  // four slots of one page
-    const float4 w = *reinterpret_cast<const float4 *>(a.kv.weights + slot);
-    const int4 t = *reinterpret_cast<const int4 *>(a.kv.tokens + slot);
-    if (evicts) {
-      const uint32_t k[4] = {slot_key(w.x, t.x, since), slot_key(w.y, t.y, since), slot_key(w.z, t.z, since),
-                             slot_key(w.w, t.w, since)};
-      if (!Wide) *reinterpret_cast<uint4 *>(skeys + p) = make_uint4(k[0], k[1], k[2], k[3]);
+  constexpr int U = 4;  // loads in flight: four slots each
+  for (int q = 4 * tid; q < n; q += 4 * U * T) {
+    int64_t slots[U];
+    float4 ws[U];
+    int4 ts[U];
 #pragma unroll
-      for (int e = 0; e < 4; e++)
-        if (p + e < n) atomicAdd(&hist[k[e] >> 21], 1);
-    }
-    if (p + 3 < keep) {
-      if (wcopy) *reinterpret_cast<float4 *>(a.wout + slot) = w;
-      if (tcopy) *reinterpret_cast<int4 *>(a.tout + slot) = t;
-    } else if (p < keep) {
-      if (wcopy) {
-        a.wout[slot] = w.x;
-        if (p + 1 < keep) a.wout[slot + 1] = w.y;
-        if (p + 2 < keep) a.wout[slot + 2] = w.z;
+    for (int u = 0; u < U; u++) {
+      const int p = q + 4 * u * T;
+      if (p < n) {
+        slots[u] = pool_slot(p);  // four slots of one page
+        ws[u] = *reinterpret_cast<const float4 *>(a.kv.weights + slots[u]);
+        ts[u] = *reinterpret_cast<const int4 *>(a.kv.tokens + slots[u]);
       }
-      if (tcopy) {
-        a.tout[slot] = t.x;
-        if (p + 1 < keep) a.tout[slot + 1] = t.y;
-        if (p + 2 < keep) a.tout[slot + 2] = t.z;
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int p = q + 4 * u * T;
+      if (p >= n) break;
+      const int64_t slot = slots[u];
+      const float4 w = ws[u];
+      const int4 t = ts[u];
+      if (evicts) {
+        const uint32_t k[4] = {slot_key(w.x, t.x, since), slot_key(w.y, t.y, since), slot_key(w.z, t.z, since),
+                               slot_key(w.w, t.w, since)};
+        if (!Wide) *reinterpret_cast<uint4 *>(skeys + p) = make_uint4(k[0], k[1], k[2], k[3]);
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          if (p + e < n) atomicAdd(&hist[k[e] >> 21], 1);
+      }
+      if (p + 3 < keep) {
+        if (wcopy) *reinterpret_cast<float4 *>(a.wout + slot) = w;
+        if (tcopy) *reinterpret_cast<int4 *>(a.tout + slot) = t;
+      } else if (p < keep) {
+        if (wcopy) {
+          a.wout[slot] = w.x;
+          if (p + 1 < keep) a.wout[slot + 1] = w.y;
+          if (p + 2 < keep) a.wout[slot + 2] = w.z;
+        }
+        if (tcopy) {
+          a.tout[slot] = t.x;
+          if (p + 1 < keep) a.tout[slot + 1] = t.y;
+          if (p + 2 < keep) a.tout[slot + 2] = t.z;
+        }
       }
     }
   }
@@ -140,10 +174,10 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    if (lane == 31) red[0][warp] = incl;
+    if (lane == 31) red[warp] = incl;
     __syncthreads();
-    int before = incl - sum;
-    for (int w = 0; w < warp; w++) before += red[0][w];
+    int all;
+    int before = incl - sum + sum_before<W>(red, warp, lane, &all);
     if (before < want && before + sum >= want) {  // (one thread)
       for (int i = 0; i < per; i++) {
         const int b = bins - 1 - tid * per - i, c = hist[b];
@@ -178,87 +212,106 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
   }
   const uint32_t key = prefix;  // of the slots with this key, the first `want` are kept
 
-  // ---- ranks: warp w has the slots w * run .. (w + 1) * run - 1 ----
-  const int run = ((n + W - 1) / W + 31) / 32 * 32;
-  const int p0 = min(n, warp * run), p1 = min(n, p0 + run);
-  const uint32_t below = (1u << lane) - 1u;
-  int ties = 0;
-  for (int p = p0 + lane; p - lane < p1; p += 32)
-    ties += __popc(__ballot_sync(0xffffffffu, p < p1 && key_of(p) == key));
-  if (lane == 0) red[0][warp] = ties;
-  __syncthreads();
-  int tie0 = 0;
-  for (int w = 0; w < warp; w++) tie0 += red[0][w];
-  __syncthreads();
-  auto walk = [&](bool write, int hole, int mover, int *holes_found, int *movers_found) {
-    int tie = tie0;
-    for (int p = p0 + lane; p - lane < p1; p += 32) {
-      const uint32_t k = p < p1 ? key_of(p) : 0u;
-      const bool eq = p < p1 && k == key;
-      const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-      const bool kept = p < p1 && (k > key || (eq && tie + __popc(eqs & below) < want));
-      tie += __popc(eqs);
-      const uint32_t hs = __ballot_sync(0xffffffffu, p < p1 && !kept && p < a.budget);
-      const uint32_t ms = __ballot_sync(0xffffffffu, kept && p >= a.budget);
-      if (write) {
-        const int hi = hole + __popc(hs & below), mi = mover + __popc(ms & below);
-        if (hs >> lane & 1u && hi < a.list) holes[hi] = p;
-        if (ms >> lane & 1u && mi < a.list) movers[mi] = p;
-      }
-      hole += __popc(hs);
-      mover += __popc(ms);
+  const bool all_ties = hist[key & 1023u] == want;
+
+  // ---- the slots as bits, a word for 32: above the key, and with it ----
+  const int words = (n + 31) / 32;
+  for (int p = tid; p < words * 32; p += T) {
+    const uint32_t k = p < n ? key_of(p) : 0u;
+    const uint32_t over = __ballot_sync(0xffffffffu, p < n && k > key), same = __ballot_sync(0xffffffffu, p < n && k == key);
+    if (lane == 0) {
+      above[p / 32] = over;
+      equal[p / 32] = same;
     }
-    *holes_found = hole;
-    *movers_found = mover;
-  };
-  int hn, mn;
-  walk(false, 0, 0, &hn, &mn);
-  if (lane == 0) {
-    red[0][warp] = hn;
-    red[1][warp] = mn;
   }
   __syncthreads();
-  int h0 = 0, m0 = 0, moves = 0;
-  for (int w = 0; w < W; w++) {
-    h0 += w < warp ? red[0][w] : 0;
-    m0 += w < warp ? red[1][w] : 0;
-    moves += red[0][w];
+  // the kept ones: ties in order until enough
+  auto scan = [&](int v, int *total) -> int {  // exclusive prefix sum over the CTA's threads
+    int incl = v, sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) red[warp] = incl;
+    __syncthreads();
+    const int before = sum_before<W>(red, warp, lane, &sum);
+    __syncthreads();
+    *total = sum;
+    return before + incl - v;
+  };
+  int tie0 = 0, hole0 = 0, mover0 = 0;
+  for (int w0 = 0; w0 < words; w0 += T) {
+    const int w = w0 + tid;
+    uint32_t kept = 0, hole = 0, mover = 0;
+    if (w < words) kept = above[w] | (all_ties ? equal[w] : 0u);
+    if (!all_ties) {  // (block-uniform)
+      const uint32_t same = w < words ? equal[w] : 0u;
+      int total;
+      int left = want - tie0 - scan(__popc(same), &total);  // ties this word may still keep
+      for (uint32_t b = same; b && left > 0; b &= b - 1, left--) kept |= b & (0u - b);
+      tie0 += total;
+    }
+    if (w < words) {
+      const int low = a.budget - 32 * w;  // bits of the word below the budget
+      const uint32_t mask = low >= 32 ? 0xFFFFFFFFu : low <= 0 ? 0u : (1u << low) - 1u;
+      hole = ~kept & mask;  // (the budget is below n: all of these are slots)
+      mover = kept & ~mask;
+    }
+    int th, tm;
+    int hi = hole0 + scan(__popc(hole), &th), mi = mover0 + scan(__popc(mover), &tm);
+    for (; hole; hole &= hole - 1, hi++)
+      if (hi < a.list) holes[hi] = 32 * w + __ffs(hole) - 1;
+    for (; mover; mover &= mover - 1, mi++)
+      if (mi < a.list) movers[mi] = 32 * w + __ffs(mover) - 1;
+    hole0 += th;
+    mover0 += tm;
   }
-  moves = min(moves, a.list);  // (as many movers as holes)
-  if (moves == 0) return;
-  walk(true, h0, m0, &hn, &mn);
+  const int moves = min(min(hole0, mover0), a.list);  // (as many of the ones as of the others)
   __syncthreads();
 
-  // ---- the moves: 16 lanes per slot; lane 0 .. 2 code_vecs - 1 a vector of codes of k or v (twice
-  //      16 of them for head dim 256 in turn), then the four group numbers, the weight, the token ----
-  const int l16 = tid & 15;
-  for (int i = tid / 16; i < moves; i += T / 16) {
-    const int64_t dst = pool_slot(holes[i]), src = pool_slot(movers[i]);
-    const int units = 2 * a.code_vecs + 6;
-    for (int u = l16; u < units; u += 16) {
-      if (u < 2 * a.code_vecs) {
-        const bool v = u >= a.code_vecs;
-        uint4 *const pool = reinterpret_cast<uint4 *>(v ? a.kv.vc : a.kv.kc);
-        const int x = v ? u - a.code_vecs : u;
-        pool[dst * a.code_vecs + x] = pool[src * a.code_vecs + x];
-      } else {
-        const int x = u - 2 * a.code_vecs;
-        if (x < 4) {
-          __half *const pool = x == 0 ? a.kv.km : x == 1 ? a.kv.ks : x == 2 ? a.kv.vm : a.kv.vs;
-          uint8_t *const b = reinterpret_cast<uint8_t *>(pool);
-          if (a.meta == 4) {
-            *reinterpret_cast<uint32_t *>(b + dst * 4) = *reinterpret_cast<const uint32_t *>(b + src * 4);
-          } else if (a.meta == 2) {
-            *reinterpret_cast<uint16_t *>(b + dst * 2) = *reinterpret_cast<const uint16_t *>(b + src * 2);
-          } else {
-            *reinterpret_cast<uint2 *>(b + dst * 8) = *reinterpret_cast<const uint2 *>(b + src * 8);
-          }
-        } else if (x == 4) {
-          a.wout[dst] = a.kv.weights[src];
-        } else {
-          a.tout[dst] = a.kv.tokens[src];
-        }
+  // ---- the moves: 16 lanes per slot, M slots of each in flight.  Lanes 0 .. 7 (0 .. 3 for head dim
+  //      64) take 16 bytes of codes, half of them k's (twice for head dim 256), lanes 8 .. 11 the
+  //      group numbers, 12 the weight, 13 the token ----
+  constexpr int M = 4;
+  const int l16 = tid & 15, cv = a.code_vecs;
+  const bool codes = l16 < 8 && l16 < 2 * cv, second = codes && cv == 8;
+  const bool of_v = l16 >= (cv == 8 ? 4 : cv);
+  uint4 *const cpool = reinterpret_cast<uint4 *>(of_v ? a.kv.vc : a.kv.kc) + (of_v ? l16 - (cv == 8 ? 4 : cv) : l16);
+  __half *const mpool = l16 == 8 ? a.kv.km : l16 == 9 ? a.kv.ks : l16 == 10 ? a.kv.vm : a.kv.vs;
+  const bool nums = l16 >= 8 && l16 < 12, track = l16 == 12 || l16 == 13;
+  const uint32_t *const tsrc = l16 == 12 ? reinterpret_cast<const uint32_t *>(a.kv.weights)
+                                         : reinterpret_cast<const uint32_t *>(a.kv.tokens);
+  uint32_t *const tdst = l16 == 12 ? reinterpret_cast<uint32_t *>(a.wout) : reinterpret_cast<uint32_t *>(a.tout);
+  for (int i0 = tid / 16; i0 < moves; i0 += M * (T / 16)) {
+    int64_t dst[M];
+    uint4 x[M], y[M];
+#pragma unroll
+    for (int u = 0; u < M; u++) {
+      const int i = i0 + u * (T / 16);
+      if (i >= moves) break;
+      const int64_t src = pool_slot(movers[i]);
+      dst[u] = pool_slot(holes[i]);
+      if (codes) x[u] = cpool[src * cv];
+      if (second) y[u] = cpool[src * cv + 4];
+      if (nums) {
+        if (a.meta == 4) x[u].x = reinterpret_cast<const uint32_t *>(mpool)[src];
+        else if (a.meta == 2) x[u].x = reinterpret_cast<const uint16_t *>(mpool)[src];
+        else *reinterpret_cast<uint2 *>(&x[u]) = reinterpret_cast<const uint2 *>(mpool)[src];
       }
+      if (track) x[u].x = tsrc[src];
+    }
+#pragma unroll
+    for (int u = 0; u < M; u++) {
+      if (i0 + u * (T / 16) >= moves) break;
+      if (codes) cpool[dst[u] * cv] = x[u];
+      if (second) cpool[dst[u] * cv + 4] = y[u];
+      if (nums) {
+        if (a.meta == 4) reinterpret_cast<uint32_t *>(mpool)[dst[u]] = x[u].x;
+        else if (a.meta == 2) reinterpret_cast<uint16_t *>(mpool)[dst[u]] = static_cast<uint16_t>(x[u].x);
+        else reinterpret_cast<uint2 *>(mpool)[dst[u]] = *reinterpret_cast<const uint2 *>(&x[u]);
+      }
+      if (track) tdst[dst[u]] = x[u].x;
     }
   }
 }
@@ -273,7 +326,7 @@ __global__ void paged_new_lengths_kernel(int32_t *lengths, int seqs, const Evict
 
 struct EvictPlan {
   bool wide;
-  int threads, keys, pages, list;
+  int threads, keys, pages, list, words;
   size_t smem, lists;
 };
 
@@ -284,10 +337,12 @@ EvictPlan evict_plan(const fg_paged_kv *kv, int budget, int max_len) {
   p.pages = (limit + kv->page_size - 1) / kv->page_size;
   const int over = limit > budget ? limit - budget : 0;
   p.list = over < budget ? over : budget;
-  const size_t need = (static_cast<size_t>(kBins) + p.keys + p.pages + 2 * static_cast<size_t>(p.list)) * 4;
+  p.words = (limit + 31) / 32;
+  const size_t lists = 2 * (static_cast<size_t>(p.list) + p.words) * 4;
+  const size_t need = (static_cast<size_t>(kBins) + p.keys + p.pages) * 4 + lists;
   p.wide = need > FG_EVICT_SMEM;
   p.smem = p.wide ? kBins * 4 : need;
-  p.lists = p.wide ? static_cast<size_t>(kv->num_seqs) * kv->num_heads * 2 * p.list * 4 : 0;
+  p.lists = p.wide ? static_cast<size_t>(kv->num_seqs) * kv->num_heads * lists : 0;
   p.threads = limit > FG_EVICT_LONG ? 1024 : 256;
   return p;
 }
@@ -342,6 +397,7 @@ extern "C" fg_status fg_paged_kv_evict(const fg_paged_kv *kv, const int32_t *len
   a.keys = p.keys;
   a.pages = p.pages;
   a.list = p.list;
+  a.words = p.words;
   a.code_vecs = kv->head_dim / 32;
   a.meta = kv->head_dim / fg_kv_group(kv->group) * 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
