@@ -11,16 +11,23 @@
 // of each at a time; the keys stay in shared memory (the `Wide` form, for more slots than fit
 // there, reads them again instead).  The budget-th key is found by a radix selection of 11, 11 and
 // 10 bits; the ranks of ties, holes and movers come from a bit per slot (ballots) and prefix sums over
-// the words.  What moves is read and written by 16 lanes
-// per slot, 16 bytes of codes a lane.
+// the words.  What moves is read and written 16 bytes of codes at a time, several a thread in
+// flight.
 #include "fg_paged.cuh"
 
 namespace {
 
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
 constexpr int kBins = 2048;
+constexpr int kRanked = 128;
 #ifndef FG_EVICT_SMEM
 #define FG_EVICT_SMEM (200 * 1024)
+#endif
+#ifndef FG_EVICT_T
+#define FG_EVICT_T 192
+#endif
+#ifndef FG_EVICT_B
+#define FG_EVICT_B 6
 #endif
 #ifndef FG_EVICT_LONG
 #define FG_EVICT_LONG 4096
@@ -63,8 +70,9 @@ __device__ __forceinline__ int sum_before(const int *red, int warp, int lane, in
   return before;
 }
 
-template <int T, bool Wide>
-__global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
+// T threads, U vectors of 4 slots a thread in flight, B CTAs per SM.
+template <int T, int U, int B, bool Wide>
+__global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
   constexpr int W = T / 32;
   extern __shared__ __align__(16) int sm[];
   int *const hist = sm;
@@ -75,6 +83,8 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
   uint32_t *const above = reinterpret_cast<uint32_t *>(movers + a.list);  // a bit per slot
   uint32_t *const equal = above + a.words;
   __shared__ int red[W];
+  __shared__ uint64_t cand[kRanked];  // the keys that are ranked one by one, with their slots
+  __shared__ int cands;
   __shared__ int pick[2];  // the bin that the budget-th key lies in; keys still wanted from it
 
   const int s = blockIdx.x / a.kv.H, h = blockIdx.x % a.kv.H;
@@ -90,6 +100,7 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
       if (!Wide) spages[i] = page;
     }
   for (int i = tid; i < kBins; i += T) hist[i] = 0;
+  if (tid == 0) cands = 0;
   bad = __syncthreads_or(bad);
   if ((range || bad) && tid == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
   const bool evicts = !range && !bad && n > a.budget;
@@ -108,7 +119,6 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
 
   // ---- every slot once: its key, the selection's first histogram, and the numbers of the slots
   //      below the budget into their new pools (the holes' are written over below) ----
-  constexpr int U = 4;  // loads in flight: four slots each
   for (int q = 4 * tid; q < n; q += 4 * U * T) {
     int64_t slots[U];
     float4 ws[U];
@@ -164,10 +174,9 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
   };
   // The bin of `bins` from the top that holds the want-th key, into pick; all threads.
   auto select = [&](int bins, int want) {
-    const int per = bins / T > 0 ? bins / T : 1;  // bins of a thread, from the top
+    const int per = (bins + T - 1) / T, top = bins - 1 - tid * per;  // a thread's bins, from the top
     int sum = 0;
-    if (tid * per < bins)
-      for (int i = 0; i < per; i++) sum += hist[bins - 1 - tid * per - i];
+    for (int i = 0; i < per && top - i >= 0; i++) sum += hist[top - i];
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -180,9 +189,9 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
     int before = incl - sum + sum_before<W>(red, warp, lane, &all);
     if (before < want && before + sum >= want) {  // (one thread)
       for (int i = 0; i < per; i++) {
-        const int b = bins - 1 - tid * per - i, c = hist[b];
+        const int c = hist[top - i];
         if (before + c >= want) {
-          pick[0] = b;
+          pick[0] = top - i;
           pick[1] = want - before;
           break;
         }
@@ -191,14 +200,20 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
     }
     __syncthreads();
   };
-  uint32_t prefix = 0;
-  int want = a.budget;
+  uint32_t prefix = 0;  // of the budget-th key: its leading bits so far
+  int want = a.budget;   // which of the keys with them it is, from the largest
   select(kBins, want);
   prefix = static_cast<uint32_t>(pick[0]);
   want = pick[1];
-#pragma unroll
-  for (int pass = 1; pass < 3; pass++) {
-    const int low = pass == 1 ? 10 : 0, bits = pass == 1 ? 11 : 10;
+  int left = hist[prefix], low = 21;  // keys with these leading bits; bits behind them
+  // Few keys left are ranked against one another; more (a bin of near or equal weights) are told
+  // apart by further bits first.
+  const int words = (n + 31) / 32;
+#pragma unroll 1
+  while (left > kRanked && left > want && low > 0) {
+    const int bits = low == 21 ? 11 : 10;
+    low -= bits;
+    __syncthreads();
     for (int i = tid; i < (1 << bits); i += T) hist[i] = 0;
     __syncthreads();
     for (int p = tid; p < n; p += T) {
@@ -207,24 +222,39 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
     }
     __syncthreads();
     select(1 << bits, want);
+    left = hist[pick[0]];
     prefix = prefix << bits | static_cast<uint32_t>(pick[0]);
     want = pick[1];
   }
-  const uint32_t key = prefix;  // of the slots with this key, the first `want` are kept
 
-  const bool all_ties = hist[key & 1023u] == want;
-
-  // ---- the slots as bits, a word for 32: above the key, and with it ----
-  const int words = (n + 31) / 32;
+  // ---- the slots as bits, a word for 32: above the leading bits, and with them ----
+  const bool all_ties = left == want;                      // all of the latter are kept
+  const bool ranked = !all_ties && left <= kRanked;        // the first `want` by key, then slot
+  const bool plain = all_ties || ranked;
   for (int p = tid; p < words * 32; p += T) {
-    const uint32_t k = p < n ? key_of(p) : 0u;
-    const uint32_t over = __ballot_sync(0xffffffffu, p < n && k > key), same = __ballot_sync(0xffffffffu, p < n && k == key);
-    if (lane == 0) {
-      above[p / 32] = over;
-      equal[p / 32] = same;
+    const uint32_t lead = p < n ? key_of(p) >> low : 0u;
+    const bool eq = p < n && lead == prefix;
+    const uint32_t up = __ballot_sync(0xffffffffu, p < n && (lead > prefix || (all_ties && eq)));
+    if (lane == 0) above[p / 32] = up;
+    if (!plain) {
+      const uint32_t same = __ballot_sync(0xffffffffu, eq);
+      if (lane == 0) equal[p / 32] = same;
     }
+    if (ranked && eq)  // (their order among themselves is of no matter)
+      cand[atomicAdd(&cands, 1)] = static_cast<uint64_t>(key_of(p)) << 32 | ~static_cast<uint32_t>(p);
   }
   __syncthreads();
+  if (ranked) {
+    if (tid < left) {
+      const uint64_t mine = cand[tid];  // larger: a larger key, or the same and a lower slot
+      int rank = 0;
+#pragma unroll 8
+      for (int i = 0; i < left; i++) rank += cand[i] > mine;
+      const uint32_t p = ~static_cast<uint32_t>(mine);
+      if (rank < want) atomicOr(&above[p / 32], 1u << (p & 31));
+    }
+    __syncthreads();
+  }
   // the kept ones: ties in order until enough
   auto scan = [&](int v, int *total) -> int {  // exclusive prefix sum over the CTA's threads
     int incl = v, sum;
@@ -244,8 +274,8 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
   for (int w0 = 0; w0 < words; w0 += T) {
     const int w = w0 + tid;
     uint32_t kept = 0, hole = 0, mover = 0;
-    if (w < words) kept = above[w] | (all_ties ? equal[w] : 0u);
-    if (!all_ties) {  // (block-uniform)
+    if (w < words) kept = above[w];
+    if (!plain) {  // (block-uniform) equal keys: the lowest slots
       const uint32_t same = w < words ? equal[w] : 0u;
       int total;
       int left = want - tie0 - scan(__popc(same), &total);  // ties this word may still keep
@@ -258,60 +288,90 @@ __global__ void __launch_bounds__(T) paged_evict_kernel(const EvictArgs a) {
       hole = ~kept & mask;  // (the budget is below n: all of these are slots)
       mover = kept & ~mask;
     }
-    int th, tm;
-    int hi = hole0 + scan(__popc(hole), &th), mi = mover0 + scan(__popc(mover), &tm);
-    for (; hole; hole &= hole - 1, hi++)
-      if (hi < a.list) holes[hi] = 32 * w + __ffs(hole) - 1;
-    for (; mover; mover &= mover - 1, mi++)
-      if (mi < a.list) movers[mi] = 32 * w + __ffs(mover) - 1;
+    int th, tm, hi, mi;
+    if (a.list < 65536) {  // both counts in one scan
+      int total;
+      const int v = scan(__popc(hole) | __popc(mover) << 16, &total);
+      hi = v & 0xFFFF, mi = static_cast<unsigned>(v) >> 16;
+      th = total & 0xFFFF, tm = static_cast<unsigned>(total) >> 16;
+    } else {
+      hi = scan(__popc(hole), &th), mi = scan(__popc(mover), &tm);
+    }
+    hi += hole0, mi += mover0;
+    // the lists: a warp takes its 32 words one after the other, a lane a bit
+    const int mine = min(32, words - w0 - 32 * warp);
+    for (int i = 0; i < mine; i++) {
+      const uint32_t hw = __shfl_sync(0xffffffffu, hole, i), mw = __shfl_sync(0xffffffffu, mover, i);
+      const int hb = __shfl_sync(0xffffffffu, hi, i), mb = __shfl_sync(0xffffffffu, mi, i);
+      if ((hw | mw) == 0) continue;
+      const uint32_t below = (1u << lane) - 1u;
+      const int p = 32 * (w0 + 32 * warp + i) + lane;
+      const int hx = hb + __popc(hw & below), mx = mb + __popc(mw & below);
+      if (hw >> lane & 1u && hx < a.list) holes[hx] = p;
+      if (mw >> lane & 1u && mx < a.list) movers[mx] = p;
+    }
     hole0 += th;
     mover0 += tm;
   }
   const int moves = min(min(hole0, mover0), a.list);  // (as many of the ones as of the others)
   __syncthreads();
 
-  // ---- the moves: 16 lanes per slot, M slots of each in flight.  Lanes 0 .. 7 (0 .. 3 for head dim
-  //      64) take 16 bytes of codes, half of them k's (twice for head dim 256), lanes 8 .. 11 the
-  //      group numbers, 12 the weight, 13 the token ----
-  constexpr int M = 4;
-  const int l16 = tid & 15, cv = a.code_vecs;
-  const bool codes = l16 < 8 && l16 < 2 * cv, second = codes && cv == 8;
-  const bool of_v = l16 >= (cv == 8 ? 4 : cv);
-  uint4 *const cpool = reinterpret_cast<uint4 *>(of_v ? a.kv.vc : a.kv.kc) + (of_v ? l16 - (cv == 8 ? 4 : cv) : l16);
-  __half *const mpool = l16 == 8 ? a.kv.km : l16 == 9 ? a.kv.ks : l16 == 10 ? a.kv.vm : a.kv.vs;
-  const bool nums = l16 >= 8 && l16 < 12, track = l16 == 12 || l16 == 13;
-  const uint32_t *const tsrc = l16 == 12 ? reinterpret_cast<const uint32_t *>(a.kv.weights)
-                                         : reinterpret_cast<const uint32_t *>(a.kv.tokens);
-  uint32_t *const tdst = l16 == 12 ? reinterpret_cast<uint32_t *>(a.wout) : reinterpret_cast<uint32_t *>(a.tout);
-  for (int i0 = tid / 16; i0 < moves; i0 += M * (T / 16)) {
-    int64_t dst[M];
-    uint4 x[M], y[M];
+  // ---- the moves: 16 bytes of codes at a time, and one number at a time (array by array, so that
+  //      neighbouring moves' numbers are neighbours); V and N of them in flight per thread ----
+  constexpr int V = 4, N = 3;
+  const int cv = a.code_vecs, vecs = moves * 2 * cv, nums = moves * 6;
+  const int cs = cv == 2 ? 1 : cv == 4 ? 2 : 3;  // log2(cv)
+  for (int v0 = tid, n0 = tid; v0 < vecs || n0 < nums; v0 += V * T, n0 += N * T) {
+    uint4 x[V];
+    uint4 *to[V];
 #pragma unroll
-    for (int u = 0; u < M; u++) {
-      const int i = i0 + u * (T / 16);
-      if (i >= moves) break;
-      const int64_t src = pool_slot(movers[i]);
-      dst[u] = pool_slot(holes[i]);
-      if (codes) x[u] = cpool[src * cv];
-      if (second) y[u] = cpool[src * cv + 4];
-      if (nums) {
-        if (a.meta == 4) x[u].x = reinterpret_cast<const uint32_t *>(mpool)[src];
-        else if (a.meta == 2) x[u].x = reinterpret_cast<const uint16_t *>(mpool)[src];
-        else *reinterpret_cast<uint2 *>(&x[u]) = reinterpret_cast<const uint2 *>(mpool)[src];
+    for (int u = 0; u < V; u++) {
+      const int v = v0 + u * T;
+      if (v < vecs) {
+        const int i = v >> (cs + 1), part = v & (2 * cv - 1);
+        uint4 *const pool = reinterpret_cast<uint4 *>(part >= cv ? a.kv.vc : a.kv.kc) + (part & (cv - 1));
+        to[u] = pool + pool_slot(holes[i]) * cv;
+        x[u] = pool[pool_slot(movers[i]) * cv];
       }
-      if (track) x[u].x = tsrc[src];
+    }
+    uint2 y[N];
+    void *dst[N];
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      const int k = n0 + u * T;
+      if (k < nums) {
+        const int arr = k / moves, i = k - arr * moves;
+        const int64_t src = pool_slot(movers[i]), d = pool_slot(holes[i]);
+        if (arr < 4) {
+          uint8_t *const b = reinterpret_cast<uint8_t *>(arr == 0   ? a.kv.km
+                                                         : arr == 1 ? a.kv.ks
+                                                         : arr == 2 ? a.kv.vm
+                                                                    : a.kv.vs);
+          dst[u] = b + d * a.meta;
+          if (a.meta == 4) y[u].x = *reinterpret_cast<const uint32_t *>(b + src * 4);
+          else if (a.meta == 2) y[u].x = *reinterpret_cast<const uint16_t *>(b + src * 2);
+          else y[u] = *reinterpret_cast<const uint2 *>(b + src * 8);
+        } else if (arr == 4) {
+          dst[u] = a.wout + d;
+          y[u].x = __float_as_uint(a.kv.weights[src]);
+        } else {
+          dst[u] = a.tout + d;
+          y[u].x = static_cast<uint32_t>(a.kv.tokens[src]);
+        }
+      }
     }
 #pragma unroll
-    for (int u = 0; u < M; u++) {
-      if (i0 + u * (T / 16) >= moves) break;
-      if (codes) cpool[dst[u] * cv] = x[u];
-      if (second) cpool[dst[u] * cv + 4] = y[u];
-      if (nums) {
-        if (a.meta == 4) reinterpret_cast<uint32_t *>(mpool)[dst[u]] = x[u].x;
-        else if (a.meta == 2) reinterpret_cast<uint16_t *>(mpool)[dst[u]] = static_cast<uint16_t>(x[u].x);
-        else reinterpret_cast<uint2 *>(mpool)[dst[u]] = *reinterpret_cast<const uint2 *>(&x[u]);
+    for (int u = 0; u < V; u++)
+      if (v0 + u * T < vecs) *to[u] = x[u];
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      const int k = n0 + u * T;
+      if (k < nums) {
+        const int meta = k < 4 * moves ? a.meta : 4;
+        if (meta == 4) *static_cast<uint32_t *>(dst[u]) = y[u].x;
+        else if (meta == 2) *static_cast<uint16_t *>(dst[u]) = static_cast<uint16_t>(y[u].x);
+        else *static_cast<uint2 *>(dst[u]) = y[u];
       }
-      if (track) tdst[dst[u]] = x[u].x;
     }
   }
 }
@@ -343,22 +403,23 @@ EvictPlan evict_plan(const fg_paged_kv *kv, int budget, int max_len) {
   p.wide = need > FG_EVICT_SMEM;
   p.smem = p.wide ? kBins * 4 : need;
   p.lists = p.wide ? static_cast<size_t>(kv->num_seqs) * kv->num_heads * lists : 0;
-  p.threads = limit > FG_EVICT_LONG ? 1024 : 256;
+  const int64_t items = static_cast<int64_t>(kv->num_seqs) * kv->num_heads;
+  p.threads = limit > FG_EVICT_LONG ? 1024 : items >= 8LL * fg_sm_count() ? FG_EVICT_T : 256;
   return p;
 }
 
-template <int T, bool Wide>
+template <int T, int U, int B, bool Wide>
 fg_status launch(const EvictArgs &a, const EvictPlan &p, unsigned grid, cudaStream_t st) {
   static bool done[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (!Wide && dev >= 0 && dev < 64 && !done[dev]) {
-    const fg_status rc = fg_cuda_check(cudaFuncSetAttribute(paged_evict_kernel<T, Wide>,
-                                                            cudaFuncAttributeMaxDynamicSharedMemorySize, FG_EVICT_SMEM));
+    const fg_status rc = fg_cuda_check(cudaFuncSetAttribute(
+        paged_evict_kernel<T, U, B, Wide>, cudaFuncAttributeMaxDynamicSharedMemorySize, FG_EVICT_SMEM));
     if (rc != FG_OK) return rc;
     done[dev] = true;
   }
-  paged_evict_kernel<T, Wide><<<grid, T, p.smem, st>>>(a);
+  paged_evict_kernel<T, U, B, Wide><<<grid, T, p.smem, st>>>(a);
   return fg_launch_check();
 }
 
@@ -402,9 +463,10 @@ extern "C" fg_status fg_paged_kv_evict(const fg_paged_kv *kv, const int32_t *len
   a.meta = kv->head_dim / fg_kv_group(kv->group) * 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned grid = static_cast<unsigned>(kv->num_seqs) * kv->num_heads;
-  if (p.wide) rc = launch<1024, true>(a, p, grid, st);
-  else if (p.threads == 1024) rc = launch<1024, false>(a, p, grid, st);
-  else rc = launch<256, false>(a, p, grid, st);
+  if (p.wide) rc = launch<1024, 4, 1, true>(a, p, grid, st);
+  else if (p.threads == 1024) rc = launch<1024, 4, 1, false>(a, p, grid, st);
+  else if (p.threads == 192) rc = launch<192, 3, FG_EVICT_B, false>(a, p, grid, st);
+  else rc = launch<256, 4, 1, false>(a, p, grid, st);
   if (rc != FG_OK || new_lengths != lengths) return rc;
   paged_new_lengths_kernel<<<kv->num_seqs, 128, 0, st>>>(new_lengths, kv->num_seqs, a);
   return fg_launch_check();
