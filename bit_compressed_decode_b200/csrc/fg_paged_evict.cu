@@ -120,23 +120,22 @@ __global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
   // ---- every slot once: its key, the selection's first histogram, and the numbers of the slots
   //      below the budget into their new pools (the holes' are written over below) ----
   for (int q = 4 * tid; q < n; q += 4 * U * T) {
-    int64_t slots[U];
     float4 ws[U];
     int4 ts[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int p = q + 4 * u * T;
       if (p < n) {
-        slots[u] = pool_slot(p);  // four slots of one page
-        ws[u] = *reinterpret_cast<const float4 *>(a.kv.weights + slots[u]);
-        ts[u] = *reinterpret_cast<const int4 *>(a.kv.tokens + slots[u]);
+        const int64_t slot = pool_slot(p);  // four slots of one page
+        ws[u] = *reinterpret_cast<const float4 *>(a.kv.weights + slot);
+        ts[u] = *reinterpret_cast<const int4 *>(a.kv.tokens + slot);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int p = q + 4 * u * T;
       if (p >= n) break;
-      const int64_t slot = slots[u];
+      const int64_t slot = wcopy || tcopy ? pool_slot(p) : 0;
       const float4 w = ws[u];
       const int4 t = ts[u];
       if (evicts) {
@@ -171,6 +170,18 @@ __global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
     if (!Wide) return skeys[p];
     const int64_t slot = pool_slot(p);
     return slot_key(a.kv.weights[slot], a.kv.tokens[slot], since);
+  };
+  auto keys4 = [&](int p, uint32_t (&k)[4]) {  // of slots p .. p + 3 (p < n; those behind n: anything)
+    if (!Wide) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(skeys + p);
+      k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+    } else {
+      const int64_t slot = pool_slot(p);
+      const float4 w = *reinterpret_cast<const float4 *>(a.kv.weights + slot);
+      const int4 t = *reinterpret_cast<const int4 *>(a.kv.tokens + slot);
+      k[0] = slot_key(w.x, t.x, since), k[1] = slot_key(w.y, t.y, since);
+      k[2] = slot_key(w.z, t.z, since), k[3] = slot_key(w.w, t.w, since);
+    }
   };
   // The bin of `bins` from the top that holds the want-th key, into pick; all threads.
   auto select = [&](int bins, int want) {
@@ -231,17 +242,35 @@ __global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
   const bool all_ties = left == want;                      // all of the latter are kept
   const bool ranked = !all_ties && left <= kRanked;        // the first `want` by key, then slot
   const bool plain = all_ties || ranked;
-  for (int p = tid; p < words * 32; p += T) {
-    const uint32_t lead = p < n ? key_of(p) >> low : 0u;
-    const bool eq = p < n && lead == prefix;
-    const uint32_t up = __ballot_sync(0xffffffffu, p < n && (lead > prefix || (all_ties && eq)));
-    if (lane == 0) above[p / 32] = up;
-    if (!plain) {
-      const uint32_t same = __ballot_sync(0xffffffffu, eq);
-      if (lane == 0) equal[p / 32] = same;
+  for (int p = 4 * tid; p - 4 * lane < words * 32; p += 4 * T) {  // four slots a lane, eight lanes a word
+    uint32_t k[4] = {0u, 0u, 0u, 0u};
+    if (p < n) keys4(p, k);
+    uint32_t up = 0, same = 0;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const uint32_t lead = k[e] >> low;
+      const bool in = p + e < n;
+      up |= in && lead > prefix ? 1u << e : 0u;
+      same |= in && lead == prefix ? 1u << e : 0u;
     }
-    if (ranked && eq)  // (their order among themselves is of no matter)
-      cand[atomicAdd(&cands, 1)] = static_cast<uint64_t>(key_of(p)) << 32 | ~static_cast<uint32_t>(p);
+    if (ranked)
+      for (uint32_t b = same; b; b &= b - 1) {  // (their order among themselves is of no matter)
+        const int e = __ffs(b) - 1;
+        const uint32_t key = e == 0 ? k[0] : e == 1 ? k[1] : e == 2 ? k[2] : k[3];
+        cand[atomicAdd(&cands, 1)] = static_cast<uint64_t>(key) << 32 | ~static_cast<uint32_t>(p + e);
+      }
+    if (all_ties) up |= same;
+    const uint32_t at = 4 * (lane & 7);
+    up <<= at, same <<= at;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) up |= __shfl_xor_sync(0xffffffffu, up, o);
+    if (!plain)
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) same |= __shfl_xor_sync(0xffffffffu, same, o);
+    if ((lane & 7) == 0 && p < words * 32) {
+      above[p / 32] = up;
+      if (!plain) equal[p / 32] = same;
+    }
   }
   __syncthreads();
   if (ranked) {
@@ -298,18 +327,24 @@ __global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
       hi = scan(__popc(hole), &th), mi = scan(__popc(mover), &tm);
     }
     hi += hole0, mi += mover0;
-    // the lists: a warp takes its 32 words one after the other, a lane a bit
-    const int mine = min(32, words - w0 - 32 * warp);
-    for (int i = 0; i < mine; i++) {
-      const uint32_t hw = __shfl_sync(0xffffffffu, hole, i), mw = __shfl_sync(0xffffffffu, mover, i);
-      const int hb = __shfl_sync(0xffffffffu, hi, i), mb = __shfl_sync(0xffffffffu, mi, i);
+    // the lists: the words in turn to the warps, a lane a bit (the histogram's place is free)
+    if (w < words) {
+      above[w] = mover;
+      equal[w] = hole;
+      hist[tid] = hi;
+      hist[T + tid] = mi;
+    }
+    __syncthreads();
+    const uint32_t below = (1u << lane) - 1u;
+    for (int i = warp; i < min(T, words - w0); i += W) {
+      const uint32_t hw = equal[w0 + i], mw = above[w0 + i];
       if ((hw | mw) == 0) continue;
-      const uint32_t below = (1u << lane) - 1u;
-      const int p = 32 * (w0 + 32 * warp + i) + lane;
-      const int hx = hb + __popc(hw & below), mx = mb + __popc(mw & below);
+      const int p = 32 * (w0 + i) + lane;
+      const int hx = hist[i] + __popc(hw & below), mx = hist[T + i] + __popc(mw & below);
       if (hw >> lane & 1u && hx < a.list) holes[hx] = p;
       if (mw >> lane & 1u && mx < a.list) movers[mx] = p;
     }
+    __syncthreads();
     hole0 += th;
     mover0 += tm;
   }
