@@ -48,55 +48,94 @@ struct AppendArgs {
   PagedArgs kv;
   const __half *k, *v;
   int64_t ld;
-  int rows, rows_per_seq, ng;  // ng: groups per head (head_dim / G)
+  int rows, rows_per_seq;
   const int32_t *positions, *counts, *first;
 };
 
-// One warp per (row, head): its 2 * ng groups (k and v), G/8 lanes each, 32 / (G/8) groups a step.
-template <int G>
+// A warp takes R consecutive rows of one head: a row's k and v are D/4 lanes of 8 values, all R rows
+// are loaded before the first is quantised, and the codes of consecutive slots of a page are
+// consecutive in the pool.  The group numbers (2 to 8 bytes of a row and array) go through shared
+// memory, so that a lane stores a row's of one array and the warp stores whole sectors where the
+// rows are a prompt's.
+template <int D>
+struct Append {
+  static constexpr int R = D == 256 ? 4 : 8;       // rows per warp
+  static constexpr int STEPS = R * (D / 4) / 32;   // 32 lanes of 8 values each
+};
+
+template <int D, int G>
 __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
-  constexpr int L = G / 8, USTEP = 32 / L;
-  const int lane = threadIdx.x & 31, unit = lane / L, j = lane % L;
-  const int64_t items = static_cast<int64_t>(a.rows) * a.kv.H;
-  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-  const int64_t capacity = static_cast<int64_t>(a.kv.max_pages) * a.kv.ps;
-  for (int64_t item = warp; item < items; item += nwarps) {
-    const int r = static_cast<int>(item / a.kv.H), h = static_cast<int>(item - static_cast<int64_t>(r) * a.kv.H);
-    const int s = r / a.rows_per_seq, i = r - s * a.rows_per_seq;
+  constexpr int L = G / 8, NG = D / G, R = Append<D>::R, STEPS = Append<D>::STEPS, ROW = D / 4;  // ROW: lanes of a row
+  __shared__ __align__(8) __half nums[8][4][R][NG];  // [warp][k min, k scale, v min, v scale]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  const int64_t block = tile / a.kv.H;  // heads of the same rows are neighbours
+  const int h = static_cast<int>(tile - block * a.kv.H);
+  if (block * R >= a.rows) return;
+  const int r0 = static_cast<int>(block) * R;
+  // lane i < R: where row r0 + i goes (-1: nowhere)
+  int64_t slot = -1;
+  int token = 0;
+  if (lane < R && r0 + lane < a.rows) {
+    const int r = r0 + lane, s = r / a.rows_per_seq, i = r - s * a.rows_per_seq;
     const int pos = a.positions[s], count = a.counts ? a.counts[s] : a.rows_per_seq;
-    if (pos < -1 || count < 0 || count > a.rows_per_seq) {
-      if (lane == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
-      continue;
+    const bool range = pos < -1 || count < 0 || count > a.rows_per_seq;
+    if (!range && pos >= 0 && i < count) {
+      const int64_t p = static_cast<int64_t>(pos) + i;
+      if (p < static_cast<int64_t>(a.kv.max_pages) * a.kv.ps) slot = paged_slot(a.kv, s, h, static_cast<int>(p));
+      if (slot < 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
+      token = (a.first ? a.first[s] : pos) + i;
     }
-    if (pos == -1 || i >= count) continue;
-    const int64_t p = static_cast<int64_t>(pos) + i;
-    const int64_t slot = p < capacity ? paged_slot(a.kv, s, h, static_cast<int>(p)) : -1;
-    if (slot < 0) {
-      if (lane == 0) atomicOr(a.kv.err, FG_DEVERR_RANGE);
-      continue;
-    }
-    if (lane == 0) {
-      if (a.kv.weights) a.kv.weights[slot] = 0.f;
-      if (a.kv.tokens) a.kv.tokens[slot] = (a.first ? a.first[s] : pos) + i;
-    }
-    for (int u0 = 0; u0 < 2 * a.ng; u0 += USTEP) {  // warp-uniform
-      const int u = u0 + unit, g = u >> 1;          // unit u: group u / 2 of k (even u) or v
-      const bool live = u < 2 * a.ng;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (live)
-        x = *reinterpret_cast<const uint4 *>(((u & 1) ? a.v : a.k) + static_cast<int64_t>(r) * a.ld +
-                                             (static_cast<int64_t>(h) * a.ng + g) * G + j * 8);
-      __half mn, sc;
-      const uint32_t w = quant_group8<L>(x, mn, sc);
-      if (!live) continue;
-      reinterpret_cast<uint32_t *>((u & 1) ? a.kv.vc : a.kv.kc)[(slot * a.ng + g) * L + j] = w;
-      if (j == 0) {
-        ((u & 1) ? a.kv.vm : a.kv.km)[slot * a.ng + g] = mn;
-        ((u & 1) ? a.kv.vs : a.kv.ks)[slot * a.ng + g] = sc;
-      }
+    if (range) atomicOr(a.kv.err, FG_DEVERR_RANGE);
+  }
+  if (__ballot_sync(0xffffffffu, slot >= 0) == 0) return;
+  if (slot >= 0) {
+    if (a.kv.weights) a.kv.weights[slot] = 0.f;
+    if (a.kv.tokens) a.kv.tokens[slot] = token;
+  }
+  // step st, lane: value vector e = (32 st + lane) % ROW of row (32 st + lane) / ROW; k, then v
+  uint4 x[STEPS];
+#pragma unroll
+  for (int st = 0; st < STEPS; st++) {
+    const int row = (32 * st + lane) / ROW, e = (32 * st + lane) % ROW;
+    x[st] = make_uint4(0, 0, 0, 0);
+    const bool on = __shfl_sync(0xffffffffu, slot, row) >= 0;
+    if (on)
+      x[st] = __ldcs(reinterpret_cast<const uint4 *>((e < D / 8 ? a.k : a.v) + static_cast<int64_t>(r0 + row) * a.ld +
+                                                     static_cast<int64_t>(h) * D + (e % (D / 8)) * 8));
+  }
+#pragma unroll
+  for (int st = 0; st < STEPS; st++) {
+    const int row = (32 * st + lane) / ROW, e = (32 * st + lane) % ROW, w8 = e % (D / 8);
+    const bool of_v = e >= D / 8;
+    __half mn, sc;
+    const uint32_t w = quant_group8<L>(x[st], mn, sc);
+    const int64_t to = __shfl_sync(0xffffffffu, slot, row);
+    if (to >= 0) reinterpret_cast<uint32_t *>(of_v ? a.kv.vc : a.kv.kc)[to * (D / 8) + w8] = w;
+    if (w8 % L == 0) {
+      nums[warp][of_v ? 2 : 0][row][w8 / L] = mn;
+      nums[warp][of_v ? 3 : 1][row][w8 / L] = sc;
     }
   }
+  __syncwarp();
+  const int arr = lane / R, row = lane % R;
+  const int64_t to = __shfl_sync(0xffffffffu, slot, row);
+  if (arr < 4 && to >= 0) {
+    __half *const pool = arr == 0 ? a.kv.km : arr == 1 ? a.kv.ks : arr == 2 ? a.kv.vm : a.kv.vs;
+    const __half *const src = nums[warp][arr][row];
+    if constexpr (NG == 1) pool[to] = src[0];
+    else if constexpr (NG == 2) reinterpret_cast<uint32_t *>(pool)[to] = *reinterpret_cast<const uint32_t *>(src);
+    else reinterpret_cast<uint2 *>(pool)[to] = *reinterpret_cast<const uint2 *>(src);
+  }
+}
+
+template <int D, int G>
+fg_status append(const AppendArgs &a, cudaStream_t st) {
+  constexpr int R = Append<D>::R;
+  const int64_t tiles = (static_cast<int64_t>(a.rows) + R - 1) / R * a.kv.H, grid = (tiles + 7) / 8;
+  if (grid > INT32_MAX) return FG_ERR_SHAPE;
+  paged_append_kernel<D, G><<<static_cast<unsigned>(grid), 256, 0, st>>>(a);
+  return fg_launch_check();
 }
 
 }  // namespace
@@ -131,14 +170,21 @@ extern "C" fg_status fg_paged_kv_append(const fg_paged_kv *kv, const fg_half *k,
   a.ld = ld;
   a.rows = rows;
   a.rows_per_seq = rows_per_seq;
-  a.ng = kv->head_dim / G;
   a.positions = positions;
   a.counts = row_counts;
   a.first = first_tokens;
-  const int64_t blocks = (static_cast<int64_t>(rows) * kv->num_heads + 7) / 8, most = 8LL * fg_sm_count();
-  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (G == 64) paged_append_kernel<64><<<grid, 256, 0, st>>>(a);
-  else paged_append_kernel<128><<<grid, 256, 0, st>>>(a);
-  return fg_launch_check();
+  if (G == 64) {
+    switch (kv->head_dim) {
+      case 64: return append<64, 64>(a, st);
+      case 128: return append<128, 64>(a, st);
+      case 256: return append<256, 64>(a, st);
+    }
+  } else {
+    switch (kv->head_dim) {
+      case 128: return append<128, 128>(a, st);
+      case 256: return append<256, 128>(a, st);
+    }
+  }
+  return FG_ERR_UNSUPPORTED;
 }
