@@ -339,7 +339,7 @@ class PagedKVCache:
                 if a.numel() != math.prod(sh) or a.device != dev:
                     raise ValueError(f"cache pool: expected {tuple(sh)} on {dev}, got {tuple(a.shape)} on {a.device}")
         self.num_pages, self.num_heads, self.head_dim, self.page_size = num_pages, num_heads, head_dim, page_size
-        self.group, self.device = group, dev
+        self.group, self.device, self._index = group, dev, page_table.get_device()
         self.num_seqs, self.max_pages = page_table.shape
         self.k_codes, self.k_mins, self.k_scales, self.v_codes, self.v_mins, self.v_scales = arrays
         self.weights, self.tokens, self.page_table = weights, tokens, page_table
@@ -365,55 +365,70 @@ class PagedKVCache:
         return sum(a.numel() * a.element_size() for a in self.arrays() + [self.weights, self.tokens] if a is not None)
 
 
-class _On:
-    """The device of a paged cache and the stream of a call: the caller's, or that device's current
-    one.  Memory that a call allocates belongs to that stream."""
-
-    def __init__(self, cache: PagedKVCache, stream):
-        self.dev, self.other = cache.device, cache.device.index != torch.cuda.current_device()
-        self.stream = torch.cuda.current_stream(cache.device) if stream is None else stream
-        if self.stream.device != cache.device:
-            raise ValueError(f"stream on {self.stream.device}, cache on {cache.device}")
-        self.own = stream is None
-        self.ptr = c_void_p(self.stream.cuda_stream)
-
-    def empty(self, shape, dtype):
-        if self.own:
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.dev)
-
-    def call(self, fn, *args) -> None:
-        if self.other:
-            with torch.cuda.device(self.dev):
-                rc = fn(*args)
-                if rc != 0:
-                    raise FgError(rc, fn.__name__)
-            return
-        rc = fn(*args)
-        if rc != 0:
-            raise FgError(rc, fn.__name__)
+# The paged calls take a few microseconds of host time each, which is what a small launch costs: one
+# comparison per property of a tensor, plain integers for pointers, no objects per call.
+_get_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t: torch.Tensor, cache: PagedKVCache, name: str, width: int | None = None) -> None:
-    if t.dtype != torch.float16 or t.dim() != 2 or t.device != cache.device or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected float16 rows of unit element stride on {cache.device}")
-    if width is not None and t.shape[1] != width:
-        raise ValueError(f"{name}: expected rows of {width} values, got {t.shape[1]}")
+def _rows(t: torch.Tensor, cache: PagedKVCache, name: str, width: int | None = None) -> int:
+    """Checks fp16 rows of unit element stride on the cache's device; their stride."""
+    if t.dtype is not torch.float16 or t.dim() != 2 or t.get_device() != cache._index:
+        raise ValueError(f"{name}: expected float16 rows on {cache.device}, got {t.dtype} on {t.device}")
+    n, m = t.shape
+    ld, one = t.stride()
+    if one != 1 and m > 1:
+        raise ValueError(f"{name}: expected rows of unit element stride")
+    if width is not None and m != width:
+        raise ValueError(f"{name}: expected rows of {width} values, got {m}")
+    return ld if n > 1 else max(ld, m)  # (a single row's stride says nothing)
 
 
-def _ints(t, cache: PagedKVCache, name: str, n: int) -> None:
-    if t is not None and (t.dtype != torch.int32 or t.device != cache.device or not t.is_contiguous() or t.numel() < n):
+def _ints(t, cache: PagedKVCache, name: str, n: int):
+    """Checks an int32 array on the cache's device; its address (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.get_device() != cache._index or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{name}: expected at least {n} contiguous int32 on {cache.device}")
+    return t.data_ptr()
 
 
-def _stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _ws(t, cache: PagedKVCache) -> None:
-    if t is not None and (t.device != cache.device or not t.is_contiguous()):
+def _scratch(t, need, cache: PagedKVCache, stream):
+    """(address, bytes, tensor) of a call's workspace: the caller's, or memory of the call's stream."""
+    if t is None:
+        n = need()
+        if n == 0:
+            return None, 0, None
+        t = _on_stream(cache, stream, (n,), torch.uint8)
+    elif t.get_device() != cache._index or not t.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous tensor on {cache.device}")
+    return t.data_ptr(), t.numel() * t.element_size(), t
+
+
+def _on_stream(cache: PagedKVCache, stream, shape, dtype) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+
+
+def _paged_call(fn, cache: PagedKVCache, stream, *args) -> None:
+    """Calls fn(cache, *args, stream) with the cache's device current."""
+    if stream is None:
+        st = _raw_stream(cache._index)
+    elif stream.device != cache.device:
+        raise ValueError(f"stream on {stream.device}, cache on {cache.device}")
+    else:
+        st = stream.cuda_stream
+    if _get_device() == cache._index:
+        rc = fn(cache._ref, *args, st)
+        if rc:
+            raise FgError(rc, fn.__name__)
+    else:
+        with torch.cuda.device(cache._index):  # (the library's error text is the device's own)
+            rc = fn(cache._ref, *args, st)
+            if rc:
+                raise FgError(rc, fn.__name__)
 
 
 def fg_paged_kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -423,17 +438,13 @@ def fg_paged_kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, po
     ``positions[s] + i`` (see fg.h for row_counts, first_tokens and inactive sequences)."""
     rows = k.shape[0]
     width = cache.num_heads * cache.head_dim
-    _rows(k, cache, "k", width)
-    _rows(v, cache, "v", width)
-    if v.shape[0] != rows or (rows > 1 and k.stride(0) != v.stride(0)):
+    ld = _rows(k, cache, "k", width)
+    if _rows(v, cache, "v", width) != ld or v.shape[0] != rows:
         raise ValueError("k and v must share their shape and a row stride")
     n = -(-rows // max(1, rows_per_seq))
-    _ints(positions, cache, "positions", n)
-    _ints(row_counts, cache, "row_counts", n)
-    _ints(first_tokens, cache, "first_tokens", n)
-    on = _On(cache, stream)
-    on.call(_lib.fg_paged_kv_append, cache._ref, _ptr(k), _ptr(v), _stride(k), rows, rows_per_seq, _ptr(positions),
-            _ptr(row_counts), _ptr(first_tokens), on.ptr)
+    _paged_call(_lib.fg_paged_kv_append, cache, stream, k.data_ptr(), v.data_ptr(), ld, rows, rows_per_seq,
+                _ints(positions, cache, "positions", n), _ints(row_counts, cache, "row_counts", n),
+                _ints(first_tokens, cache, "first_tokens", n))
 
 
 def fg_paged_attention_workspace_bytes(cache: PagedKVCache, num_q_heads: int, rows: int, rows_per_seq: int = 1,
@@ -448,32 +459,36 @@ def fg_paged_attention(cache: PagedKVCache, q: torch.Tensor, positions: torch.Te
                        stream=None) -> torch.Tensor:
     """Attention of q [rows, num_q_heads * head_dim] over the cache; ``accumulate=True`` adds each
     slot's probabilities to ``cache.weights``.  ``workspace``: None allocates it."""
-    rows = q.shape[0]
-    _rows(q, cache, "q")
-    hq = q.shape[1] // cache.head_dim
-    if hq * cache.head_dim != q.shape[1]:
-        raise ValueError(f"q: rows of {q.shape[1]} values are no whole heads of {cache.head_dim}")
+    ldq = _rows(q, cache, "q")
+    rows, width = q.shape
+    hq = width // cache.head_dim
+    if hq * cache.head_dim != width:
+        raise ValueError(f"q: rows of {width} values are no whole heads of {cache.head_dim}")
     n = -(-rows // max(1, rows_per_seq))
-    _ints(positions, cache, "positions", n)
-    _ints(row_counts, cache, "row_counts", n)
-    on = _On(cache, stream)
     if out is None:
-        out = on.empty(q.shape, torch.float16)
-    _rows(out, cache, "out", q.shape[1])
+        out = _on_stream(cache, stream, q.shape, torch.float16)
+    ldo = _rows(out, cache, "out", width)
     if out.shape[0] != rows:
         raise ValueError(f"out: expected {rows} rows")
-    if workspace is None:
-        need = fg_paged_attention_workspace_bytes(cache, hq, rows, rows_per_seq, max_len, accumulate)
-        workspace = on.empty(need, torch.uint8) if need else None
-    _ws(workspace, cache)
-    on.call(_lib.fg_paged_attention, cache._ref, _ptr(q), _stride(q), hq, _ptr(out), _stride(out), rows, rows_per_seq,
-            _ptr(positions), _ptr(row_counts), max_len or 0, int(accumulate), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), on.ptr)
+    ws, nbytes, _keep = _scratch(workspace, lambda: fg_paged_attention_workspace_bytes(
+        cache, hq, rows, rows_per_seq, max_len, accumulate), cache, stream)
+    _paged_call(_lib.fg_paged_attention, cache, stream, q.data_ptr(), ldq, hq, out.data_ptr(), ldo, rows, rows_per_seq,
+                _ints(positions, cache, "positions", n), _ints(row_counts, cache, "row_counts", n), max_len or 0,
+                1 if accumulate else 0, ws, nbytes)
     return out
 
 
 def fg_paged_kv_evict_workspace_bytes(cache: PagedKVCache, budget: int, max_len: int | None = None) -> int:
     return int(_lib.fg_paged_kv_evict_workspace_bytes(cache._ref, budget, max_len or 0))
+
+
+def _pool_like(t, like, name: str):
+    if t is None:
+        return None
+    if like is None or t.dtype is not like.dtype or t.get_device() != like.get_device() or t.numel() != like.numel() or \
+            not t.is_contiguous():
+        raise ValueError(f"{name}: expected a pool like the cache's own")
+    return t.data_ptr()
 
 
 def fg_paged_kv_evict(cache: PagedKVCache, lengths: torch.Tensor, next_tokens: torch.Tensor, budget: int,
@@ -483,23 +498,14 @@ def fg_paged_kv_evict(cache: PagedKVCache, lengths: torch.Tensor, next_tokens: t
     """Evict every sequence's heads down to ``budget`` slots: the last ``recent`` tokens, then the
     largest weights.  Returns the new lengths."""
     n = cache.num_seqs
-    _ints(lengths, cache, "lengths", n)
-    _ints(next_tokens, cache, "next_tokens", n)
-    on = _On(cache, stream)
     if new_lengths is None:
-        new_lengths = on.empty(n, torch.int32)
-    _ints(new_lengths, cache, "new_lengths", n)
-    for t, like, name in ((weights_out, cache.weights, "weights_out"), (tokens_out, cache.tokens, "tokens_out")):
-        if t is not None and (like is None or t.dtype != like.dtype or t.device != like.device or
-                              t.numel() != like.numel() or not t.is_contiguous()):
-            raise ValueError(f"{name}: expected a pool like the cache's own")
-    if workspace is None:
-        need = fg_paged_kv_evict_workspace_bytes(cache, budget, max_len)
-        workspace = on.empty(need, torch.uint8) if need else None
-    _ws(workspace, cache)
-    on.call(_lib.fg_paged_kv_evict, cache._ref, _ptr(lengths), _ptr(next_tokens), budget, recent, max_len or 0,
-            _ptr(new_lengths), _ptr(weights_out), _ptr(tokens_out), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), on.ptr)
+        new_lengths = _on_stream(cache, stream, (n,), torch.int32)
+    ws, nbytes, _keep = _scratch(workspace, lambda: fg_paged_kv_evict_workspace_bytes(cache, budget, max_len), cache,
+                                 stream)
+    _paged_call(_lib.fg_paged_kv_evict, cache, stream, _ints(lengths, cache, "lengths", n),
+                _ints(next_tokens, cache, "next_tokens", n), budget, recent, max_len or 0,
+                _ints(new_lengths, cache, "new_lengths", n), _pool_like(weights_out, cache.weights, "weights_out"),
+                _pool_like(tokens_out, cache.tokens, "tokens_out"), ws, nbytes)
     return new_lengths
 
 

@@ -94,24 +94,28 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
     if (a.kv.tokens) a.kv.tokens[slot] = token;
   }
   // step st, lane: value vector e = (32 st + lane) % ROW of row (32 st + lane) / ROW; k, then v
+  constexpr int PER = STEPS > R ? STEPS / R : 1;  // steps of a row
   uint4 x[STEPS];
+  int64_t to[STEPS / PER];
+  const int e0 = lane % ROW;
+  const __half *const ksrc = a.k + static_cast<int64_t>(r0) * a.ld + static_cast<int64_t>(h) * D;
+  const __half *const vsrc = a.v + static_cast<int64_t>(r0) * a.ld + static_cast<int64_t>(h) * D;
 #pragma unroll
   for (int st = 0; st < STEPS; st++) {
-    const int row = (32 * st + lane) / ROW, e = (32 * st + lane) % ROW;
+    const int row = (32 * st + lane) / ROW, e = PER == 1 ? e0 : (32 * st + lane) % ROW;
+    if (st % PER == 0) to[st / PER] = __shfl_sync(0xffffffffu, slot, row);
     x[st] = make_uint4(0, 0, 0, 0);
-    const bool on = __shfl_sync(0xffffffffu, slot, row) >= 0;
-    if (on)
-      x[st] = __ldcs(reinterpret_cast<const uint4 *>((e < D / 8 ? a.k : a.v) + static_cast<int64_t>(r0 + row) * a.ld +
-                                                     static_cast<int64_t>(h) * D + (e % (D / 8)) * 8));
+    if (to[st / PER] >= 0)
+      x[st] = __ldcs(reinterpret_cast<const uint4 *>((e < D / 8 ? ksrc : vsrc) + row * a.ld + (e % (D / 8)) * 8));
   }
 #pragma unroll
   for (int st = 0; st < STEPS; st++) {
-    const int row = (32 * st + lane) / ROW, e = (32 * st + lane) % ROW, w8 = e % (D / 8);
+    const int row = (32 * st + lane) / ROW, e = PER == 1 ? e0 : (32 * st + lane) % ROW, w8 = e % (D / 8);
     const bool of_v = e >= D / 8;
     __half mn, sc;
     const uint32_t w = quant_group8<L>(x[st], mn, sc);
-    const int64_t to = __shfl_sync(0xffffffffu, slot, row);
-    if (to >= 0) reinterpret_cast<uint32_t *>(of_v ? a.kv.vc : a.kv.kc)[to * (D / 8) + w8] = w;
+    if (to[st / PER] >= 0)
+      reinterpret_cast<uint32_t *>(of_v ? a.kv.vc : a.kv.kc)[to[st / PER] * (D / 8) + w8] = w;
     if (w8 % L == 0) {
       nums[warp][of_v ? 2 : 0][row][w8 / L] = mn;
       nums[warp][of_v ? 3 : 1][row][w8 / L] = sc;
@@ -119,13 +123,13 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const AppendArgs a) {
   }
   __syncwarp();
   const int arr = lane / R, row = lane % R;
-  const int64_t to = __shfl_sync(0xffffffffu, slot, row);
-  if (arr < 4 && to >= 0) {
+  const int64_t mine = __shfl_sync(0xffffffffu, slot, row);
+  if (arr < 4 && mine >= 0) {
     __half *const pool = arr == 0 ? a.kv.km : arr == 1 ? a.kv.ks : arr == 2 ? a.kv.vm : a.kv.vs;
     const __half *const src = nums[warp][arr][row];
-    if constexpr (NG == 1) pool[to] = src[0];
-    else if constexpr (NG == 2) reinterpret_cast<uint32_t *>(pool)[to] = *reinterpret_cast<const uint32_t *>(src);
-    else reinterpret_cast<uint2 *>(pool)[to] = *reinterpret_cast<const uint2 *>(src);
+    if constexpr (NG == 1) pool[mine] = src[0];
+    else if constexpr (NG == 2) reinterpret_cast<uint32_t *>(pool)[mine] = *reinterpret_cast<const uint32_t *>(src);
+    else reinterpret_cast<uint2 *>(pool)[mine] = *reinterpret_cast<const uint2 *>(src);
   }
 }
 
