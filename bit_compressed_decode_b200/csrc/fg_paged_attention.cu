@@ -387,45 +387,34 @@ __device__ __forceinline__ void grow_by(float4 *add, const float *scores, int t,
 }
 
 // The weights of a single-column item's slots begin .. end - 1, once its maximum and 1 / sum are
-// known, by `n` threads of which this is number i: four slots at a time, four times before any is written, so that the table's and the pools'
-// latencies are paid once for 16 slots.
+// known, by `n` threads of which this is number i.
 __device__ __forceinline__ void grow_row(const PagedAttnArgs &a, int s, int h, const float *scores, int begin, int end,
                                          float m, float inv, int i, int n) {
-  constexpr int U = 4;
-  for (int t0 = begin + 4 * i; t0 < end; t0 += 4 * U * n) {
-    int64_t slot[U];
-    float4 v[U], w[U];
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int t = t0 + 4 * u * n;
-      slot[u] = -1;
-      if (t < end) {
-        slot[u] = paged_slot(a.kv, s, h, t);
-        v[u] = *reinterpret_cast<const float4 *>(scores + t);  // (behind `end`: anything, not used)
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; u++)
-      if (slot[u] >= 0) w[u] = *reinterpret_cast<const float4 *>(a.kv.weights + slot[u]);
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int t = t0 + 4 * u * n;
-      if (slot[u] < 0) continue;
-      float *dst = a.kv.weights + slot[u];
-      w[u].x += fast_exp2(v[u].x - m) * inv;
-      w[u].y += fast_exp2(v[u].y - m) * inv;
-      w[u].z += fast_exp2(v[u].z - m) * inv;
-      w[u].w += fast_exp2(v[u].w - m) * inv;
-      if (t + 3 < end) {
-        *reinterpret_cast<float4 *>(dst) = w[u];
-      } else {  // the slots behind stay as they are
-        dst[0] = w[u].x;
-        if (t + 1 < end) dst[1] = w[u].y;
-        if (t + 2 < end) dst[2] = w[u].z;
-      }
-    }
+  for (int t = begin + 4 * i; t < end; t += 4 * n) {
+    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+    grow_by(&add, scores, t, end, m, inv);
+    grow4(a, s, h, t, end, add);
   }
 }
+
+// A slot's numbers of one array (its groups' minima, or scales), loaded at once.
+template <int NG>
+struct Nums {
+  uint32_t w[(NG + 1) / 2];
+  __device__ __forceinline__ explicit Nums(const __half *p) {
+    if constexpr (NG == 1) w[0] = *reinterpret_cast<const uint16_t *>(p);
+    else if constexpr (NG == 2) w[0] = *reinterpret_cast<const uint32_t *>(p);
+    else {
+      const uint2 v = *reinterpret_cast<const uint2 *>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ float get(int g) const {
+    const __half2 h = *reinterpret_cast<const __half2 *>(&w[g / 2]);
+    return g & 1 ? __high2float(h) : __low2float(h);
+  }
+};
 
 // The B operands of 8 dims of q (v), for the low and the high nibbles.  A high nibble counts 16 times
 // what a low one does in its place, so the low nibbles' q is taken 16 times (exact), unless a value
@@ -605,6 +594,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     float sc[NT][2][2][2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
+      const __half *const n0 = nbase + OFF / 2 + 16 * u * NG, *const n1 = n0 + 8 * NG;
+      const Nums<NG> km[2] = {Nums<NG>(n0), Nums<NG>(n1)};
+      const Nums<NG> ks[2] = {Nums<NG>(n0 + kBlock * NG), Nums<NG>(n1 + kBlock * NG)};
 #pragma unroll
       for (int g = 0; g < NG; g++) {
         uint32_t k0[KW], k1[KW];
@@ -629,14 +621,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         }
 #pragma unroll
         for (int x = 0; x < 2; x++) {
-          const __half *n = nbase + OFF / 2 + (16 * u + 8 * x) * NG + g;
-          const float mn = __half2float(n[0]), ks = __half2float(n[kBlock * NG]);
+          const float mn = km[x].get(g), sl = ks[x].get(g);
 #pragma unroll
           for (int nt = 0; nt < NT; nt++)
 #pragma unroll
             for (int e = 0; e < 2; e++) {
               const float v = g == 0 ? mn * qsum[nt][e][g] : fmaf(mn, qsum[nt][e][g], sc[nt][u][x][e]);
-              sc[nt][u][x][e] = fmaf(ks, lo[nt][2 * x + e] + hi[nt][2 * x + e], v);
+              sc[nt][u][x][e] = fmaf(sl, lo[nt][2 * x + e] + hi[nt][2 * x + e], v);
             }
         }
       }
@@ -721,12 +712,14 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
             l[nt][e] += p[nt][x][e];
           }
       uint32_t b[NT][NG][2];
+      const __half *const n0 = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG, *const n1 = n0 + 8 * NG;
+      const Nums<NG> vm[2] = {Nums<NG>(n0), Nums<NG>(n1)};
+      const Nums<NG> vsc[2] = {Nums<NG>(n0 + kBlock * NG), Nums<NG>(n1 + kBlock * NG)};
 #pragma unroll
       for (int g = 0; g < NG; g++) {
 #pragma unroll
         for (int x = 0; x < 2; x++) {
-          const __half *n = nbase + OFF / 2 + (2 * kBlock + 16 * u + 8 * x) * NG + g;
-          const float vs = __half2float(n[kBlock * NG]), vb = __half2float(n[0]) + 7.5f * vs;
+          const float vs = vsc[x].get(g), vb = vm[x].get(g) + 7.5f * vs;
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
             float w0 = p[nt][x][0] * vs, w1 = p[nt][x][1] * vs, o0 = p[nt][x][0] * vb, o1 = p[nt][x][1] * vb;
@@ -1390,12 +1383,6 @@ void plan_bytes(Plan *p, int64_t items, int D, int limit, bool accumulate) {
   p->total = p->ml + p->po + p->parts + p->cut + p->scores;
 }
 
-#ifndef FG_ENOUGH
-#define FG_ENOUGH 2LL
-#endif
-#ifndef FG_DIRECT
-#define FG_DIRECT 1024
-#endif
 // Accumulating launches take the column tiles one after the other, so that a slot's weight is grown
 // by one CTA at a time and in a fixed order.
 Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate, int64_t *items) {
@@ -1407,7 +1394,9 @@ Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate
   *items = pairs * (accumulate ? 1 : p.tiles);
   const int warps = per_sm * kWarps * fg_sm_count();
   const bool many = *items >= 4LL * warps;
-  p.units = limit <= FG_DIRECT || (*items >= FG_ENOUGH * (warps / kWarps) && limit <= 4096) ? 0 : warps;
+  const int sms = fg_sm_count();
+  const bool direct = limit <= 1024 || (limit <= 2048 && *items >= sms) || (limit <= 4096 && *items >= 8LL * sms);
+  p.units = direct ? 0 : warps;
   p.shared_unit = !p.units && !many;
   plan_bytes(&p, *items, D, limit, accumulate);
   return p;
