@@ -97,9 +97,9 @@ struct Item {
 
 __device__ __forceinline__ Item load_item(const PagedAttnArgs &a, int s, int ht, bool flag) {
   Item it;
-  const int tile = a.tile0 + ht % a.tiles;
+  it.h = a.tiles == 1 ? ht : ht / a.tiles;
+  const int tile = a.tile0 + ht - it.h * a.tiles;
   it.s = s;
-  it.h = ht / a.tiles;
   it.n0 = tile * a.pcols;
   it.ncols = min(a.pcols, a.rows_per_seq * a.R - it.n0);
   const int pos = a.positions[it.s], count = a.counts ? a.counts[it.s] : a.rows_per_seq;
@@ -119,16 +119,30 @@ __device__ __forceinline__ int seq_blocks(const PagedAttnArgs &a, int s) {
 }
 
 // A warp's way through its share of the work.  Partitioned launches lay the blocks of all items in
-// a row (sequence, then head and tile, then block) and cut it into `units` equal runs, at most one
-// for every kMinBlocks blocks: a run is up to two parts of cut items, the first and the last, with
+// a row (sequence, then head and tile, then block) and cut it into `units` runs that differ by a
+// block at most, no more than one for every kMinBlocks blocks: a run is up to two parts of cut items, the first and the last, with
 // whole items in between.  A part is number 2 * unit + 1 if it begins its item, else 2 * unit.
 constexpr int kMinBlocks = FG_MIN_BLOCKS;
 
-struct Walk {
-  int s, ht, b, nblk;      // at block b of head and tile ht of sequence s, which has nblk blocks
-  int64_t g, end, total;   // place in the row of all blocks
-  int units;
+// x / d; the 64-bit division only where 32 bits do not hold x (both are not negative, d > 0).
+__device__ __forceinline__ int64_t divide(int64_t x, int d) {
+  return x <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
+}
 
+struct Walk {
+  int s, ht, b, nblk;  // at block b of head and tile ht of sequence s, which has nblk blocks
+  int longer;          // the units 0 .. longer - 1 have one block more than `per`
+  int64_t per, g, end; // place in the row of all blocks, and where this unit's run ends
+
+  __device__ __forceinline__ int64_t start_of(int unit) const { return unit * per + min(unit, longer); }
+  __device__ __forceinline__ int unit_of(int64_t block) const {
+    const int64_t head = longer * (per + 1);
+    const int64_t x = block < head ? block : block - head;
+    const int64_t d = block < head ? per + 1 : per;
+    const int64_t u = x <= 0xFFFFFFFFll && d <= 0xFFFFFFFFll
+                          ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
+    return static_cast<int>(block < head ? u : longer + u);
+  }
   __device__ __forceinline__ bool begin(const PagedAttnArgs &a, int unit, int lane) {
     const int HT = a.kv.H * a.tiles;
     if (!a.units) {
@@ -142,12 +156,14 @@ struct Walk {
     for (int i = lane; i < a.seqs; i += 32) sum += seq_blocks(a, i);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    total = sum * HT;
+    const int64_t total = sum * HT;
     const int64_t most = (total + kMinBlocks - 1) / kMinBlocks;
-    units = static_cast<int>(most < a.units ? most : a.units);
+    const int units = static_cast<int>(most < a.units ? most : a.units);
     if (unit >= units) return false;
-    g = unit * total / units;
-    end = (unit + 1) * total / units;
+    per = divide(total, units);
+    longer = static_cast<int>(total - per * units);
+    g = start_of(unit);
+    end = start_of(unit + 1);
     nblk = 0;
     int64_t base = 0;  // blocks of one head and tile before the chunk of 32 sequences
     for (int i = 0; i < a.seqs; i += 32) {
@@ -170,7 +186,7 @@ struct Walk {
     }
     if (nblk == 0) return false;
     const int64_t rest = g - base * HT;
-    ht = static_cast<int>(rest / nblk);
+    ht = static_cast<int>(divide(rest, nblk));
     b = static_cast<int>(rest - static_cast<int64_t>(ht) * nblk);
     return true;
   }
@@ -190,9 +206,6 @@ struct Walk {
       } while (nblk == 0);
     }
     return true;
-  }
-  __device__ __forceinline__ int unit_of(int64_t block) const {
-    return static_cast<int>(((block + 1) * units - 1) / total);
   }
 };
 
@@ -230,10 +243,15 @@ __device__ __forceinline__ Target target_of(const PagedAttnArgs &a, const Walk &
   t.whole = !a.units || ran == w.nblk;
   t.index = 2 * static_cast<int64_t>(unit) + (w.b == 0);
   if (a.units && leader) {
-    const int64_t g0 = w.g - w.b, g1 = g0 + w.nblk;
-    if (w.b == 0) a.cut[item] = t.whole ? make_int2(-1, -1) : make_int2(unit, w.unit_of(g1 - 1));
-    if (a.scores && !t.whole)
-      a.parts[t.index] = Part{item, w.unit_of(g0), w.unit_of(g1 - 1), w.b * kBlock, (w.b + ran) * kBlock};
+    if (t.whole) {
+      a.cut[item] = make_int2(-1, -1);
+    } else {
+      const int64_t g0 = w.g - w.b;
+      const int u1 = w.b == 0 || a.scores ? w.unit_of(g0 + w.nblk - 1) : 0;
+      if (w.b == 0) a.cut[item] = make_int2(unit, u1);
+      if (a.scores)
+        a.parts[t.index] = Part{item, w.b == 0 ? unit : w.unit_of(g0), u1, w.b * kBlock, (w.b + ran) * kBlock};
+    }
   }
   return t;
 }
@@ -500,7 +518,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     }
   }
   const int ran = a.units ? walk.run() : 0;
-  const Target target = target_of(a, walk, unit, item, ran, lane == 0);
   const int t_begin = a.units ? walk.b * kBlock : 0;
   const int t_end = a.units ? min(lmax, t_begin + ran * kBlock) : lmax;
   const int t_first = t_begin + first * kBlock;
@@ -511,6 +528,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     cp.issue(0, 0, bar0, lane);
     if (steps > 1) cp.issue(1, S::STAGE_B, bar0 + 8, lane);
   }
+  const Target target = target_of(a, walk, unit, item, ran, lane == 0);
 
   // ---- q of column n0 + 8 nt + gid as the B operand of the score MMAs ----
   // Word j of group g of lane class c: dims 2o .. 2o+7, o = g*G/2 + c*G/8 + 4j.  Low-nibble MMA
@@ -526,12 +544,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     const bool on = col < it.ncols && it.len(n, a.R) > 0;
     const __half *qrow = a.q + (static_cast<int64_t>(it.s) * a.rows_per_seq + n / a.R) * a.ldq +
                          (static_cast<int64_t>(it.h) * a.R + n % a.R) * D;
+    uint4 v[NG][KW];
     bool big = false;
-    if (on)
 #pragma unroll
-      for (int g = 0; g < NG; g++)
+    for (int g = 0; g < NG; g++)
 #pragma unroll
-        for (int j = 0; j < KW; j++) big |= q_big(*reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j));
+      for (int j = 0; j < KW; j++) {
+        v[g][j] = make_uint4(0, 0, 0, 0);
+        if (on) v[g][j] = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
+        big |= q_big(v[g][j]);
+      }
     big = __ballot_sync(0xffffffffu, big) >> (4 * gid) & 15u;
     const float unit_of_gid = q_unit(big) * kLog2e;
     qunit[nt][0] = __shfl_sync(0xffffffffu, unit_of_gid, 8 * c);
@@ -541,10 +563,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < KW; j++) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (on) v = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
-        const __half *e = reinterpret_cast<const __half *>(&v);
-        q_operands(qf[nt][g][j], v, big);
+        const __half *e = reinterpret_cast<const __half *>(&v[g][j]);
+        q_operands(qf[nt][g][j], v[g][j], big);
 #pragma unroll
         for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
       }
@@ -789,8 +809,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     if (a.shared_unit) bad_page = 1;
   }
 
-  // ---- this warp's columns: their totals, and their outputs into its (drained) stages ----
-  float *const wo = reinterpret_cast<float *>(wbase);  // [NC][D]
+  // ---- this warp's columns: totals, and outputs ----
+  float *const wo = reinterpret_cast<float *>(wbase);  // [NC][D], in the (drained) stages, for the join below
+  const bool good_warp = ok && !any_bad;
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
@@ -806,48 +827,53 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         red_m[warp][n] = m[nt][e];
         red_l[warp][n] = l[nt][e];
       }
-      if (n < it.ncols) {
+      if (n >= it.ncols) continue;
+      const int cn = it.n0 + n;
+      const float inv = len[nt][e] > 0 && good_warp ? 1.0f / l[nt][e] : 0.f;
+      const int64_t pi = target.index * NC + n;
+      if (!a.shared_unit && !target.whole && gid == 0) a.ml[pi] = make_float2(m[nt][e], good_warp ? l[nt][e] : -1.f);
+      __half *const orow = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
+                           (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + 4 * gid;
 #pragma unroll
-        for (int ch = 0; ch < CH; ch++) {
-          const float base = vacc[nt][e][ch * 32 / G] - 7.5f * wacc[nt][ch * 32 / G][e];
-          float v[4];
+      for (int ch = 0; ch < CH; ch++) {
+        const float base = vacc[nt][e][ch * 32 / G] - 7.5f * wacc[nt][ch * 32 / G][e];
+        float v[4];
 #pragma unroll
-          for (int x = 0; x < 2; x++) {
-            v[2 * x + 1] = ov[nt][ch][x][2 + e] * kS20;
-            v[2 * x] = ov[nt][ch][x][e] * kS24 - 16.f * v[2 * x + 1];
-          }
-          *reinterpret_cast<float4 *>(wo + n * D + ch * 32 + 4 * gid) =
-              make_float4(v[0] + base, v[1] + base, v[2] + base, v[3] + base);
+        for (int x = 0; x < 2; x++) {
+          v[2 * x + 1] = ov[nt][ch][x][2 + e] * kS20;
+          v[2 * x] = ov[nt][ch][x][e] * kS24 - 16.f * v[2 * x + 1] + base;
+          v[2 * x + 1] += base;
+        }
+        if (a.shared_unit) {
+          *reinterpret_cast<float4 *>(wo + n * D + ch * 32 + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
+        } else if (!target.whole) {
+          *reinterpret_cast<float4 *>(a.po + pi * D + ch * 32 + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+          uint2 r = make_uint2(0u, 0u);  // (a row that sees nothing, or a bad page: zero, whatever v is)
+          if (inv != 0.f) r = make_uint2(pack_h2(v[0] * inv, v[1] * inv), pack_h2(v[2] * inv, v[3] * inv));
+          *reinterpret_cast<uint2 *>(orow + ch * 32) = r;
         }
       }
     }
   }
-  // ---- the unit's warps joined: all four of the CTA, or this one ----
-  bool good;
-  if (a.shared_unit) {
-    good = __syncthreads_and(ok) && !bad_page;
-  } else {
-    __syncwarp();
-    good = ok && !any_bad;
-  }
+  bool good = good_warp;
   const int w0 = a.shared_unit ? 0 : warp, w1 = a.shared_unit ? kWarps : warp + 1;
   const int me = a.shared_unit ? tid : lane, all = a.shared_unit ? kWarps * 32 : 32;
-  for (int i = me; i < it.ncols * (D / 4); i += all) {
-    const int n = i / (D / 4), d = 4 * (i % (D / 4));
-    float M = -INFINITY, den = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = w0; w < w1; w++) M = fmaxf(M, red_m[w][n]);
-    for (int w = w0; w < w1; w++) {
-      const float f = red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M);
-      const float4 v = *reinterpret_cast<const float4 *>(smem + w * S::WARP_B + (n * D + d) * 4);
-      den += f * red_l[w][n];
-      if (f != 0.f) o = make_float4(o.x + f * v.x, o.y + f * v.y, o.z + f * v.z, o.w + f * v.w);
-    }
-    const int64_t pi = target.index * NC + n;
-    if (!target.whole) {
-      if (d == 0) a.ml[pi] = make_float2(M, good ? den : -1.f);
-      *reinterpret_cast<float4 *>(a.po + pi * D + d) = o;
-    } else {
+  if (a.shared_unit) {  // the CTA's warps joined
+    good = __syncthreads_and(ok) && !bad_page;
+    for (int i = tid; i < it.ncols * (D / 4); i += kWarps * 32) {
+      const int n = i / (D / 4), d = 4 * (i % (D / 4));
+      float M = -INFINITY, den = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) M = fmaxf(M, red_m[w][n]);
+#pragma unroll
+      for (int w = 0; w < kWarps; w++) {
+        const float f = red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M);
+        const float4 v = *reinterpret_cast<const float4 *>(smem + w * S::WARP_B + (n * D + d) * 4);
+        den += f * red_l[w][n];
+        if (f != 0.f) o = make_float4(o.x + f * v.x, o.y + f * v.y, o.z + f * v.z, o.w + f * v.w);
+      }
       const int cn = it.n0 + n;
       const float inv = 1.0f / den;
       uint2 r = make_uint2(0u, 0u);
@@ -855,6 +881,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
       *reinterpret_cast<uint2 *>(a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
                                  (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + d) = r;
     }
+  } else {
+    __syncwarp();
   }
   if (TRACK && target.whole && good) {  // the unit saw whole rows: its slots' weights
     for (int i = 4 * me; i < lmax; i += 4 * all) {
@@ -950,7 +978,6 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   const int s = walk.s, h = walk.ht, item = s * a.kv.H + h;
   const int len = load_item(a, s, h, !a.units && first == 0 && lane == 0).len(0, 1);
   const int ran = a.units ? walk.run() : 0;
-  const Target target = target_of(a, walk, unit, item, ran, lane == 0);
   const int t_begin = a.units ? walk.b * kBlock : 0;
   const int t_end = a.units ? min(len, t_begin + ran * kBlock) : len;
   const int t_first = t_begin + first * kBlock;
@@ -961,6 +988,7 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     cp.issue(0, 0, bar0, lane);
     if (steps > 1) cp.issue(1, S::STAGE_B, bar0 + 8, lane);
   }
+  const Target target = target_of(a, walk, unit, item, ran, lane == 0);
 
   // ---- q as the B operand; word j of lane class c: dims 2o .. 2o+7 ----
   const __half *qrow = a.q + static_cast<int64_t>(s) * a.ldq + static_cast<int64_t>(h) * D;
@@ -1253,31 +1281,57 @@ __device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, int n, int u0,
 constexpr int kJoinWarps = 8;
 constexpr int kMaxCols = 16;  // columns per item: at most two tiles
 
-// One column's parts joined into its output row by `n` warps, of which this is number w: V dims a
-// lane.  M, inv: the column's maximum and 1 / sum.
+// A column's parts number w, w + warps, .. joined by a warp, V dims a lane: their maximum and sum
+// (sum < 0: a bad page among them) and outputs.  Parts are read four at a time.
 template <int D>
-__device__ __forceinline__ void join_parts(const PagedAttnArgs &a, int n, int u0, int u1, float M, int w, int warps,
-                                           float (&o)[D / 32]) {
-  constexpr int V = D / 32;
+__device__ __forceinline__ float2 join_parts(const PagedAttnArgs &a, int n, int u0, int u1, int w, int warps,
+                                             float (&o)[D / 32]) {
+  constexpr int V = D / 32, U = 4;
   const int lane = threadIdx.x & 31;
+  float M = -INFINITY, den = 0.f;
+  bool bad = false;
 #pragma unroll
   for (int e = 0; e < V; e++) o[e] = 0.f;
-#pragma unroll 4
-  for (int u = u0 + w; u <= u1; u += warps) {
-    const int64_t pi = (2 * static_cast<int64_t>(u) + (u == u0)) * a.pcols + n;
-    const float x = a.ml[pi].x;
-    const float f = x == -INFINITY ? 0.f : exp2f(x - M);
-    const float *p = a.po + pi * D + lane * V;
-    float v[V];
-    if constexpr (V == 2) {
-      *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(p);
-    } else {
+  for (int u = u0 + w; u <= u1; u += U * warps) {
+    float2 t[U];
+    float v[U][V];
 #pragma unroll
-      for (int e = 0; e < V; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(p + e);
+    for (int i = 0; i < U; i++) {
+      const int x = u + i * warps;
+      t[i] = make_float2(-INFINITY, 0.f);
+      if (x <= u1) {
+        const int64_t pi = (2 * static_cast<int64_t>(x) + (x == u0)) * a.pcols + n;
+        t[i] = a.ml[pi];
+        const float *p = a.po + pi * D + lane * V;
+        if constexpr (V == 2) {
+          *reinterpret_cast<float2 *>(v[i]) = *reinterpret_cast<const float2 *>(p);
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; e += 4) *reinterpret_cast<float4 *>(v[i] + e) = *reinterpret_cast<const float4 *>(p + e);
+        }
+      }
     }
+    float mx = M;
 #pragma unroll
-    for (int e = 0; e < V; e++) o[e] += f == 0.f ? 0.f : f * v[e];
+    for (int i = 0; i < U; i++) {
+      mx = fmaxf(mx, t[i].x);
+      bad |= t[i].y < 0.f;
+    }
+    const float keep = M == -INFINITY ? 0.f : exp2f(M - mx);
+    den *= keep;
+#pragma unroll
+    for (int e = 0; e < V; e++) o[e] *= keep;
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+      if (t[i].x == -INFINITY) continue;  // a part that saw nothing of the column
+      const float f = exp2f(t[i].x - mx);
+      den += f * t[i].y;
+#pragma unroll
+      for (int e = 0; e < V; e++) o[e] += f * v[i][e];
+    }
+    M = mx;
   }
+  return make_float2(M, bad ? -1.f : den);
 }
 
 template <int V>
@@ -1299,6 +1353,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
   constexpr int V = D / 32;  // dims per lane
   __shared__ float2 col[2][kMaxCols];
   __shared__ float part[kJoinWarps][D];
+  __shared__ float2 part_ml[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, HT = a.kv.H * a.tiles;
   if (static_cast<int>(blockIdx.x) < out_blocks) {
     const int i = wide ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
@@ -1310,23 +1365,43 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     griddep_wait();
     const int2 c = it.live ? a.cut[item] : make_int2(0, 0);
     if (c.x < 0) return;
-    const float2 t = it.len(cn, a.R) > 0 ? join_ml(a, n, c.x, c.y) : make_float2(0.f, 0.f);
-    const float inv = t.y != 0.f ? 1.0f / t.y : 0.f;
     float o[V];
+    float2 t = make_float2(-INFINITY, 0.f);
 #pragma unroll
     for (int e = 0; e < V; e++) o[e] = 0.f;
-    if (t.y != 0.f) join_parts<D>(a, n, c.x, c.y, t.x, wide ? warp : 0, wide ? kJoinWarps : 1, o);
+    const bool sees = it.len(cn, a.R) > 0;
+    if (sees) t = join_parts<D>(a, n, c.x, c.y, wide ? warp : 0, wide ? kJoinWarps : 1, o);
     __half *const dst = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
                         (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D;
-    if (wide) {
+    if (wide && sees) {
 #pragma unroll
       for (int e = 0; e < V; e++) part[warp][lane * V + e] = o[e];
+      if (lane == 0) part_ml[warp] = t;
       __syncthreads();
       if (warp > 0) return;
-      for (int w = 1; w < kJoinWarps; w++)
+      float M = -INFINITY, den = 0.f;
+      bool bad = false;
 #pragma unroll
-        for (int e = 0; e < V; e++) o[e] += part[w][lane * V + e];
+      for (int w = 0; w < kJoinWarps; w++) M = fmaxf(M, part_ml[w].x);
+#pragma unroll
+      for (int e = 0; e < V; e++) o[e] = 0.f;
+      for (int w = 0; w < kJoinWarps; w++) {
+        bad |= part_ml[w].y < 0.f;
+        if (part_ml[w].x == -INFINITY) continue;
+        const float f = exp2f(part_ml[w].x - M);
+        den += f * part_ml[w].y;
+#pragma unroll
+        for (int e = 0; e < V; e++) o[e] += f * part[w][lane * V + e];
+      }
+      t = make_float2(M, bad ? -1.f : den);
+    } else if (wide && warp > 0) {
+      return;
     }
+    const bool good = sees && !(t.y < 0.f);
+    if (!good)
+#pragma unroll
+      for (int e = 0; e < V; e++) o[e] = 0.f;
+    const float inv = good ? 1.0f / t.y : 0.f;
     store_row<V>(dst + lane * V, o, inv);
     return;
   }
@@ -1454,8 +1529,8 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int cols, bool accumulate, cuda
     const int left = cols - r * p.pcols, out_cols = left < p.pcols ? left : p.pcols;
     // a programmatic dependent: its blocks start while the last units run and wait for them
     cudaLaunchConfig_t lc = {};
-    // few columns have many parts each
-    const bool wide = a.items * out_cols <= 16 * fg_sm_count();
+    // few items have many parts each
+    const bool wide = p.units >= 16LL * a.items;
     const int out_blocks = wide ? a.items * out_cols : (a.items * out_cols + kJoinWarps - 1) / kJoinWarps;
     lc.gridDim = dim3(out_blocks + (accumulate ? p.units : 0));
     lc.blockDim = dim3(kJoinWarps * 32);
