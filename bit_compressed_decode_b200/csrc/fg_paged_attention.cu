@@ -5,14 +5,19 @@
 // "FlexGen Guide: High-Throughput LLM Offloading on One GPU", section 3: the KV cache is held as
 // 4-bit groups and dequantised on the fly for the attention dot products.
 //
-// The query rows of a sequence that share a key-value head -- its new tokens' rows times the query
-// heads of the head's group -- are columns of one product.  A tile is 8 of them, the width of an
-// mma.sync n8 operand: with more than one live column the codes are read and unpacked once for all.
-// A CTA takes one (sequence, key-value head, column tile) over C slots of the sequence; its four
-// warps take 32-slot blocks in turn, each with a pipeline of its own: kStages blocks of codes and
-// group numbers in flight by bulk copies (cp.async.bulk), an mbarrier per stage, and no barrier of
-// the CTA before the end.  A block lies in one or two pages (page_size % 16 == 0), six copies each,
-// issued by as many lanes; the lanes look the table up for 32 blocks at a time.
+// Bound: the cache's bytes (D + 8 D/G per slot and key-value head: 144 for heads of 128 in groups
+// of 64).  The query rows of a sequence that share a key-value head -- its new tokens' rows times
+// the query heads of the head's group -- are columns of one product, 8 (the width of an mma.sync n8
+// operand) or two times 8 to a tile, so that the codes are read and unpacked once for all of them.
+// One column alone has a kernel of its own (below).
+//
+// Work is cut in blocks of 32 slots of one (sequence, key-value head, column tile), an item.  A warp
+// streams its blocks through two stages of its own shared memory by bulk copies (cp.async.bulk, an
+// mbarrier per stage) and meets no other warp before it is done.  A block lies in one or two pages
+// (page_size % 16 == 0), six copies each, issued by as many lanes; the lanes look the page table up
+// for 32 blocks at a time.  Two unrolled stages measured 210 us where three in a ring, whose
+// addresses are computed, took 219 (512 sequences of 513 to 544 slots, 32 heads of 128: 1.26 GB,
+// 5.97 TB/s of 6.46 measured for a copy).  Which warp takes which blocks: make_plan below.
 //
 // Both products run on the tensor cores straight from the codes (the group decomposition):
 //     q . k_t = sum_g ( min_tg * sum_{d in g} q_d  +  scale_tg * sum_{d in g} q_d c_td )
@@ -20,14 +25,17 @@
 // with w_tg = p_t scale_tg rounded to fp16, the operand's type.  The last term, one more MMA per
 // group with an operand of ones, takes back what the rounding of w has in common for all codes, so
 // that an error of w weighs |c - 7.5| instead of c.  A nibble left in bits 0-3 of a 16-bit half is
-// the fp16 subnormal c * 2^-24, one in bits 4-7 is c * 2^-20, both exact: an AND per pair of codes
-// unpacks them, and the fp32 results are rescaled by the power of two.  Scores, softmax state and
-// sums are fp32.
+// the fp16 subnormal c * 2^-24, one in bits 4-7 is c * 2^-20, a whole byte (lo + 16 hi) * 2^-24, all
+// exact: an AND per pair of codes unpacks them, and the fp32 results are rescaled by the power of
+// two.  Scores, softmax state and sums are fp32.
 //   scores: A = codes of 16 slots x 16 dims of one group, B = q (16 dims x 8 columns)
-//   output: A = codes of 16 dims x 16 slots, B = w of the dims' group (16 slots x 8 columns), which
-//           is the score tile's layout transposed (movmatrix)
+//   output: A = codes of 16 dims x 16 slots (ldmatrix.trans), B = w of the dims' group (16 slots x 8
+//           columns), which is the score tile's layout transposed (movmatrix)
 // Both score and output fragments give a lane the columns 2c, 2c+1 (c = lane % 4), so the softmax
-// state of a column never leaves its lanes.
+// state of a column never leaves its lanes.  What the tile kernel costs beyond the bytes is the
+// fixed part of a launch (7 us from its start to the first block's arrival, 6 us of join) and, for D
+// = 256, instructions: 24 sequences of 8192 slots and 8 heads of 8 columns take 57 us of which the
+// blocks themselves take 41, 5.2 TB/s.
 #include <math.h>
 
 #include <type_traits>
@@ -40,24 +48,20 @@ constexpr int kWarps = 4;
 constexpr int kBlock = 32;              // slots per warp step
 constexpr int kCta = kWarps * kBlock;   // slots per CTA step
 constexpr int kCols = 8;                // columns per tile
-#ifndef FG_MIN_BLOCKS
-#define FG_MIN_BLOCKS 4
-#endif
-#ifndef FG_CTAS
-#define FG_CTAS 3
-#endif
-#ifndef FG_NT2
-#define FG_NT2 1
-#endif
-#ifndef FG_ONE_CTAS
-#define FG_ONE_CTAS 4
-#endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 2.0f;
 constexpr uint32_t kLoNib = 0x000F000Fu;  // bits 0-3 of both halves: c * 2^-24
 constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves: c * 2^-20
 constexpr uint32_t kByte = 0x00FF00FFu;   // both nibbles of the low byte: (lo + 16 hi) * 2^-24
 constexpr uint32_t kOnes = 0x3C003C00u;   // fp16 {1, 1}
+
+// CTAs (of four warps) resident per SM, which is what the register budgets are cut for.  Tile kernel:
+// 168 registers a thread hold one tile of D <= 128 without spills (at 128, four CTAs, the three
+// tracked sequences of the benchmark took 69 us instead of 58); two tiles, or D = 256, need 255.
+// Single-column kernel: 128 registers (five CTAs spill: 236 us instead of 210 for 512 sequences of
+// 513 to 544 slots and 32 heads of 128).
+__host__ __device__ constexpr int tile_ctas(int D, int cols) { return cols <= kCols && D <= 128 ? 3 : 2; }
+__host__ __device__ constexpr int one_ctas(int D) { return D <= 128 ? 4 : 3; }
 
 struct Part {  // a unit's part of a cut item: the units that have it, the part's slots
   int item, u0, u1, t0, t1;
@@ -122,7 +126,7 @@ __device__ __forceinline__ int seq_blocks(const PagedAttnArgs &a, int s) {
 // a row (sequence, then head and tile, then block) and cut it into `units` runs that differ by a
 // block at most, no more than one for every kMinBlocks blocks: a run is up to two parts of cut items, the first and the last, with
 // whole items in between.  A part is number 2 * unit + 1 if it begins its item, else 2 * unit.
-constexpr int kMinBlocks = FG_MIN_BLOCKS;
+constexpr int kMinBlocks = 4;
 
 // x / d; the 64-bit division only where 32 bits do not hold x (both are not negative, d > 0).
 __device__ __forceinline__ int64_t divide(int64_t x, int d) {
@@ -266,7 +270,7 @@ struct Shape {
   static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
   static constexpr int WARP_B = 2 * STAGE_B > NT * kCols * D * 4 ? 2 * STAGE_B : NT * kCols * D * 4;
   static constexpr int SMEM = kWarps * WARP_B;  // a warp's two stages, at the end its outputs
-  static constexpr int kCtas = NT == 1 && D <= 128 ? FG_CTAS : 2;
+  static constexpr int kCtas = tile_ctas(D, NT * kCols);
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -622,7 +626,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         uint32_t k0[KW], k1[KW];
         load_words<KW>(kbase + OFF + 16 * u * RB + g * (G / 2), k0);
         load_words<KW>(kbase + OFF + (16 * u + 8) * RB + g * (G / 2), k1);
-        float lo[NT][4], hi[NT][4];  // two chains of MMAs: their latency bounds a warp
+        float lo[NT][4], hi[NT][4];  // two chains of MMAs
 #pragma unroll
         for (int j = 0; j < KW; j++) {
           const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
@@ -912,8 +916,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
 //           operand: columns 0-3 for slots 0-7 of the 16, columns 4-7 for slots 8-15.
 // A = V codes transposed comes from ldmatrix.trans on 16-bit elements (4 codes of a slot): a lane
 // gets two slots' codes of dims 4 gid .. 4 gid + 3, in operand order.
-// Units: with many items a warp takes a whole split of one item and no two warps ever meet;
-// otherwise the CTA's four warps share a unit, 32-slot blocks in turn, and join at the end.
 // ------------------------------------------------------------------------------------------------
 template <int D, int G>
 struct One {
@@ -925,7 +927,7 @@ struct One {
   static constexpr int STAGE_B = 2 * CODE_B + 4 * META_B;
   static constexpr int WARP_B = 2 * STAGE_B;  // two stages; >= D * 4, the warp's outputs at the end
   static constexpr int SMEM = kWarps * WARP_B;
-  static constexpr int kCtas = D <= 128 ? FG_ONE_CTAS : 3;
+  static constexpr int kCtas = one_ctas(D);
 };
 
 template <int D, int G, bool TRACK>
@@ -1065,7 +1067,7 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
           k1[j] = y.x, k1[j + 1] = y.y, k1[j + 2] = y.z, k1[j + 3] = y.w;
         }
       }
-      float lo[4], hi[4];  // two chains of MMAs: their latency bounds a warp
+      float lo[4], hi[4];  // two chains of MMAs
 #pragma unroll
       for (int j = 0; j < KW; j++) {
         const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
@@ -1458,14 +1460,21 @@ void plan_bytes(Plan *p, int64_t items, int D, int limit, bool accumulate) {
   p->total = p->ml + p->po + p->parts + p->cut + p->scores;
 }
 
+// Direct launches (units = 0) give an item to a CTA, or to a warp once there are several items for
+// each resident one, and write its rows at once.  Partitioned launches run one wave of warps that
+// share all blocks evenly (Walk) and a join.  Direct is for short items, and for somewhat longer
+// ones where there are many: 30 sequences of 2000 slots and 32 heads of 128 took 58.8 us direct and
+// 62.3 partitioned, 8 of them 23.9 and 26.0, one 21.4 and 19.5; 64 tracked ones of 1500 to 2112
+// slots 120 and 133; 24 ragged ones of up to 16384 slots and 8 shared heads 95 and 79.
+// Two column tiles to an item halve the unpacking: 8 heads of 64 with 16 columns 77 us instead of 89.
 // Accumulating launches take the column tiles one after the other, so that a slot's weight is grown
 // by one CTA at a time and in a fixed order.
 Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate, int64_t *items) {
   Plan p;
   p.one = cols == 1 && D / G <= 2;
-  p.pcols = p.one ? 1 : cols > kCols && D <= 128 && FG_NT2 ? 2 * kCols : kCols;
+  p.pcols = p.one ? 1 : cols > kCols && D <= 128 ? 2 * kCols : kCols;
   p.tiles = (cols + p.pcols - 1) / p.pcols;
-  const int per_sm = p.one ? (D <= 128 ? FG_ONE_CTAS : 3) : p.pcols > kCols || D > 128 ? 2 : FG_CTAS;
+  const int per_sm = p.one ? one_ctas(D) : tile_ctas(D, p.pcols);
   *items = pairs * (accumulate ? 1 : p.tiles);
   const int warps = per_sm * kWarps * fg_sm_count();
   const bool many = *items >= 4LL * warps;

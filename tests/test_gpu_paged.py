@@ -497,12 +497,14 @@ def test_evict_ranks(what):
     check_evict(c, lengths, nxt, budget, 24)
 
 
-@pytest.mark.parametrize("n,budget", [(20000, 1024), (9000, 8000), (40000, 39999), (5000, 16)])
-def test_evict_long(n, budget):
+@pytest.mark.parametrize("weights", ["ties", "apart"])
+@pytest.mark.parametrize("n,budget", [(20000, 1024), (9000, 8000), (40000, 39999), (5000, 16), (70001, 30000)])
+def test_evict_long(n, budget, weights):
     rng = np.random.default_rng(n)
     c = make_cache(rng, [n, 100], 1, 64, 64, 64, track=True)
     tokens_in_order(c, [n, 100])
-    c.weights.copy_(torch.round(c.weights * 2000))                      # many ties
+    if weights == "ties":
+        c.weights.copy_(torch.round(c.weights * 2000))
     check_evict(c, [n, 100], [n, 100], budget, min(budget, 128), max_len=n)
 
 
@@ -533,7 +535,74 @@ def test_evict_flags_bad_sequences_only():
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+def test_evict_workspace():
+    """More slots than a CTA's shared memory holds: scratch is asked for, and refused without."""
+    c = make_cache(np.random.default_rng(2), [100, 100], 1, 64, 64, 64, track=True)
+    assert fg.fg_paged_kv_evict_workspace_bytes(c, 64) == 0
+    wide = fg.PagedKVCache(c.num_pages, 1, 64, 64, torch.zeros((2, 4000), dtype=torch.int32, device="cuda"),
+                           arrays=c.arrays(), weights=c.weights, tokens=c.tokens)
+    n = torch.tensor([100, -1], dtype=torch.int32, device="cuda")
+    assert fg.fg_paged_kv_evict_workspace_bytes(wide, 64) > 0
+    with pytest.raises(fg.FgError, match="WORKSPACE"):
+        fg.fg_paged_kv_evict(wide, n, n, 64, 0, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert fg.fg_paged_kv_evict_workspace_bytes(wide, 64, max_len=1000) == 0
+
+
 # ------------------------------------------------------------------ together ----------
+
+
+def test_pools_past_32_bits():
+    """Pages whose bytes lie past 2^32 of their pool: the same bits as a small pool's."""
+    rng = np.random.default_rng(77)
+    H, D, ps, lengths = 2, 256, 256, [700, 3000]
+    small = make_cache(rng, lengths, H, D, 64, ps, track=True)
+    pages = (2**32 + 2**24) // (H * ps * (D // 2))                      # of codes alone
+    if torch.cuda.mem_get_info()[0] < 3 * pages * H * ps * (D + 72):
+        pytest.skip("not enough device memory")
+    shift = pages - small.num_pages
+    big = [torch.empty((pages,) + a.shape[1:], dtype=a.dtype, device="cuda") for a in small.arrays() + [small.weights, small.tokens]]
+    for x, y in zip(big, small.arrays() + [small.weights, small.tokens]):
+        x[shift:] = y
+    t = small.page_table
+    table = torch.where((t >= 0) & (t < small.num_pages), t + shift, t)
+    c = fg.PagedKVCache(pages, H, D, ps, table, arrays=big[:6], weights=big[6], tokens=big[7])
+    q = queries(rng, 2, 3 * H, D)
+    kv = queries(rng, 2, H, D, 16.0)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    got = []
+    for k in (small, c):
+        o = fg.fg_paged_attention(k, q, i32([n - 1 for n in lengths]), accumulate=True)
+        fg.fg_paged_kv_append(k, kv, kv, i32([n - 1 for n in lengths]))
+        new = fg.fg_paged_kv_evict(k, i32(lengths), i32(lengths), 512, 100)
+        fg.fg_sync_status()
+        got.append((o, new, [a[-small.num_pages:].clone() for a in k.arrays() + [k.weights, k.tokens]]))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    for x, y in zip(got[0][2], got[1][2]):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("R,rows,limit", [(1, 1, 300), (1, 1, 6000), (3, 2, 300), (3, 2, 6000)])
+def test_first_call_captured_and_many_sequences(R, rows, limit):
+    """Many ragged sequences, most of them short or out, captured at once; the plan's bound far above the lengths."""
+    rng = np.random.default_rng(limit + R)
+    lengths = [int(x) for x in rng.integers(0, 60, 150)] + [290]
+    pos = [n - rows if n >= rows else -1 for n in lengths]
+    c = make_cache(rng, lengths, 1, 64, 64, 16, track=True)
+    q = queries(rng, len(lengths) * rows, R, 64)
+    p = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    w0 = c.weights.clone()
+    ws = torch.empty(fg.fg_paged_attention_workspace_bytes(c, R, len(lengths) * rows, rows, limit, True), dtype=torch.uint8,
+                     device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fg.fg_paged_attention(c, q, p, rows_per_seq=rows, max_len=limit, accumulate=True, out=out, workspace=ws)
+    g.replay()
+    fg.fg_sync_status()
+    w1 = c.weights.clone()
+    c.weights.copy_(w0)
+    assert torch.equal(out, check_attention(c, q, pos, rows, max_len=limit, accumulate=True))
+    assert torch.equal(c.weights, w1)
 
 
 def step(c, qkv, H, R, D, pos, first, out, ws, stream=None):
