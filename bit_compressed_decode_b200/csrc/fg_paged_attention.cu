@@ -592,8 +592,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
 
   float m[NT][2], l[NT][2];
   float vacc[NT][2][NG];   // sum of p (min + 7.5 scale) over this lane's slots
-  float ov[NT][CH][2][4];  // chunk ch, x: dims 32 ch + 4 gid + 2x (row gid, with 16 times the next) and + 1
-  float wacc[NT][NG][4];   // every row: sum of w
+  float ov[NT][CH][2][4];  // chunk ch, x: dims 32 ch + 4 gid + 2x ([0], [1]: columns 2c, 2c+1) and + 1 ([2], [3])
+  float wacc[NT][NG][2];   // sum of w
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
     m[nt][0] = m[nt][1] = -INFINITY;
@@ -601,8 +601,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
 #pragma unroll
     for (int g = 0; g < NG; g++) {
       vacc[nt][0][g] = vacc[nt][1][g] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; e++) wacc[nt][g][e] = 0.f;
+      wacc[nt][g][0] = wacc[nt][g][1] = 0.f;
     }
 #pragma unroll
     for (int i = 0; i < CH; i++)
@@ -711,8 +710,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         for (int g = 0; g < NG; g++) {
           vacc[nt][0][g] *= al[0];
           vacc[nt][1][g] *= al[1];
-#pragma unroll
-          for (int i = 0; i < 4; i++) wacc[nt][g][i] *= al[i & 1];
+          wacc[nt][g][0] *= al[0];
+          wacc[nt][g][1] *= al[1];
         }
 #pragma unroll
         for (int ch = 0; ch < CH; ch++)
@@ -722,7 +721,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
             for (int i = 0; i < 4; i++) ov[nt][ch][x][i] *= al[i & 1];
       }
     }
-    // ---- p, the sums, and the output product ----
+    // ---- p and the sums ----
+    uint32_t b[2][NT][NG][2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
       float p[NT][2][2];
@@ -735,12 +735,11 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
             p[nt][x][e] = EDGE && sc[nt][u][x][e] == -INFINITY ? 0.f : fast_exp2(fmaf(sc[nt][u][x][e], qunit[nt][e], -m[nt][e]));
             l[nt][e] += p[nt][x][e];
           }
-      uint32_t b[NT][NG][2];
       const __half *const n0 = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG, *const n1 = n0 + 8 * NG;
       const Nums<NG> vm[2] = {Nums<NG>(n0), Nums<NG>(n1)};
       const Nums<NG> vsc[2] = {Nums<NG>(n0 + kBlock * NG), Nums<NG>(n1 + kBlock * NG)};
 #pragma unroll
-      for (int g = 0; g < NG; g++) {
+      for (int g = 0; g < NG; g++)
 #pragma unroll
         for (int x = 0; x < 2; x++) {
           const float vs = vsc[x].get(g), vb = vm[x].get(g) + 7.5f * vs;
@@ -753,31 +752,54 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
             }
             vacc[nt][0][g] += o0;
             vacc[nt][1][g] += o1;
-            b[nt][g][x] = transpose_8x8(pack_h2(w0, w1));
+            b[u][nt][g][x] = transpose_8x8(pack_h2(w0, w1));
           }
         }
+    }
+    // ---- the output product: a block's MMAs start from zero and are added in fp32 registers (the
+    //      tensor core's own additions truncate, and what they lose grows with the sum) ----
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) mma_f16(wacc[nt][g], kOnes, kOnes, kOnes, kOnes, b[nt][g][0], b[nt][g][1]);
+    for (int g = 0; g < NG; g++)
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++) {
+        float d[4];
+        mma_f16_z(d, kOnes, kOnes, kOnes, kOnes, b[0][nt][g][0], b[0][nt][g][1]);
+        mma_f16(d, kOnes, kOnes, kOnes, kOnes, b[1][nt][g][0], b[1][nt][g][1]);
+        wacc[nt][g][0] += d[0];
+        wacc[nt][g][1] += d[1];
       }
 #pragma unroll
-      for (int ch = 0; ch < CH; ch += 2) {
-        uint32_t r[4];  // slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
-        ldmatrix_x4_trans(r, vbase + OFF + 16 * u * RB + ch * 16);
-        const int g = ch * 32 / G;
+    for (int ch = 0; ch < CH; ch += 2) {
+      uint32_t r[2][4];  // [u]: slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
+      ldmatrix_x4_trans(r[0], vbase + OFF + ch * 16);
+      ldmatrix_x4_trans(r[1], vbase + OFF + 16 * RB + ch * 16);
+      const int g = ch * 32 / G;
 #pragma unroll
-        for (int y = 0; y < 2; y++) {
+      for (int y = 0; y < 2; y++)
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
           // rows gid take both nibbles of a byte, lo + 16 hi (<= 255, exact), rows gid + 8 the high one
-          const uint32_t P = r[2 * y], Q = r[2 * y + 1];
-          const uint32_t Pb = __byte_perm(P, 0u, 0x4341), Qb = __byte_perm(Q, 0u, 0x4341);
-          const uint32_t Pl = P & kByte, Ph = P & kHiNib, Ql = Q & kByte, Qh = Q & kHiNib;
-          const uint32_t Pbh = Pb & kHiNib, Qbh = Qb & kHiNib;
+          uint32_t lo[2][2], hi[2][2];
+#pragma unroll
+          for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int z = 0; z < 2; z++) {
+              const uint32_t w = r[u][2 * y + z];
+              lo[u][z] = x ? __byte_perm(w, 0u, 0x4341) : w & kByte;
+              hi[u][z] = (x ? lo[u][z] : w) & kHiNib;
+            }
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
-            mma_f16(ov[nt][ch + y][0], Pl, Ph, Ql, Qh, b[nt][g][0], b[nt][g][1]);
-            mma_f16(ov[nt][ch + y][1], Pb, Pbh, Qb, Qbh, b[nt][g][0], b[nt][g][1]);
+            float d[4];
+            mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][nt][g][0], b[0][nt][g][1]);
+            mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], b[1][nt][g][0], b[1][nt][g][1]);
+            float(&o)[4] = ov[nt][ch + y][x];
+            o[0] += d[0] - d[2];  // 16 hi 2^-24 = hi 2^-20
+            o[1] += d[1] - d[3];
+            o[2] += d[2];
+            o[3] += d[3];
           }
         }
-      }
     }
   };
 
@@ -844,9 +866,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         float v[4];
 #pragma unroll
         for (int x = 0; x < 2; x++) {
-          v[2 * x + 1] = ov[nt][ch][x][2 + e] * kS20;
-          v[2 * x] = ov[nt][ch][x][e] * kS24 - 16.f * v[2 * x + 1] + base;
-          v[2 * x + 1] += base;
+          v[2 * x] = ov[nt][ch][x][e] * kS24 + base;
+          v[2 * x + 1] = ov[nt][ch][x][2 + e] * kS20 + base;
         }
         if (a.shared_unit) {
           *reinterpret_cast<float4 *>(wo + n * D + ch * 32 + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
@@ -1041,11 +1062,11 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
 
   float m = -INFINITY, l = 0.f, vacc = 0.f;
-  float ov[CH][2][4];
+  float ov[CH][2][2];  // chunk ch, x: dims 32 ch + 4 gid + 2x and + 1
 #pragma unroll
   for (int i = 0; i < CH; i++)
 #pragma unroll
-    for (int x = 0; x < 2; x++) ov[i][x][0] = ov[i][x][1] = ov[i][x][2] = ov[i][x][3] = 0.f;
+    for (int x = 0; x < 2; x++) ov[i][x][0] = ov[i][x][1] = 0.f;
 
   // one block of 32 slots at t, in stage ST; EDGE: some of them are not seen
   auto block = [&](auto stage, auto edge, int t) {
@@ -1106,10 +1127,12 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
 #pragma unroll
       for (int i = 0; i < CH; i++)
 #pragma unroll
-        for (int x = 0; x < 2; x++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) ov[i][x][e] *= al;
+        for (int x = 0; x < 2; x++) {
+          ov[i][x][0] *= al;
+          ov[i][x][1] *= al;
+        }
     }
+    uint32_t b[2][2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
       const __half *n = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG;
@@ -1122,20 +1145,37 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
       uint32_t wp = pack_h2(w, w - __half2float(__float2half_rn(w)));
       if (NG == 1 && (c & 1)) wp = 0u;
       const uint32_t wt = transpose_8x8(wp);
-      const uint32_t b0 = gid < 4 ? wt : 0u, b1 = gid < 4 ? 0u : wt;
+      b[u][0] = gid < 4 ? wt : 0u;
+      b[u][1] = gid < 4 ? 0u : wt;
+    }
+    // the block's MMAs start from zero and are added in fp32 registers (the tensor core's own
+    // additions truncate, and what they lose grows with the sum)
 #pragma unroll
-      for (int ch = 0; ch < CH; ch += 2) {
-        uint32_t r[4];  // slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
-        ldmatrix_x4_trans(r, vbase + OFF + 16 * u * RB + ch * 16);
+    for (int ch = 0; ch < CH; ch += 2) {
+      uint32_t r[2][4];  // [u]: slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
+      ldmatrix_x4_trans(r[0], vbase + OFF + ch * 16);
+      ldmatrix_x4_trans(r[1], vbase + OFF + 16 * RB + ch * 16);
 #pragma unroll
-        for (int y = 0; y < 2; y++) {
+      for (int y = 0; y < 2; y++)
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
           // rows gid take both nibbles of a byte, lo + 16 hi (<= 255, exact), rows gid + 8 the high one
-          const uint32_t P = r[2 * y], Q = r[2 * y + 1];
-          const uint32_t Pb = __byte_perm(P, 0u, 0x4341), Qb = __byte_perm(Q, 0u, 0x4341);
-          mma_f16(ov[ch + y][0], P & kByte, P & kHiNib, Q & kByte, Q & kHiNib, b0, b1);
-          mma_f16(ov[ch + y][1], Pb, Pb & kHiNib, Qb, Qb & kHiNib, b0, b1);
+          uint32_t lo[2][2], hi[2][2];
+#pragma unroll
+          for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int z = 0; z < 2; z++) {
+              const uint32_t w = r[u][2 * y + z];
+              lo[u][z] = x ? __byte_perm(w, 0u, 0x4341) : w & kByte;
+              hi[u][z] = (x ? lo[u][z] : w) & kHiNib;
+            }
+          float d[4];
+          mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][0], b[0][1]);
+          mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], b[1][0], b[1][1]);
+          const float high = d[2] + d[3];  // both columns of w
+          ov[ch + y][x][0] += (d[0] + d[1]) - high;  // 16 hi 2^-24 = hi 2^-20
+          ov[ch + y][x][1] += high;
         }
-      }
     }
   };
 
@@ -1184,8 +1224,8 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     float v[4];
 #pragma unroll
     for (int x = 0; x < 2; x++) {
-      v[2 * x + 1] = (ov[i][x][2] + ov[i][x][3]) * kS20;
-      v[2 * x] = (ov[i][x][0] + ov[i][x][1]) * kS24 - 16.f * v[2 * x + 1];
+      v[2 * x] = ov[i][x][0] * kS24;
+      v[2 * x + 1] = ov[i][x][1] * kS20;
     }
 #pragma unroll
     for (int x = 0; x < 4; x++) {
