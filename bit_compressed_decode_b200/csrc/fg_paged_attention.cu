@@ -16,8 +16,8 @@
 // mbarrier per stage) and meets no other warp before it is done.  A block lies in one or two pages
 // (page_size % 16 == 0), six copies each, issued by as many lanes; the lanes look the page table up
 // for 32 blocks at a time.  Two unrolled stages measured 210 us where three in a ring, whose
-// addresses are computed, took 219 (512 sequences of 513 to 544 slots, 32 heads of 128: 1.26 GB,
-// 5.97 TB/s of 6.46 measured for a copy).  Which warp takes which blocks: make_plan below.
+// addresses are computed, took 219 (512 sequences of 513 to 544 slots, 32 heads of 128: 1.26 GB; 215
+// us now, 5.8 TB/s of 6.46 measured for a copy).  Which warp takes which blocks: make_plan below.
 //
 // Both products run on the tensor cores straight from the codes (the group decomposition):
 //     q . k_t = sum_g ( min_tg * sum_{d in g} q_d  +  scale_tg * sum_{d in g} q_d c_td )
@@ -58,8 +58,8 @@ constexpr uint32_t kOnes = 0x3C003C00u;   // fp16 {1, 1}
 // CTAs (of four warps) resident per SM, which is what the register budgets are cut for.  Tile kernel:
 // 168 registers a thread hold one tile of D <= 128 without spills (at 128, four CTAs, the three
 // tracked sequences of the benchmark took 69 us instead of 58); two tiles, or D = 256, need 255.
-// Single-column kernel: 128 registers (five CTAs spill: 236 us instead of 210 for 512 sequences of
-// 513 to 544 slots and 32 heads of 128).
+// Single-column kernel: 128 registers (five CTAs spill: 221 to 226 us instead of 214 to 216 for 512
+// sequences of 513 to 544 slots and 32 heads of 128).
 __host__ __device__ constexpr int tile_ctas(int D, int cols) { return cols <= kCols && D <= 128 ? 3 : 2; }
 __host__ __device__ constexpr int one_ctas(int D) { return D <= 128 ? 4 : 3; }
 
@@ -1321,6 +1321,7 @@ __device__ __forceinline__ float2 join_ml(const PagedAttnArgs &a, int n, int u0,
 }
 
 constexpr int kJoinWarps = 8;
+constexpr int kPartsPerBlock = 2;  // of those whose slots' weights grow
 constexpr int kMaxCols = 16;  // columns per item: at most two tiles
 
 // A column's parts number w, w + warps, .. joined by a warp, V dims a lane: their maximum and sum
@@ -1388,12 +1389,12 @@ __device__ __forceinline__ void store_row(__half *dst, const float (&o)[V], floa
 
 // The first blocks: a column of an item to a warp, or (wide) to a block: a cut item's parts joined
 // into the column's output row, and zeros for items without blocks, which no unit meets.  Behind
-// them (accumulate) a block per unit: the weights of its parts' slots, half the block to a part.
+// them (accumulate) the weights of the parts' slots, kPartsPerBlock to a block.
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedAttnArgs a, int out_cols, int out_blocks,
                                                                      bool wide) {
   constexpr int V = D / 32;  // dims per lane
-  __shared__ float2 col[2][kMaxCols];
+  __shared__ float2 col[kPartsPerBlock][kMaxCols];
   __shared__ float part[kJoinWarps][D];
   __shared__ float2 part_ml[kJoinWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, HT = a.kv.H * a.tiles;
@@ -1447,15 +1448,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     store_row<V>(dst + lane * V, o, inv);
     return;
   }
-  const int unit = blockIdx.x - out_blocks, k = warp / (kJoinWarps / 2);
+  constexpr int P = kPartsPerBlock, WP = kJoinWarps / P;  // warps per part
+  const int k = warp / WP, w = warp % WP, i = tid % (32 * WP);
+  const int number = (blockIdx.x - out_blocks) * P + k;
   griddep_wait();
-  const Part p = a.parts[2 * unit + k];
-  const int i = tid & (kJoinWarps * 16 - 1), w = warp & (kJoinWarps / 2 - 1);
+  Part p;
+  p.item = -1;
+  if (number < 2 * a.units) p = a.parts[number];
   Item it;
   it.ncols = 0;
   if (p.item >= 0) {
     it = load_item(a, p.item / HT, p.item % HT, false);
-    for (int n = w; n < it.ncols; n += kJoinWarps / 2) {
+    for (int n = w; n < it.ncols; n += WP) {
       const float2 v = it.len(it.n0 + n, a.R) > 0 ? join_ml(a, n, p.u0, p.u1) : make_float2(0.f, 0.f);
       if (lane == 0) col[k][n] = make_float2(v.x, v.y != 0.f ? 1.0f / v.y : 0.f);
     }
@@ -1466,10 +1470,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
   const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
   const int end = min(p.t1, last >= it.n0 ? it.len(last, a.R) : 0);
   if (a.pcols == 1) {
-    if (col[k][0].y != 0.f) grow_row(a, it.s, it.h, sc, p.t0, end, col[k][0].x, col[k][0].y, i, kJoinWarps * 16);
+    if (col[k][0].y != 0.f) grow_row(a, it.s, it.h, sc, p.t0, end, col[k][0].x, col[k][0].y, i, 32 * WP);
     return;
   }
-  for (int t = p.t0 + 4 * i; t < end; t += 4 * kJoinWarps * 16) {
+  for (int t = p.t0 + 4 * i; t < end; t += 4 * 32 * WP) {
     float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int n = 0; n < it.ncols; n++) {
       const float2 c = col[k][n];
@@ -1581,7 +1585,7 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int cols, bool accumulate, cuda
     // few items have many parts each
     const bool wide = p.units >= 16LL * a.items;
     const int out_blocks = wide ? a.items * out_cols : (a.items * out_cols + kJoinWarps - 1) / kJoinWarps;
-    lc.gridDim = dim3(out_blocks + (accumulate ? p.units : 0));
+    lc.gridDim = dim3(out_blocks + (accumulate ? (2 * p.units + kPartsPerBlock - 1) / kPartsPerBlock : 0));
     lc.blockDim = dim3(kJoinWarps * 32);
     lc.stream = st;
     cudaLaunchAttribute attr[1];

@@ -256,8 +256,8 @@ FG_API fg_status fg_paged_kv_append(const fg_paged_kv *kv, const fg_half *k, con
  * flags it too and is zero; the sequence's other rows are zero or as they would be, and its weights
  * have grown by the rows that are not zero.
  * workspace: fg_paged_attention_workspace_bytes of device scratch (16-byte aligned), nothing kept
- * in it between calls; with less the attention is split less, or accumulate is refused
- * (FG_ERR_WORKSPACE).  Two calls that may run at once need a workspace each. */
+ * in it between calls; with less the attention is not split over the length, or accumulate is
+ * refused (FG_ERR_WORKSPACE).  Two calls that may run at once need a workspace each. */
 FG_API size_t fg_paged_attention_workspace_bytes(const fg_paged_kv *kv, int num_q_heads, int rows, int rows_per_seq,
                                                  int max_len, int accumulate);
 FG_API fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q, int64_t ldq, int num_q_heads, fg_half *out,
