@@ -21,13 +21,15 @@
 //
 // Both products run on the tensor cores straight from the codes (the group decomposition):
 //     q . k_t = sum_g ( min_tg * sum_{d in g} q_d  +  scale_tg * sum_{d in g} q_d c_td )
-//     o_d     = sum_t p_t (min_tg + 7.5 scale_tg)  +  sum_t w_tg c_td  -  7.5 sum_t w_tg
-// with w_tg = p_t scale_tg rounded to fp16, the operand's type.  The last term, one more MMA per
-// group with an operand of ones, takes back what the rounding of w has in common for all codes, so
-// that an error of w weighs |c - 7.5| instead of c.  A nibble left in bits 0-3 of a 16-bit half is
-// the fp16 subnormal c * 2^-24, one in bits 4-7 is c * 2^-20, a whole byte (lo + 16 hi) * 2^-24, all
-// exact: an AND per pair of codes unpacks them, and the fp32 results are rescaled by the power of
-// two.  Scores, softmax state and sums are fp32.
+//     o_d     = sum_t p_t min_tg  +  sum_t w_tg c_td,  w_tg = p_t scale_tg
+// The operands are fp16; w goes in as its rounding and the rest, 22 bits together: a row whose
+// weight lies on a few slots would otherwise carry their rounding in all of its values (half a step,
+// 2.4e-4, against the output's own).  A nibble in bits 4-7 of a 16-bit half is
+// the fp16 subnormal c * 2^-20, exact, so that a shift and an AND unpack a pair of codes, and the fp32
+// results are rescaled.  Not bits 0-3, which two of four nibbles would reach without a shift: the
+// tensor core aligns a product by its operands' exponents, -14 for every subnormal, and drops what
+// lies some 24 bits below; with c * 2^-24 that was 3e-5 of a code's weight, with c * 2^-20 it is 6e-7
+// (codes of 1 under minima of -scale).  Scores, softmax state and sums are fp32.
 //   scores: A = codes of 16 slots x 16 dims of one group, B = q (16 dims x 8 columns)
 //   output: A = codes of 16 dims x 16 slots (ldmatrix.trans), B = w of the dims' group (16 slots x 8
 //           columns), which is the score tile's layout transposed (movmatrix)
@@ -50,14 +52,25 @@ constexpr int kCta = kWarps * kBlock;   // slots per CTA step
 constexpr int kCols = 8;                // columns per tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 2.0f;
-constexpr uint32_t kLoNib = 0x000F000Fu;  // bits 0-3 of both halves: c * 2^-24
-constexpr uint32_t kHiNib = 0x00F000F0u;  // bits 4-7 of both halves: c * 2^-20
-constexpr uint32_t kByte = 0x00FF00FFu;   // both nibbles of the low byte: (lo + 16 hi) * 2^-24
-constexpr uint32_t kOnes = 0x3C003C00u;   // fp16 {1, 1}
+constexpr uint32_t kNibble = 0x00F000F0u;  // bits 4-7 of both halves: c * 2^-20
+constexpr float kUnit = 1048576.0f;        // 2^20: sums of products with codes, back to their size
+constexpr float kScore = kUnit * kLog2e;   // and to log2 units
+
+// The four nibbles of a word's 16-bit halves as pairs of fp16 numbers, c * 2^-20 each: nibble i (bits
+// 4i .. 4i+3) of the low and of the high half.
+struct Nibbles {
+  uint32_t n[4];
+  __device__ __forceinline__ explicit Nibbles(uint32_t x) {
+    n[0] = (x << 4) & kNibble;
+    n[1] = x & kNibble;
+    n[2] = (x >> 4) & kNibble;
+    n[3] = (x >> 8) & kNibble;
+  }
+};
 
 // CTAs (of four warps) resident per SM, which is what the register budgets are cut for.  Tile kernel:
-// 168 registers a thread hold one tile of D <= 128 without spills (at 128, four CTAs, the three
-// tracked sequences of the benchmark took 69 us instead of 58); two tiles, or D = 256, need 255.
+// 168 registers a thread hold one tile of D <= 128 (at 128, four CTAs, three tracked sequences of up
+// to 40000 slots and 8 heads of 4 columns took 69 us instead of 58); two tiles, or D = 256, need 255.
 // Single-column kernel: 128 registers (five CTAs spill: 221 to 226 us instead of 214 to 216 for 512
 // sequences of 513 to 544 slots and 32 heads of 128).
 __host__ __device__ constexpr int tile_ctas(int D, int cols) { return cols <= kCols && D <= 128 ? 3 : 2; }
@@ -438,36 +451,19 @@ struct Nums {
   }
 };
 
-// The B operands of 8 dims of q (v), for the low and the high nibbles.  A high nibble counts 16 times
-// what a low one does in its place, so the low nibbles' q is taken 16 times (exact), unless a value
-// of the column is too large for that (`big`): then the high nibbles' q a 16th (what that loses of
-// tiny values is far below the rounding of the column's sums).  Sums of products with q then count
-// q_unit(big) each.
-__device__ __forceinline__ float q_unit(bool big) { return big ? 16777216.0f : 1048576.0f; }  // 2^24, 2^20
-
-__device__ __forceinline__ bool q_big(const uint4 &v) {  // some |q| >= 2048
-  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-  return (m & 0xFFFFu) >= 0x6800u || (m >> 16) >= 0x6800u;
-}
-
-__device__ __forceinline__ void q_operands(uint32_t (&f)[4], const uint4 &v, bool big) {
-  f[0] = __byte_perm(v.x, v.z, 0x5410);  // dims 0, 4
-  f[1] = __byte_perm(v.y, v.w, 0x5410);  // dims 2, 6
-  f[2] = __byte_perm(v.x, v.z, 0x7632);  // dims 1, 5
-  f[3] = __byte_perm(v.y, v.w, 0x7632);  // dims 3, 7
-  const __half2 s = big ? __float2half2_rn(0.0625f) : __float2half2_rn(16.0f);
-#pragma unroll
-  for (int i = 0; i < 2; i++) {
-    __half2 *h = reinterpret_cast<__half2 *>(&f[big ? 2 + i : i]);
-    *h = __hmul2(*h, s);
-  }
+// The B operands of 8 dims of q (v): dims (0, 4) and (2, 6), the A operands' nibbles 0 and 2, then
+// (1, 5) and (3, 7), nibbles 1 and 3.
+__device__ __forceinline__ void q_operands(uint32_t (&f)[4], const uint4 &v) {
+  f[0] = __byte_perm(v.x, v.z, 0x5410);
+  f[1] = __byte_perm(v.y, v.w, 0x5410);
+  f[2] = __byte_perm(v.x, v.z, 0x7632);
+  f[3] = __byte_perm(v.y, v.w, 0x7632);
 }
 
 template <int D, int G, int NT, bool TRACK>
 __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_attn_kernel(const PagedAttnArgs a) {
   using S = Shape<D, G, NT>;
   constexpr int NG = S::NG, RB = S::RB, KW = S::KW, CH = S::CH, NC = NT * kCols;
-  constexpr float kS24 = 16777216.0f, kS20 = 1048576.0f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full_bar[kWarps][2];
   __shared__ float red_m[kWarps][NC], red_l[kWarps][NC];
@@ -536,11 +532,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
 
   // ---- q of column n0 + 8 nt + gid as the B operand of the score MMAs ----
   // Word j of group g of lane class c: dims 2o .. 2o+7, o = g*G/2 + c*G/8 + 4j.  Low-nibble MMA
-  // (bits 0-3 of w and of w >> 8): k slots (2c, 2c+1) = dims (2o, 2o+4), (2c+8, 2c+9) = (2o+2,
+  // (nibbles 0 and 2 of the halves): k slots (2c, 2c+1) = dims (2o, 2o+4), (2c+8, 2c+9) = (2o+2,
   // 2o+6); high-nibble MMA: the same + 1.
   uint32_t qf[NT][NG][KW][4];
-  float qsum[NT][2][NG];  // columns 2c, 2c+1: sum of q over the group, over the column's unit
-  float qunit[NT][2];     // the unit, times log2(e): what the scores below are multiplied with in the exponent
+  float qsum[NT][2][NG];  // columns 2c, 2c+1: sum of q over the group, over kUnit
   int len[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
@@ -548,33 +543,21 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
     const bool on = col < it.ncols && it.len(n, a.R) > 0;
     const __half *qrow = a.q + (static_cast<int64_t>(it.s) * a.rows_per_seq + n / a.R) * a.ldq +
                          (static_cast<int64_t>(it.h) * a.R + n % a.R) * D;
-    uint4 v[NG][KW];
-    bool big = false;
-#pragma unroll
-    for (int g = 0; g < NG; g++)
-#pragma unroll
-      for (int j = 0; j < KW; j++) {
-        v[g][j] = make_uint4(0, 0, 0, 0);
-        if (on) v[g][j] = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
-        big |= q_big(v[g][j]);
-      }
-    big = __ballot_sync(0xffffffffu, big) >> (4 * gid) & 15u;
-    const float unit_of_gid = q_unit(big) * kLog2e;
-    qunit[nt][0] = __shfl_sync(0xffffffffu, unit_of_gid, 8 * c);
-    qunit[nt][1] = __shfl_sync(0xffffffffu, unit_of_gid, 8 * c + 4);
 #pragma unroll
     for (int g = 0; g < NG; g++) {
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < KW; j++) {
-        const __half *e = reinterpret_cast<const __half *>(&v[g][j]);
-        q_operands(qf[nt][g][j], v[g][j], big);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (on) v = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
+        const __half *e = reinterpret_cast<const __half *>(&v);
+        q_operands(qf[nt][g][j], v);
 #pragma unroll
         for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      sum *= 1.0f / q_unit(big);
+      sum *= 1.0f / kUnit;
       qsum[nt][0][g] = __shfl_sync(0xffffffffu, sum, 8 * c);
       qsum[nt][1][g] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
     }
@@ -591,9 +574,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
 
   float m[NT][2], l[NT][2];
-  float vacc[NT][2][NG];   // sum of p (min + 7.5 scale) over this lane's slots
+  float vacc[NT][2][NG];   // sum of p min over this lane's slots
   float ov[NT][CH][2][4];  // chunk ch, x: dims 32 ch + 4 gid + 2x ([0], [1]: columns 2c, 2c+1) and + 1 ([2], [3])
-  float wacc[NT][NG][2];   // sum of w
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
     m[nt][0] = m[nt][1] = -INFINITY;
@@ -601,7 +583,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
 #pragma unroll
     for (int g = 0; g < NG; g++) {
       vacc[nt][0][g] = vacc[nt][1][g] = 0.f;
-      wacc[nt][g][0] = wacc[nt][g][1] = 0.f;
     }
 #pragma unroll
     for (int i = 0; i < CH; i++)
@@ -613,7 +594,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   auto block = [&](auto stage, auto edge, int t) {
     constexpr int OFF = decltype(stage)::value * S::STAGE_B;
     constexpr bool EDGE = decltype(edge)::value;
-    // ---- scores (over their column's unit) of slots t + 16u + gid + 8x, columns 2c + e ----
+    // ---- scores (over kUnit) of slots t + 16u + gid + 8x, columns 2c + e ----
     float sc[NT][2][2][2];
 #pragma unroll
     for (int u = 0; u < 2; u++) {
@@ -628,17 +609,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         float lo[NT][4], hi[NT][4];  // two chains of MMAs
 #pragma unroll
         for (int j = 0; j < KW; j++) {
-          const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
-          const uint32_t l0 = x0 & kLoNib, l1 = x1 & kLoNib, l2 = y0 & kLoNib, l3 = y1 & kLoNib;
-          const uint32_t h0 = x0 & kHiNib, h1 = x1 & kHiNib, h2 = y0 & kHiNib, h3 = y1 & kHiNib;
+          const Nibbles x0(k0[j]), x1(k1[j]);
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
             if (j == 0) {
-              mma_f16_z(lo[nt], l0, l1, l2, l3, qf[nt][g][j][0], qf[nt][g][j][1]);
-              mma_f16_z(hi[nt], h0, h1, h2, h3, qf[nt][g][j][2], qf[nt][g][j][3]);
+              mma_f16_z(lo[nt], x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[nt][g][j][0], qf[nt][g][j][1]);
+              mma_f16_z(hi[nt], x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[nt][g][j][2], qf[nt][g][j][3]);
             } else {
-              mma_f16(lo[nt], l0, l1, l2, l3, qf[nt][g][j][0], qf[nt][g][j][1]);
-              mma_f16(hi[nt], h0, h1, h2, h3, qf[nt][g][j][2], qf[nt][g][j][3]);
+              mma_f16(lo[nt], x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[nt][g][j][0], qf[nt][g][j][1]);
+              mma_f16(hi[nt], x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[nt][g][j][2], qf[nt][g][j][3]);
             }
           }
         }
@@ -677,7 +656,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
 #pragma unroll
               for (int x = 0; x < 2; x++) {
                 const int ts = t + 16 * u + gid + 8 * x;
-                if (!EDGE || ts < len[nt][e]) srow[(nt * kCols + 2 * c + e) * a.score_ld + ts] = sc[nt][u][x][e] * qunit[nt][e];
+                if (!EDGE || ts < len[nt][e]) srow[(nt * kCols + 2 * c + e) * a.score_ld + ts] = sc[nt][u][x][e] * kScore;
               }
     }
     // ---- running maximum: moves only when a score exceeds it by more than kSlack, so that
@@ -689,7 +668,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
 #pragma unroll
       for (int e = 0; e < 2; e++) {
         cmax[nt][e] =
-            fmaxf(fmaxf(sc[nt][0][0][e], sc[nt][0][1][e]), fmaxf(sc[nt][1][0][e], sc[nt][1][1][e])) * qunit[nt][e];
+            fmaxf(fmaxf(sc[nt][0][0][e], sc[nt][0][1][e]), fmaxf(sc[nt][1][0][e], sc[nt][1][1][e])) * kScore;
         moves |= cmax[nt][e] > m[nt][e] + kSlack;
       }
     if (__any_sync(0xffffffffu, moves)) {
@@ -710,8 +689,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         for (int g = 0; g < NG; g++) {
           vacc[nt][0][g] *= al[0];
           vacc[nt][1][g] *= al[1];
-          wacc[nt][g][0] *= al[0];
-          wacc[nt][g][1] *= al[1];
         }
 #pragma unroll
         for (int ch = 0; ch < CH; ch++)
@@ -722,7 +699,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
       }
     }
     // ---- p and the sums ----
-    uint32_t b[2][NT][NG][2];
+    uint32_t b[2][NT][NG][2], bl[2][NT][NG][2];  // w rounded, and the rest
 #pragma unroll
     for (int u = 0; u < 2; u++) {
       float p[NT][2][2];
@@ -732,7 +709,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         for (int x = 0; x < 2; x++)
 #pragma unroll
           for (int e = 0; e < 2; e++) {
-            p[nt][x][e] = EDGE && sc[nt][u][x][e] == -INFINITY ? 0.f : fast_exp2(fmaf(sc[nt][u][x][e], qunit[nt][e], -m[nt][e]));
+            p[nt][x][e] = EDGE && sc[nt][u][x][e] == -INFINITY ? 0.f : fast_exp2(fmaf(sc[nt][u][x][e], kScore, -m[nt][e]));
             l[nt][e] += p[nt][x][e];
           }
       const __half *const n0 = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG, *const n1 = n0 + 8 * NG;
@@ -742,7 +719,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
       for (int g = 0; g < NG; g++)
 #pragma unroll
         for (int x = 0; x < 2; x++) {
-          const float vs = vsc[x].get(g), vb = vm[x].get(g) + 7.5f * vs;
+          const float vs = vsc[x].get(g), vb = vm[x].get(g);
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
             float w0 = p[nt][x][0] * vs, w1 = p[nt][x][1] * vs, o0 = p[nt][x][0] * vb, o1 = p[nt][x][1] * vb;
@@ -752,22 +729,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
             }
             vacc[nt][0][g] += o0;
             vacc[nt][1][g] += o1;
-            b[u][nt][g][x] = transpose_8x8(pack_h2(w0, w1));
+            const uint32_t w = pack_h2(w0, w1);
+            const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+            b[u][nt][g][x] = transpose_8x8(w);
+            bl[u][nt][g][x] = transpose_8x8(pack_h2(w0 - r.x, w1 - r.y));
           }
         }
     }
     // ---- the output product: a block's MMAs start from zero and are added in fp32 registers (the
     //      tensor core's own additions truncate, and what they lose grows with the sum) ----
-#pragma unroll
-    for (int g = 0; g < NG; g++)
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++) {
-        float d[4];
-        mma_f16_z(d, kOnes, kOnes, kOnes, kOnes, b[0][nt][g][0], b[0][nt][g][1]);
-        mma_f16(d, kOnes, kOnes, kOnes, kOnes, b[1][nt][g][0], b[1][nt][g][1]);
-        wacc[nt][g][0] += d[0];
-        wacc[nt][g][1] += d[1];
-      }
 #pragma unroll
     for (int ch = 0; ch < CH; ch += 2) {
       uint32_t r[2][4];  // [u]: slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
@@ -778,26 +748,25 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
       for (int y = 0; y < 2; y++)
 #pragma unroll
         for (int x = 0; x < 2; x++) {
-          // rows gid take both nibbles of a byte, lo + 16 hi (<= 255, exact), rows gid + 8 the high one
-          uint32_t lo[2][2], hi[2][2];
+          uint32_t lo[2][2], hi[2][2];  // dims 2x (rows gid) and 2x + 1 (rows gid + 8) of the four
 #pragma unroll
           for (int u = 0; u < 2; u++)
 #pragma unroll
             for (int z = 0; z < 2; z++) {
               const uint32_t w = r[u][2 * y + z];
-              lo[u][z] = x ? __byte_perm(w, 0u, 0x4341) : w & kByte;
-              hi[u][z] = (x ? lo[u][z] : w) & kHiNib;
+              lo[u][z] = (x ? w >> 4 : w << 4) & kNibble;
+              hi[u][z] = (x ? w >> 8 : w) & kNibble;
             }
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
             float d[4];
             mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][nt][g][0], b[0][nt][g][1]);
             mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], b[1][nt][g][0], b[1][nt][g][1]);
+            mma_f16(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], bl[0][nt][g][0], bl[0][nt][g][1]);
+            mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], bl[1][nt][g][0], bl[1][nt][g][1]);
             float(&o)[4] = ov[nt][ch + y][x];
-            o[0] += d[0] - d[2];  // 16 hi 2^-24 = hi 2^-20
-            o[1] += d[1] - d[3];
-            o[2] += d[2];
-            o[3] += d[3];
+#pragma unroll
+            for (int i = 0; i < 4; i++) o[i] += d[i];
           }
         }
     }
@@ -862,12 +831,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
                            (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + 4 * gid;
 #pragma unroll
       for (int ch = 0; ch < CH; ch++) {
-        const float base = vacc[nt][e][ch * 32 / G] - 7.5f * wacc[nt][ch * 32 / G][e];
+        const float base = vacc[nt][e][ch * 32 / G];
         float v[4];
 #pragma unroll
         for (int x = 0; x < 2; x++) {
-          v[2 * x] = ov[nt][ch][x][e] * kS24 + base;
-          v[2 * x + 1] = ov[nt][ch][x][2 + e] * kS20 + base;
+          v[2 * x] = ov[nt][ch][x][e] * kUnit + base;
+          v[2 * x + 1] = ov[nt][ch][x][2 + e] * kUnit + base;
         }
         if (a.shared_unit) {
           *reinterpret_cast<float4 *>(wo + n * D + ch * 32 + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
@@ -955,7 +924,6 @@ template <int D, int G, bool TRACK>
 __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_kernel(const PagedAttnArgs a) {
   using S = One<D, G>;
   constexpr int NG = S::NG, RB = S::RB, KW = S::KW, CH = S::CH;
-  constexpr float kS24 = 16777216.0f, kS20 = 1048576.0f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full_bar[kWarps][2];
   __shared__ float red_m[kWarps], red_l[kWarps];
@@ -1016,42 +984,33 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   // ---- q as the B operand; word j of lane class c: dims 2o .. 2o+7 ----
   const __half *qrow = a.q + static_cast<int64_t>(s) * a.ldq + static_cast<int64_t>(h) * D;
   uint32_t qf[KW][4];
-  float ql, qunit;  // sum of q over this lane's group, over the unit; the unit times log2(e)
+  float ql;  // sum of q over this lane's group, over kUnit
   const int g = NG == 2 ? c & 1 : 0;
   {
-    uint4 v[KW];
     float part[NG];
-    bool big = false;
 #pragma unroll
     for (int i = 0; i < NG; i++) part[i] = 0.f;
 #pragma unroll
     for (int j = 0; j < KW; j++) {
       const int o = D == 64 ? 8 * c + 4 * j : 64 * (j >> 2) + 16 * c + 4 * (j & 3);
-      v[j] = make_uint4(0, 0, 0, 0);
-      if (len > 0) v[j] = *reinterpret_cast<const uint4 *>(qrow + 2 * o);
-      big |= q_big(v[j]);
-      const __half *e = reinterpret_cast<const __half *>(&v[j]);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (len > 0) v = *reinterpret_cast<const uint4 *>(qrow + 2 * o);
+      const __half *e = reinterpret_cast<const __half *>(&v);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
 #pragma unroll
       for (int i = 0; i < NG; i++) part[i] += o / (G / 2) == i ? sum : 0.f;
-    }
-    big = __any_sync(0xffffffffu, big);
-#pragma unroll
-    for (int j = 0; j < KW; j++) {
-      const int o = D == 64 ? 8 * c + 4 * j : 64 * (j >> 2) + 16 * c + 4 * (j & 3);
       const bool on = !(gid & 1) && (NG == 1 || o / (G / 2) == ((gid >> 1) & 1));
-      if (!on) v[j] = make_uint4(0, 0, 0, 0);
-      q_operands(qf[j], v[j], big);
+      if (!on) v = make_uint4(0, 0, 0, 0);
+      q_operands(qf[j], v);
     }
 #pragma unroll
     for (int i = 0; i < NG; i++) {
       part[i] += __shfl_xor_sync(0xffffffffu, part[i], 1);
       part[i] += __shfl_xor_sync(0xffffffffu, part[i], 2);
     }
-    ql = (NG == 2 && g ? part[NG - 1] : part[0]) * (1.0f / q_unit(big));
-    qunit = q_unit(big) * kLog2e;
+    ql = (NG == 2 && g ? part[NG - 1] : part[0]) * (1.0f / kUnit);
   }
   const bool upper = c & 2;  // this lane's slot is gid + 8 of the 16
   const int tq = gid + (upper ? 8 : 0);
@@ -1091,13 +1050,13 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
       float lo[4], hi[4];  // two chains of MMAs
 #pragma unroll
       for (int j = 0; j < KW; j++) {
-        const uint32_t x0 = k0[j], x1 = k1[j], y0 = x0 >> 8, y1 = x1 >> 8;
+        const Nibbles x0(k0[j]), x1(k1[j]);
         if (j == 0) {
-          mma_f16_z(lo, x0 & kLoNib, x1 & kLoNib, y0 & kLoNib, y1 & kLoNib, qf[j][0], qf[j][1]);
-          mma_f16_z(hi, x0 & kHiNib, x1 & kHiNib, y0 & kHiNib, y1 & kHiNib, qf[j][2], qf[j][3]);
+          mma_f16_z(lo, x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[j][0], qf[j][1]);
+          mma_f16_z(hi, x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[j][2], qf[j][3]);
         } else {
-          mma_f16(lo, x0 & kLoNib, x1 & kLoNib, y0 & kLoNib, y1 & kLoNib, qf[j][0], qf[j][1]);
-          mma_f16(hi, x0 & kHiNib, x1 & kHiNib, y0 & kHiNib, y1 & kHiNib, qf[j][2], qf[j][3]);
+          mma_f16(lo, x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[j][0], qf[j][1]);
+          mma_f16(hi, x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[j][2], qf[j][3]);
         }
       }
       const __half *n = nbase + OFF / 2 + 16 * u * NG;
@@ -1114,9 +1073,9 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
       if (!(c & 1))
 #pragma unroll
         for (int u = 0; u < 2; u++)
-          if (!EDGE || t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u] * qunit;
+          if (!EDGE || t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u] * kScore;
     }
-    float cmax = fmaxf(sc[0], sc[1]) * qunit;  // scores are held over the unit
+    float cmax = fmaxf(sc[0], sc[1]) * kScore;  // scores are held over kUnit
     if (__any_sync(0xffffffffu, cmax > m + kSlack)) {  // the running maximum moves
 #pragma unroll
       for (int o = 2; o < 32; o <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
@@ -1136,7 +1095,7 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
 #pragma unroll
     for (int u = 0; u < 2; u++) {
       const __half *n = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG;
-      const float p = fast_exp2(fmaf(sc[u], qunit, -m));
+      const float p = fast_exp2(fmaf(sc[u], kScore, -m));
       float w = p * __half2float(n[kBlock * NG]), pm = p * __half2float(n[0]);
       if (EDGE && t + 16 * u + tq >= t_end) w = pm = 0.f;  // masked slots may hold anything (their p is 0)
       l += p;
@@ -1159,22 +1118,20 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
       for (int y = 0; y < 2; y++)
 #pragma unroll
         for (int x = 0; x < 2; x++) {
-          // rows gid take both nibbles of a byte, lo + 16 hi (<= 255, exact), rows gid + 8 the high one
-          uint32_t lo[2][2], hi[2][2];
+          uint32_t lo[2][2], hi[2][2];  // dims 2x (rows gid) and 2x + 1 (rows gid + 8) of the four
 #pragma unroll
           for (int u = 0; u < 2; u++)
 #pragma unroll
             for (int z = 0; z < 2; z++) {
               const uint32_t w = r[u][2 * y + z];
-              lo[u][z] = x ? __byte_perm(w, 0u, 0x4341) : w & kByte;
-              hi[u][z] = (x ? lo[u][z] : w) & kHiNib;
+              lo[u][z] = (x ? w >> 4 : w << 4) & kNibble;
+              hi[u][z] = (x ? w >> 8 : w) & kNibble;
             }
           float d[4];
           mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][0], b[0][1]);
           mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], b[1][0], b[1][1]);
-          const float high = d[2] + d[3];  // both columns of w
-          ov[ch + y][x][0] += (d[0] + d[1]) - high;  // 16 hi 2^-24 = hi 2^-20
-          ov[ch + y][x][1] += high;
+          ov[ch + y][x][0] += d[0] + d[1];  // both columns of w
+          ov[ch + y][x][1] += d[2] + d[3];
         }
     }
   };
@@ -1224,8 +1181,8 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     float v[4];
 #pragma unroll
     for (int x = 0; x < 2; x++) {
-      v[2 * x] = ov[i][x][0] * kS24;
-      v[2 * x + 1] = ov[i][x][1] * kS20;
+      v[2 * x] = ov[i][x][0] * kUnit;
+      v[2 * x + 1] = ov[i][x][1] * kUnit;
     }
 #pragma unroll
     for (int x = 0; x < 4; x++) {
@@ -1510,13 +1467,14 @@ void plan_bytes(Plan *p, int64_t items, int D, int limit, bool accumulate) {
 // ones where there are many: 30 sequences of 2000 slots and 32 heads of 128 took 58.8 us direct and
 // 62.3 partitioned, 8 of them 23.9 and 26.0, one 21.4 and 19.5; 64 tracked ones of 1500 to 2112
 // slots 120 and 133; 24 ragged ones of up to 16384 slots and 8 shared heads 95 and 79.
-// Two column tiles to an item halve the unpacking: 8 heads of 64 with 16 columns 77 us instead of 89.
+// Two column tiles to an item halve the unpacking; heads of 64 have the registers for it (24
+// sequences of 8192 slots, 8 heads of 16 columns: 77 us instead of 89).
 // Accumulating launches take the column tiles one after the other, so that a slot's weight is grown
 // by one CTA at a time and in a fixed order.
 Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate, int64_t *items) {
   Plan p;
   p.one = cols == 1 && D / G <= 2;
-  p.pcols = p.one ? 1 : cols > kCols && D <= 128 ? 2 * kCols : kCols;
+  p.pcols = p.one ? 1 : cols > kCols && D == 64 ? 2 * kCols : kCols;
   p.tiles = (cols + p.pcols - 1) / p.pcols;
   const int per_sm = p.one ? one_ctas(D) : tile_ctas(D, p.pcols);
   *items = pairs * (accumulate ? 1 : p.tiles);
@@ -1574,7 +1532,7 @@ fg_status launch(PagedAttnArgs a, const Plan &p, int cols, bool accumulate, cuda
       }
     }
     if (!p.one && p.pcols == kCols) rc = launch_tiles<D, G, 1>(a, grid, accumulate, st);
-    if constexpr (D <= 128) {
+    if constexpr (D == 64) {
       if (!p.one && p.pcols == 2 * kCols) rc = launch_tiles<D, G, 2>(a, grid, accumulate, st);
     }
     if (rc != FG_OK || (rc = fg_launch_check()) != FG_OK) return rc;
