@@ -52,19 +52,29 @@ constexpr int kCta = kWarps * kBlock;   // slots per CTA step
 constexpr int kCols = 8;                // columns per tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 2.0f;
-constexpr uint32_t kNibble = 0x00F000F0u;  // bits 4-7 of both halves: c * 2^-20
-constexpr float kUnit = 1048576.0f;        // 2^20: sums of products with codes, back to their size
-constexpr float kScore = kUnit * kLog2e;   // and to log2 units
+constexpr uint32_t kLowNibble = 0x000F000Fu;  // bits 0-3 of both halves: c * 2^-24
+constexpr uint32_t kNibble = 0x00F000F0u;     // bits 4-7 of both halves: c * 2^-20
+constexpr float kUnit = 1048576.0f;           // 2^20: sums of products with codes, back to their size
+constexpr float kScore = kUnit * kLog2e;      // and to log2 units
 
-// The four nibbles of a word's 16-bit halves as pairs of fp16 numbers, c * 2^-20 each: nibble i (bits
-// 4i .. 4i+3) of the low and of the high half.
+// Pairs of fp16 numbers c * 2^-20 from nibbles 0, and from nibbles 1, of a word's 16-bit halves.  The
+// multiplication by 16 (exact) is the FMA pipe's, which has room; a shift would be the ALU's.
+__device__ __forceinline__ uint32_t nibble0(uint32_t x) {
+  const uint32_t n = x & kLowNibble;
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&n), __float2half2_rn(16.0f));
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t nibble1(uint32_t x) { return x & kNibble; }
+
+// The four nibbles of a word's halves: nibble i is bits 4i .. 4i+3 of the low and of the high half.
 struct Nibbles {
   uint32_t n[4];
   __device__ __forceinline__ explicit Nibbles(uint32_t x) {
-    n[0] = (x << 4) & kNibble;
-    n[1] = x & kNibble;
-    n[2] = (x >> 4) & kNibble;
-    n[3] = (x >> 8) & kNibble;
+    const uint32_t y = x >> 8;
+    n[0] = nibble0(x);
+    n[1] = nibble1(x);
+    n[2] = nibble0(y);
+    n[3] = nibble1(y);
   }
 };
 
@@ -753,9 +763,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
           for (int u = 0; u < 2; u++)
 #pragma unroll
             for (int z = 0; z < 2; z++) {
-              const uint32_t w = r[u][2 * y + z];
-              lo[u][z] = (x ? w >> 4 : w << 4) & kNibble;
-              hi[u][z] = (x ? w >> 8 : w) & kNibble;
+              const uint32_t w = x ? r[u][2 * y + z] >> 8 : r[u][2 * y + z];
+              lo[u][z] = nibble0(w);
+              hi[u][z] = nibble1(w);
             }
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
@@ -1123,9 +1133,9 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
           for (int u = 0; u < 2; u++)
 #pragma unroll
             for (int z = 0; z < 2; z++) {
-              const uint32_t w = r[u][2 * y + z];
-              lo[u][z] = (x ? w >> 4 : w << 4) & kNibble;
-              hi[u][z] = (x ? w >> 8 : w) & kNibble;
+              const uint32_t w = x ? r[u][2 * y + z] >> 8 : r[u][2 * y + z];
+              lo[u][z] = nibble0(w);
+              hi[u][z] = nibble1(w);
             }
           float d[4];
           mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][0], b[0][1]);
