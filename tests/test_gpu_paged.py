@@ -1,19 +1,19 @@
 """The paged 4-bit KV cache against plain implementations in 64 bits: append (bit for bit), attention with and without
 the accumulation of its weights, eviction (exact), and a run of them together.
 
-Attention's tolerance, per output value.  The kernel holds scores, softmax and sums in fp32; it rounds twice to fp16:
-the product w = p * scale of each slot and group that multiplies the codes (at most half a step, 2^-11 relative, or
-2^-25 absolute where w is subnormal; the rounding's share that all codes of the group have in common, 7.5 * (w' - w), is
-taken back, so a code's error weighs at most |c - 7.5| <= 7.5), and the output (2^-11).  With q.k = sum_g (min_g sum q +
-scale_g sum q c), each of the <= D + 2 D/G fp32 additions and products of a score is off by 2^-24 of magnitudes below
-A = sum |q| (|min| + 15 scale) in each direction, twice that on a tensor core that truncates; exp2 adds 2^-21 and each of
-the n/128 + 8 chained additions and rescalings of the sums 2^-23.  So
-  |out - ref| <= 2^-11 (|ref| + sum p scale 7.5) + 2 delta sum p (|min| + 15 scale) + n 2^-25 * 7.5 * 4 / l
+Attention's tolerance, per output value.  The kernel holds scores, softmax and sums in fp32.  Its output is rounded to
+fp16: 2^-11 of it.  The weight w = p * scale that multiplies a group's codes enters the tensor core as two fp16 numbers,
+2^-22 of it (2^-25 absolute where the second is subnormal), against codes of at most 15.  The codes are fp16 subnormals
+c * 2^-20, and a product with one is aligned by the exponent -14: what is kept of the 16 products of an MMA is a multiple
+of 2^-24 * 2 w_max 2^-14, that is 2^-17 w_max in units of a code, so that an MMA drops less than 16 * 2^-17 w_max, and all
+of them less than 2^-13 sum p scale.  With q.k = sum_g (min_g sum q + scale_g sum q c), each of the <= D + 2 D/G fp32
+additions and products of a score is off by 2^-24 of magnitudes below A = sum |q| (|min| + 15 scale) in each direction,
+twice that on a tensor core that truncates; exp2 adds 2^-21 and each of the n/128 + 8 chained additions and rescalings
+of the sums 2^-23.  So
+  |out - ref| <= 2^-11 |ref| + (2^-13 + 15 * 2^-22) sum p scale + 2 delta sum p (|min| + 15 scale) + n 2^-25 * 15 * 4 / l
   delta = 2 (D + 2 D/G) 2^-23 max A + 2^-21 + (n/128 + 8) 2^-23,  l = sum exp(s - max s)
 (4: the running reference of the exponent may lie 2 binary orders below the maximum).  A slot's weight grows by sums of
 p: delta of the growth, and 2^-23 per addition (one for each row and head) of the total."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -121,8 +121,8 @@ def ref_attention(cache, q, positions, rows_per_seq, counts=None):
             delta = 2 * (D + 2 * NG) * 2.0**-23 * A + 2.0**-21 + (m / 128 + 8) * 2.0**-23
             o = np.einsum("hrt,htd->hrd", p, v[:, :m])
             out[r] = o
-            tol[r] = (2.0**-11 * (np.abs(o) + 7.5 * np.einsum("hrt,htd->hrd", p, vs[:, :m]))
-                      + 2 * delta * np.einsum("hrt,htd->hrd", p, va[:, :m]) + m * 2.0**-25 * 30 / l)
+            tol[r] = (2.0**-11 * np.abs(o) + (2.0**-13 + 15 * 2.0**-22) * np.einsum("hrt,htd->hrd", p, vs[:, :m])
+                      + 2 * delta * np.einsum("hrt,htd->hrd", p, va[:, :m]) + m * 2.0**-25 * 60 / l)
             add[:, :m] += p.sum(1)
             add_tol[:, :m] += (2 * delta * p).sum(1)
         grown[s] = (add, add_tol)
@@ -298,6 +298,20 @@ def test_attention_split_over_long_sequences(D, G, ps, H, R, lengths, accumulate
                                       max_len=max(lengths), accumulate=True,
                                       workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
     assert out.shape == q.shape
+
+
+@pytest.mark.parametrize("accumulate", [False, True], ids=["plain", "tracked"])
+@pytest.mark.parametrize("D,G,R,rows", [(128, 64, 8, 6), (64, 64, 5, 7), (256, 128, 1, 9), (128, 128, 1, 1)])
+def test_attention_partitioned_tiles_and_counts(D, G, R, rows, accumulate):
+    """Long enough to be shared by all warps: tiles without a live column, cut and whole items, inactive sequences."""
+    rng = np.random.default_rng(D + R)
+    counts = [rows, 0, 1, max(1, rows - 2), rows, rows, 1]
+    positions = [0, 9, 3001, 31, -1, 2500, 700]
+    c = make_cache(rng, [max(0, p) + n if p >= 0 else 0 for p, n in zip(positions, counts)], 2, D, G, 48, track=accumulate)
+    assert c.max_pages * 48 > 2048
+    out = check_attention(c, queries(rng, len(counts) * rows, 2 * R, D), positions, rows, counts, accumulate=accumulate)
+    for s, n in enumerate(counts):
+        assert torch.count_nonzero(out.view(len(counts), rows, -1)[s, (n if positions[s] >= 0 else 0):]) == 0
 
 
 @pytest.mark.parametrize("rows,R", [(33, 1), (20, 5)])
