@@ -341,6 +341,7 @@ class PagedKVCache:
         self.num_pages, self.num_heads, self.head_dim, self.page_size = num_pages, num_heads, head_dim, page_size
         self.group, self.device, self._index = group, dev, page_table.get_device()
         self.num_seqs, self.max_pages = page_table.shape
+        self._width = num_heads * head_dim
         self.k_codes, self.k_mins, self.k_scales, self.v_codes, self.v_mins, self.v_scales = arrays
         self.weights, self.tokens, self.page_table = weights, tokens, page_table
         ptrs = [0 if a is None else a.data_ptr() for a in list(arrays) + [weights, tokens, page_table]]
@@ -371,17 +372,15 @@ _get_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t: torch.Tensor, cache: PagedKVCache, name: str, width: int | None = None) -> int:
-    """Checks fp16 rows of unit element stride on the cache's device; their stride."""
-    if t.dtype is not torch.float16 or t.dim() != 2 or t.get_device() != cache._index:
+def _rows(t: torch.Tensor, cache: PagedKVCache, name: str) -> tuple:
+    """Checks fp16 rows of unit element stride on the cache's device; (rows, width, row stride)."""
+    if t.dtype is not torch.float16 or t.get_device() != cache._index or t.ndim != 2:
         raise ValueError(f"{name}: expected float16 rows on {cache.device}, got {t.dtype} on {t.device}")
     n, m = t.shape
     ld, one = t.stride()
     if one != 1 and m > 1:
         raise ValueError(f"{name}: expected rows of unit element stride")
-    if width is not None and m != width:
-        raise ValueError(f"{name}: expected rows of {width} values, got {m}")
-    return ld if n > 1 else max(ld, m)  # (a single row's stride says nothing)
+    return n, m, ld if n > 1 or ld > m else m  # (a single row's stride says nothing)
 
 
 def _ints(t, cache: PagedKVCache, name: str, n: int):
@@ -393,16 +392,11 @@ def _ints(t, cache: PagedKVCache, name: str, n: int):
     return t.data_ptr()
 
 
-def _scratch(t, need, cache: PagedKVCache, stream):
-    """(address, bytes, tensor) of a call's workspace: the caller's, or memory of the call's stream."""
-    if t is None:
-        n = need()
-        if n == 0:
-            return None, 0, None
-        t = _on_stream(cache, stream, (n,), torch.uint8)
-    elif t.get_device() != cache._index or not t.is_contiguous():
+def _scratch(t: torch.Tensor, cache: PagedKVCache) -> tuple:
+    """(address, bytes) of a caller's workspace."""
+    if t.get_device() != cache._index or not t.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous tensor on {cache.device}")
-    return t.data_ptr(), t.numel() * t.element_size(), t
+    return t.data_ptr(), t.nbytes
 
 
 def _on_stream(cache: PagedKVCache, stream, shape, dtype) -> torch.Tensor:
@@ -436,12 +430,12 @@ def fg_paged_kv_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, po
                        first_tokens: torch.Tensor | None = None, stream=None) -> None:
     """Quantise and append rows k, v [rows, num_heads * head_dim]; row i of sequence s goes to slot
     ``positions[s] + i`` (see fg.h for row_counts, first_tokens and inactive sequences)."""
-    rows = k.shape[0]
-    width = cache.num_heads * cache.head_dim
-    ld = _rows(k, cache, "k", width)
-    if _rows(v, cache, "v", width) != ld or v.shape[0] != rows:
+    shape = rows, width, ld = _rows(k, cache, "k")
+    if _rows(v, cache, "v") != shape:
         raise ValueError("k and v must share their shape and a row stride")
-    n = -(-rows // max(1, rows_per_seq))
+    if width != cache._width:
+        raise ValueError(f"k: expected rows of {cache._width} values, got {width}")
+    n = rows if rows_per_seq <= 1 else -(-rows // rows_per_seq)
     _paged_call(_lib.fg_paged_kv_append, cache, stream, k.data_ptr(), v.data_ptr(), ld, rows, rows_per_seq,
                 _ints(positions, cache, "positions", n), _ints(row_counts, cache, "row_counts", n),
                 _ints(first_tokens, cache, "first_tokens", n))
@@ -459,22 +453,24 @@ def fg_paged_attention(cache: PagedKVCache, q: torch.Tensor, positions: torch.Te
                        stream=None) -> torch.Tensor:
     """Attention of q [rows, num_q_heads * head_dim] over the cache; ``accumulate=True`` adds each
     slot's probabilities to ``cache.weights``.  ``workspace``: None allocates it."""
-    ldq = _rows(q, cache, "q")
-    rows, width = q.shape
+    rows, width, ldq = _rows(q, cache, "q")
     hq = width // cache.head_dim
     if hq * cache.head_dim != width:
         raise ValueError(f"q: rows of {width} values are no whole heads of {cache.head_dim}")
-    n = -(-rows // max(1, rows_per_seq))
+    n = rows if rows_per_seq <= 1 else -(-rows // rows_per_seq)
     if out is None:
-        out = _on_stream(cache, stream, q.shape, torch.float16)
-    ldo = _rows(out, cache, "out", width)
-    if out.shape[0] != rows:
-        raise ValueError(f"out: expected {rows} rows")
-    ws, nbytes, _keep = _scratch(workspace, lambda: fg_paged_attention_workspace_bytes(
-        cache, hq, rows, rows_per_seq, max_len, accumulate), cache, stream)
+        out = _on_stream(cache, stream, (rows, width), torch.float16)
+    rows_out, width_out, ldo = _rows(out, cache, "out")
+    if rows_out != rows or width_out != width:
+        raise ValueError(f"out: expected {rows} rows of {width} values")
+    if workspace is None:
+        need = fg_paged_attention_workspace_bytes(cache, hq, rows, rows_per_seq, max_len, accumulate)
+        workspace = _on_stream(cache, stream, (need,), torch.uint8)
+    ws, nbytes = _scratch(workspace, cache)
     _paged_call(_lib.fg_paged_attention, cache, stream, q.data_ptr(), ldq, hq, out.data_ptr(), ldo, rows, rows_per_seq,
-                _ints(positions, cache, "positions", n), _ints(row_counts, cache, "row_counts", n), max_len or 0,
-                1 if accumulate else 0, ws, nbytes)
+                _ints(positions, cache, "positions", n),
+                None if row_counts is None else _ints(row_counts, cache, "row_counts", n), max_len or 0,
+                1 if accumulate else 0, ws or None, nbytes)
     return out
 
 
@@ -500,12 +496,14 @@ def fg_paged_kv_evict(cache: PagedKVCache, lengths: torch.Tensor, next_tokens: t
     n = cache.num_seqs
     if new_lengths is None:
         new_lengths = _on_stream(cache, stream, (n,), torch.int32)
-    ws, nbytes, _keep = _scratch(workspace, lambda: fg_paged_kv_evict_workspace_bytes(cache, budget, max_len), cache,
-                                 stream)
+    if workspace is None:
+        need = fg_paged_kv_evict_workspace_bytes(cache, budget, max_len)
+        workspace = _on_stream(cache, stream, (need,), torch.uint8) if need else None
+    ws, nbytes = (None, 0) if workspace is None else _scratch(workspace, cache)
     _paged_call(_lib.fg_paged_kv_evict, cache, stream, _ints(lengths, cache, "lengths", n),
                 _ints(next_tokens, cache, "next_tokens", n), budget, recent, max_len or 0,
                 _ints(new_lengths, cache, "new_lengths", n), _pool_like(weights_out, cache.weights, "weights_out"),
-                _pool_like(tokens_out, cache.tokens, "tokens_out"), ws, nbytes)
+                _pool_like(tokens_out, cache.tokens, "tokens_out"), ws or None, nbytes)
     return new_lengths
 
 

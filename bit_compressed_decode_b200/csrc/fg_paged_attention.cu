@@ -16,8 +16,8 @@
 // mbarrier per stage) and meets no other warp before it is done.  A block lies in one or two pages
 // (page_size % 16 == 0), six copies each, issued by as many lanes; the lanes look the page table up
 // for 32 blocks at a time.  Two unrolled stages measured 210 us where three in a ring, whose
-// addresses are computed, took 219 (512 sequences of 513 to 544 slots, 32 heads of 128: 1.26 GB; 215
-// us now, 5.8 TB/s of 6.46 measured for a copy).  Which warp takes which blocks: make_plan below.
+// addresses are computed, took 219 (512 sequences of 513 to 544 slots, 32 heads of 128: 1.26 GB; 227
+// us since the sums are exact, 5.5 TB/s of 6.46 measured for a copy).  Which warp takes which blocks: make_plan below.
 //
 // Both products run on the tensor cores straight from the codes (the group decomposition):
 //     q . k_t = sum_g ( min_tg * sum_{d in g} q_d  +  scale_tg * sum_{d in g} q_d c_td )
@@ -34,10 +34,11 @@
 //   output: A = codes of 16 dims x 16 slots (ldmatrix.trans), B = w of the dims' group (16 slots x 8
 //           columns), which is the score tile's layout transposed (movmatrix)
 // Both score and output fragments give a lane the columns 2c, 2c+1 (c = lane % 4), so the softmax
-// state of a column never leaves its lanes.  What the tile kernel costs beyond the bytes is the
-// fixed part of a launch (7 us from its start to the first block's arrival, 6 us of join) and, for D
-// = 256, instructions: 24 sequences of 8192 slots and 8 heads of 8 columns take 57 us of which the
-// blocks themselves take 41, 5.2 TB/s.
+// state of a column never leaves its lanes.  A block's output products start from
+// zero and are added in fp32 registers: the tensor core's additions truncate, which grows with a sum.
+// What the tile kernel costs beyond the bytes is the fixed part of a launch (7 us from its start to
+// the first block's arrival, 6 us of join) and instructions: 24 sequences of 8192 slots and 8 heads of
+// 8 columns take 68 us for 214 MB.
 #include <math.h>
 
 #include <type_traits>
@@ -81,8 +82,8 @@ struct Nibbles {
 // CTAs (of four warps) resident per SM, which is what the register budgets are cut for.  Tile kernel:
 // 168 registers a thread hold one tile of D <= 128 (at 128, four CTAs, three tracked sequences of up
 // to 40000 slots and 8 heads of 4 columns took 69 us instead of 58); two tiles, or D = 256, need 255.
-// Single-column kernel: 128 registers (five CTAs spill: 221 to 226 us instead of 214 to 216 for 512
-// sequences of 513 to 544 slots and 32 heads of 128).
+// Single-column kernel: 128 registers (five CTAs spill: 242 us instead of 225 for 512 sequences of 513
+// to 544 slots and 32 heads of 128).
 __host__ __device__ constexpr int tile_ctas(int D, int cols) { return cols <= kCols && D <= 128 ? 3 : 2; }
 __host__ __device__ constexpr int one_ctas(int D) { return D <= 128 ? 4 : 3; }
 
