@@ -25,8 +25,8 @@
 // The operands are fp16; w goes in as its rounding and the rest, 22 bits together: a row whose
 // weight lies on a few slots would otherwise carry their rounding in all of its values (half a step,
 // 2.4e-4, against the output's own).  A nibble in bits 4-7 of a 16-bit half is
-// the fp16 subnormal c * 2^-20, exact, so that a shift and an AND unpack a pair of codes, and the fp32
-// results are rescaled.  Not bits 0-3, which two of four nibbles would reach without a shift: the
+// the fp16 subnormal c * 2^-20, exact, so that an AND, and for some a shift or a multiplication,
+// unpacks a pair of codes, and the fp32 results are rescaled.  Not bits 0-3, which two of four nibbles would reach without a shift: the
 // tensor core aligns a product by its operands' exponents, -14 for every subnormal, and drops what
 // lies some 24 bits below; with c * 2^-24 that was 3e-5 of a code's weight, with c * 2^-20 it is 6e-7
 // (codes of 1 under minima of -scale).  Scores, softmax state and sums are fp32.
