@@ -12,7 +12,7 @@ fg_status fg_paged_validate(const fg_paged_kv *kv) {
   const int G = fg_kv_group(kv->group);
   if (G == 0 || (kv->head_dim != 64 && kv->head_dim != 128 && kv->head_dim != 256)) return FG_ERR_UNSUPPORTED;
   if (kv->head_dim % G || kv->page_size % 16) return FG_ERR_SHAPE;
-  if (static_cast<int64_t>(kv->max_pages) * kv->page_size > INT32_MAX) return FG_ERR_SHAPE;
+  if (static_cast<int64_t>(kv->max_pages) * kv->page_size > (1 << 30)) return FG_ERR_SHAPE;
   if (!kv->k_codes || !kv->v_codes || !kv->k_mins || !kv->k_scales || !kv->v_mins || !kv->v_scales || !kv->page_table)
     return FG_ERR_INVALID;
   if (!fg_aligned16(kv->k_codes) || !fg_aligned16(kv->v_codes) || !fg_aligned16(kv->k_mins) ||

@@ -200,7 +200,7 @@ FG_API fg_status fg_attention_decode_append(const fg_kv_cache *kv, const fg_half
  * An fg_kv_cache is the case page_size = max_len, num_pages = num_seqs, page_table[s] = {s}.
  * Device memory, caller-owned; the pools 16-byte aligned, the table 4-byte.
  * Requirements: page_size a multiple of 16, head_dim in {64, 128, 256} and a multiple of G,
- * max_pages * page_size <= INT32_MAX.  Table entries that no call below reaches may hold anything.
+ * max_pages * page_size <= 2^30.  Table entries that no call below reaches may hold anything.
  * Sequences may share pages that are only read; pages that a call appends to, accumulates weights
  * in or evicts from belong to one sequence, once.
  * An entry that is reached and lies outside [0, num_pages) flags FG_ERR_RANGE (fg_sync_status). */

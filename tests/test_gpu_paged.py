@@ -721,6 +721,33 @@ def test_side_stream_and_graph_replay():
     fg.fg_sync_status()
 
 
+def test_two_calls_at_once():
+    """Two caches on two streams, a workspace each: the bits of the calls one after the other."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    lengths = [[6000, 50, 1200], [3000, 3001, 2]]
+    caches, alone = ([make_cache(np.random.default_rng(i), n, 2, 128, 64, 32, track=True) for i, n in enumerate(lengths)]
+                     for _ in range(2))
+    qs = [queries(np.random.default_rng(9 + i), 3, 4, 128) for i in range(2)]
+    pos = [torch.tensor([x - 1 for x in n], dtype=torch.int32, device="cuda") for n in lengths]
+    ln = [torch.tensor(n, dtype=torch.int32, device="cuda") for n in lengths]
+    want = []
+    for c, q, p, n in zip(alone, qs, pos, ln):
+        want.append([fg.fg_paged_attention(c, q, p, accumulate=True) for _ in range(4)] + [fg.fg_paged_kv_evict(c, n, n, 100, 10)])
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i in range(2):
+            got[i].append(fg.fg_paged_attention(caches[i], qs[i], pos[i], accumulate=True, stream=streams[i]))
+    for i in range(2):
+        got[i].append(fg.fg_paged_kv_evict(caches[i], ln[i], ln[i], 100, 10, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(got[i], want[i]))
+        for x, y in zip(caches[i].arrays() + [caches[i].weights, caches[i].tokens], alone[i].arrays() + [alone[i].weights, alone[i].tokens]):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    fg.fg_sync_status()
+
+
 def test_evict_in_a_graph():
     rng = np.random.default_rng(31)
     lengths = [400, 90, 399]

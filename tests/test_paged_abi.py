@@ -45,7 +45,7 @@ BAD_CACHES = [
     (dict(group=32), UNSUPPORTED), (dict(head_dim=64, group=128), SHAPE), (dict(k_codes=None), INVALID),
     (dict(v_scales=None), INVALID), (dict(page_table=None), INVALID), (dict(k_codes=0x100008), INVALID),
     (dict(v_mins=0x100008), INVALID), (dict(page_table=0x100002), INVALID), (dict(weights=0x100002), INVALID),
-    (dict(tokens=0x100001), INVALID), (dict(max_pages=1 << 27), SHAPE),
+    (dict(tokens=0x100001), INVALID), (dict(max_pages=1 << 27), SHAPE), (dict(max_pages=(1 << 24) + 1), SHAPE),
 ]
 
 
