@@ -18,7 +18,7 @@
 // in slot order from a bit per slot).  Kept or not is a bit per slot, holes and movers are listed by
 // prefix sums over the words.  What moves is read and written 16 bytes of codes at a time, several a
 // thread in flight: the moves, a dependent load after a store, were half of the time before.
-// Measured: 2048 items of 2049 to 2112 slots to 2048 in 41 us (87 MB, 2.1 TB/s: the latencies of
+// Measured: 2048 items of 2049 to 2112 slots to 2048 in 38 us (87 MB, 2.3 TB/s: the latencies of
 // the phases, one after the other); 128 items of 700 to 16384 slots to 1024 in 26 us.
 #include "fg_paged.cuh"
 
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
 
   // ---- the moves: 16 bytes of codes at a time, and one number at a time (array by array, so that
   //      neighbouring moves' numbers are neighbours); V and N of them in flight per thread ----
-  constexpr int V = 4, N = 3;
+  constexpr int V = B > 1 ? 2 : 4, N = B > 1 ? 2 : 3;  // (many CTAs per SM: fewer registers)
   const int cv = a.code_vecs, vecs = moves * 2 * cv, nums = moves * 6;
   const int cs = cv == 2 ? 1 : cv == 4 ? 2 : 3;  // log2(cv)
   for (int v0 = tid, n0 = tid; v0 < vecs || n0 < nums; v0 += V * T, n0 += N * T) {
@@ -436,7 +436,8 @@ EvictPlan evict_plan(const fg_paged_kv *kv, int budget, int max_len) {
   p.lists = p.wide ? static_cast<size_t>(kv->num_seqs) * kv->num_heads * lists : 0;
   const int64_t items = static_cast<int64_t>(kv->num_seqs) * kv->num_heads;
   // long items have an SM each (16384 slots: 27 us, 45 with 192 threads); many items are throughput:
-  // 192 threads, six CTAs per SM (2048 items of 2100 slots: 41 us; 58 with 256 threads)
+  // 192 threads, eight CTAs per SM (2048 items of 2100 slots: 38 us; 41 with six, whose third wave is
+  // a third full, 58 with 256 threads)
   p.threads = limit > 4096 ? 1024 : items >= 8LL * fg_sm_count() ? 192 : 256;
   return p;
 }
@@ -498,7 +499,7 @@ extern "C" fg_status fg_paged_kv_evict(const fg_paged_kv *kv, const int32_t *len
   const unsigned grid = static_cast<unsigned>(kv->num_seqs) * kv->num_heads;
   if (p.wide) rc = launch<1024, 4, 1, true>(a, p, grid, st);
   else if (p.threads == 1024) rc = launch<1024, 4, 1, false>(a, p, grid, st);
-  else if (p.threads == 192) rc = launch<192, 3, 6, false>(a, p, grid, st);
+  else if (p.threads == 192) rc = launch<192, 3, 8, false>(a, p, grid, st);
   else rc = launch<256, 4, 1, false>(a, p, grid, st);
   if (rc != FG_OK || new_lengths != lengths) return rc;
   paged_new_lengths_kernel<<<kv->num_seqs, 128, 0, st>>>(new_lengths, kv->num_seqs, a);
