@@ -17,25 +17,26 @@
 // (page_size % 16 == 0), six copies each, issued by as many lanes; the lanes look the page table up
 // for 32 blocks at a time.  Two unrolled stages measured 210 us where three in a ring, whose
 // addresses are computed, took 219 (512 sequences of 513 to 544 slots, 32 heads of 128: 1.26 GB; 227
-// us since the sums are exact, 5.5 TB/s of 6.46 measured for a copy).  Which warp takes which blocks: make_plan below.
+// us since the sums are exact, 5.5 TB/s of 6.46 measured for a copy).  Which warp takes which blocks:
+// make_plan below.
 //
 // Both products run on the tensor cores straight from the codes (the group decomposition):
 //     q . k_t = sum_g ( min_tg * sum_{d in g} q_d  +  scale_tg * sum_{d in g} q_d c_td )
 //     o_d     = sum_t p_t min_tg  +  sum_t w_tg c_td,  w_tg = p_t scale_tg
 // The operands are fp16; w goes in as its rounding and the rest, 22 bits together: a row whose
 // weight lies on a few slots would otherwise carry their rounding in all of its values (half a step,
-// 2.4e-4, against the output's own).  A nibble in bits 4-7 of a 16-bit half is
-// the fp16 subnormal c * 2^-20, exact, so that an AND, and for some a shift or a multiplication,
-// unpacks a pair of codes, and the fp32 results are rescaled.  Not bits 0-3, which two of four nibbles would reach without a shift: the
-// tensor core aligns a product by its operands' exponents, -14 for every subnormal, and drops what
-// lies some 24 bits below; with c * 2^-24 that was 3e-5 of a code's weight, with c * 2^-20 it is 6e-7
-// (codes of 1 under minima of -scale).  Scores, softmax state and sums are fp32.
+// 2.4e-4, against the output's own).  A nibble in bits 4-7 of a 16-bit half is the fp16 subnormal
+// c * 2^-20, exact, so that an AND, and for some a shift or a multiplication, unpacks a pair of codes,
+// and the fp32 results are rescaled.  Not bits 0-3, which two of four nibbles would reach without a
+// shift: the tensor core aligns a product by its operands' exponents, -14 for every subnormal, and
+// drops what lies some 24 bits below; with c * 2^-24 that was 3e-5 of a code's weight, with c * 2^-20
+// it is 6e-7 (codes of 1 under minima of -scale).  Scores, softmax state and sums are fp32.
 //   scores: A = codes of 16 slots x 16 dims of one group, B = q (16 dims x 8 columns)
 //   output: A = codes of 16 dims x 16 slots (ldmatrix.trans), B = w of the dims' group (16 slots x 8
 //           columns), which is the score tile's layout transposed (movmatrix)
 // Both score and output fragments give a lane the columns 2c, 2c+1 (c = lane % 4), so the softmax
-// state of a column never leaves its lanes.  A block's output products start from
-// zero and are added in fp32 registers: the tensor core's additions truncate, which grows with a sum.
+// state of a column never leaves its lanes.  A block's output products start from zero and are added
+// in fp32 registers: the tensor core's additions truncate, which grows with a sum.
 // What the tile kernel costs beyond the bytes is the fixed part of a launch (7 us from its start to
 // the first block's arrival, 6 us of join) and instructions: 24 sequences of 8192 slots and 8 heads of
 // 8 columns take 68 us for 214 MB.
@@ -148,8 +149,9 @@ __device__ __forceinline__ int seq_blocks(const PagedAttnArgs &a, int s) {
 
 // A warp's way through its share of the work.  Partitioned launches lay the blocks of all items in
 // a row (sequence, then head and tile, then block) and cut it into `units` runs that differ by a
-// block at most, no more than one for every kMinBlocks blocks: a run is up to two parts of cut items, the first and the last, with
-// whole items in between.  A part is number 2 * unit + 1 if it begins its item, else 2 * unit.
+// block at most, no more than one for every kMinBlocks blocks: a run is up to two parts of cut items,
+// the first and the last, with whole items in between.  A part is number 2 * unit + 1 if it begins
+// its item, else 2 * unit.
 constexpr int kMinBlocks = 4;
 
 // x / d; the 64-bit division only where 32 bits do not hold x (both are not negative, d > 0).
