@@ -25,7 +25,12 @@
 //     o_d     = sum_t p_t min_tg  +  sum_t w_tg c_td,  w_tg = p_t scale_tg
 // The operands are fp16; w goes in as its rounding and the rest, 22 bits together: a row whose
 // weight lies on a few slots would otherwise carry their rounding in all of its values (half a step,
-// 2.4e-4, against the output's own).  A nibble in bits 4-7 of a 16-bit half is the fp16 subnormal
+// 2.4e-4, against the output's own).  Both are of w times a power of two F that brings the largest V
+// scale met so far to 2^12 .. 2^13 (Fit below; undone where a block's products are added in fp32), so
+// that what the pair's last place, 2^-24, drops is 2^-37 of that scale for every slot: without F a
+// slot with w below 2^-25 lost its codes and kept its minimum, and thousands of them beside one slot
+// with most of the weight were 2 to 30 % of an output (16384 slots, 2 % of the weight off that slot, V
+// scales of 0.03 and 0.001).  A nibble in bits 4-7 of a 16-bit half is the fp16 subnormal
 // c * 2^-20, exact, so that an AND, and for some a shift or a multiplication, unpacks a pair of codes,
 // and the fp32 results are rescaled.  Not bits 0-3, which two of four nibbles would reach without a
 // shift: the tensor core aligns a product by its operands' exponents, -14 for every subnormal, and
@@ -404,6 +409,26 @@ struct Copies {
   }
 };
 
+// The power of two by which a run's weights w = p * scale are multiplied on their way into fp16.  It
+// starts where the smallest scale, 2^-24, wants it and falls when a scale does not fit: scale * f <=
+// kFits and p <= 2^kSlack leave w * f <= 2^15.  Uniform in the warp.  The check of every block's scales
+// costs 1 to 3 % (512 sequences of 513 to 544 slots, 32 heads of 128: 225.2 to 227.5 us; 24 ragged ones
+// of up to 16384, 8 columns a head: 77.5 to 79.7); the scales kept in registers from the check to their
+// use, and compared in fp16 pairs, measured the same or up to 1.6 % more.
+constexpr float kFits = 8192.0f;
+
+struct Fit {
+  float f, inv;
+  __device__ __forceinline__ Fit() : f(68719476736.0f), inv(1.0f / 68719476736.0f) {}  // 2^36
+  // `scale`: the warp's largest, above kFits / f.  Its exponent e gives f = 2^(12 - e); fp16's largest
+  // is taken for an infinite one.
+  __device__ __forceinline__ void fall(float scale) {
+    const uint32_t e = min(__float_as_uint(scale) >> 23, 127u + 15u);
+    f = __uint_as_float((127u + 12u + 127u - e) << 23);
+    inv = __uint_as_float((e - 12u) << 23);
+  }
+};
+
 // The weights of the 4 slots t .. t + 3 (t % 4 == 0, so that they lie in one page), of which those
 // below `end` grow.
 __device__ __forceinline__ void grow4(const PagedAttnArgs &a, int s, int h, int t, int end, float4 add) {
@@ -586,6 +611,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   const __half *const nbase = reinterpret_cast<const __half *>(wbase + 2 * S::CODE_B) + gid * NG;
   const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
 
+  Fit fit;
   float m[NT][2], l[NT][2];
   float vacc[NT][2][NG];   // sum of p min over this lane's slots
   float ov[NT][CH][2][4];  // chunk ch, x: dims 32 ch + 4 gid + 2x ([0], [1]: columns 2c, 2c+1) and + 1 ([2], [3])
@@ -673,9 +699,18 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
               }
     }
     // ---- running maximum: moves only when a score exceeds it by more than kSlack, so that
-    //      p = 2^(s - m) <= 2^kSlack and w = p * scale stays inside fp16 ----
+    //      p = 2^(s - m) <= 2^kSlack and w = p * scale * fit.f stays inside fp16 ----
+    const __half *const vs0 = nbase + OFF / 2 + 3 * kBlock * NG;  // V scales of slots gid, gid + 8, ..
+    float vmax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const Nums<NG> v(vs0 + 8 * i * NG);
+#pragma unroll
+      for (int g = 0; g < NG; g++)
+        if (!EDGE || t + 8 * i + gid < t_end) vmax = fmaxf(vmax, fabsf(v.get(g)));
+    }
     float cmax[NT][2];
-    bool moves = false;
+    bool moves = vmax * fit.f > kFits;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -685,6 +720,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
         moves |= cmax[nt][e] > m[nt][e] + kSlack;
       }
     if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+      if (vmax * fit.f > kFits) fit.fall(vmax);
 #pragma unroll
       for (int nt = 0; nt < NT; nt++) {
         float al[2];
@@ -732,7 +770,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
       for (int g = 0; g < NG; g++)
 #pragma unroll
         for (int x = 0; x < 2; x++) {
-          const float vs = vsc[x].get(g), vb = vm[x].get(g);
+          const float vs = vsc[x].get(g) * fit.f, vb = vm[x].get(g);
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
             float w0 = p[nt][x][0] * vs, w1 = p[nt][x][1] * vs, o0 = p[nt][x][0] * vb, o1 = p[nt][x][1] * vb;
@@ -779,7 +817,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
             mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], bl[1][nt][g][0], bl[1][nt][g][1]);
             float(&o)[4] = ov[nt][ch + y][x];
 #pragma unroll
-            for (int i = 0; i < 4; i++) o[i] += d[i];
+            for (int i = 0; i < 4; i++) o[i] = fmaf(d[i], fit.inv, o[i]);
           }
         }
     }
@@ -1033,6 +1071,7 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   const __half *const nbase = reinterpret_cast<const __half *>(wbase + 2 * S::CODE_B) + tq * NG + g;
   const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
 
+  Fit fit;
   float m = -INFINITY, l = 0.f, vacc = 0.f;
   float ov[CH][2][2];  // chunk ch, x: dims 32 ch + 4 gid + 2x and + 1
 #pragma unroll
@@ -1089,10 +1128,22 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
           if (!EDGE || t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u] * kScore;
     }
     float cmax = fmaxf(sc[0], sc[1]) * kScore;  // scores are held over kUnit
-    if (__any_sync(0xffffffffu, cmax > m + kSlack)) {  // the running maximum moves
+    float vs[2];
+#pragma unroll
+    for (int u = 0; u < 2; u++) {
+      vs[u] = __half2float(nbase[OFF / 2 + (3 * kBlock + 16 * u) * NG]);
+      if (EDGE && t + 16 * u + tq >= t_end) vs[u] = 0.f;  // masked slots may hold anything
+    }
+    const float vmax = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
+    if (__any_sync(0xffffffffu, cmax > m + kSlack || vmax * fit.f > kFits)) {  // the running maximum moves, or F falls
+      float v = vmax;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+      if (v * fit.f > kFits) fit.fall(v);
 #pragma unroll
       for (int o = 2; o < 32; o <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
-      const float al = fast_exp2(m - cmax);
+      cmax = fmaxf(m, cmax);
+      const float al = cmax == -INFINITY ? 1.f : fast_exp2(m - cmax);
       m = cmax;
       l *= al;
       vacc *= al;
@@ -1109,8 +1160,8 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
     for (int u = 0; u < 2; u++) {
       const __half *n = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG;
       const float p = fast_exp2(fmaf(sc[u], kScore, -m));
-      float w = p * __half2float(n[kBlock * NG]), pm = p * __half2float(n[0]);
-      if (EDGE && t + 16 * u + tq >= t_end) w = pm = 0.f;  // masked slots may hold anything (their p is 0)
+      float w = p * (vs[u] * fit.f), pm = p * __half2float(n[0]);
+      if (EDGE && t + 16 * u + tq >= t_end) w = pm = 0.f;  // (their p is 0)
       l += p;
       vacc += pm;
       // w rounded, and the rest, in columns 2c and 2c+1 of the slot's row
@@ -1143,8 +1194,8 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
           float d[4];
           mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][0], b[0][1]);
           mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], b[1][0], b[1][1]);
-          ov[ch + y][x][0] += d[0] + d[1];  // both columns of w
-          ov[ch + y][x][1] += d[2] + d[3];
+          ov[ch + y][x][0] = fmaf(d[0] + d[1], fit.inv, ov[ch + y][x][0]);  // both columns of w
+          ov[ch + y][x][1] = fmaf(d[2] + d[3], fit.inv, ov[ch + y][x][1]);
         }
     }
   };

@@ -414,6 +414,186 @@ def test_attention_is_deterministic():
         assert torch.equal(o, got[0][0]) and torch.equal(w, got[0][1])
 
 
+# ------------------------------------------------------------------ one slot with most of the weight --------------
+#
+# A query row with a single one in it reads one dim of the keys, whose minima and steps are multiples of 2^-6: scores are
+# exact, and what is left of the tolerance above is the weights' own.  With T the span of a row's scores (nats):
+#   p       the product with log2 e and its subtraction from the running maximum, 2^-23 T each, exp2 2^-22 and the same
+#           for rescalings: (T + 8) 2^-22 of it
+#   sums    a warp that has all slots adds two a block of 32 to a lane's sums: (n / 16 + 16) 2^-24 of their terms, and the
+#           same for the sum that divides
+#   w       two fp16 numbers, 2^-22 of w, of w times a power of two under which the run's largest scale lies in [2^12,
+#           2^13]: where the second is subnormal 2^-25 absolute of that, 2^-37 max scale, against codes of 15
+#   MMA     16 products aligned to the largest: 2^-13 sum p scale, as above
+#   output  2^-11 of it, 2^-25 where it is subnormal
+# With N = sum p (|min| + 15 scale) and l = sum exp(s - max s):
+#   |out - ref| <= 2^-11 |ref| + 2^-25 + (2^-13 + 15 * 2^-22) sum p scale + 15 * 2^-37 n max scale / l
+#                  + 2 ((T + 8) 2^-22 + (n / 16 + 16) 2^-24) N
+
+
+def sink_cache(rng, n, H, D, G, ps, vscale, span, track=False, sink=0, step=2.0**-3):
+    """A sequence of n slots whose dim scores are -span + step code for all slots but `sink`, whose own is 0 with V a tenth of
+    the others' size.  V's scales lie around vscale, its minima at -7.5 scales."""
+    c = make_cache(rng, [n], H, D, G, ps, track=track)
+    t = c.page_table[0].cpu().numpy()
+    page, off = t[np.arange(n) // ps], np.arange(n) % ps
+    NG = D // G
+    km, ks = np.full((n, H, NG), -span, np.float16), np.full((n, H, NG), step, np.float16)
+    km[sink], ks[sink] = 0, 0
+    vs = (vscale * np.exp(0.2 * rng.normal(size=(n, H, NG)))).astype(np.float16)
+    vs[sink] = np.float16(vscale * 0.1)
+    vm = (-7.5 * vs.astype(np.float64)).astype(np.float16)
+    at = (torch.from_numpy(page).long().cuda(), slice(None), torch.from_numpy(off).cuda())
+    for pool, x in ((c.k_mins, km), (c.k_scales, ks), (c.v_mins, vm), (c.v_scales, vs)):
+        pool[at] = torch.from_numpy(x).cuda()
+    return c
+
+
+def unit_queries(rows, heads, D, size=1.0):
+    """Row r's head h: `size` at one dim, another for every row and head; zeros else."""
+    q = np.zeros((rows, heads, D), np.float16)
+    for r in range(rows):
+        for h in range(heads):
+            q[r, h, (7 * r + 13 * h + 3) % D] = size
+    return torch.from_numpy(q.reshape(rows, -1)).cuda()
+
+
+def sharp_attention(cache, q, n, rows):
+    """(out, tolerance, growth, its tolerance) of the rows of a sequence with n slots in all, by the formulas above."""
+    q = q.cpu().numpy().astype(np.float64)
+    D, H = cache.head_dim, cache.num_heads
+    q = q.reshape(rows, H, -1, D)
+    k, _, _ = values(cache, 0, n, "k")
+    v, va, vs = values(cache, 0, n, "v")
+    out, tol = np.zeros_like(q), np.zeros_like(q)
+    add, add_tol = np.zeros((H, n)), np.zeros((H, n))
+    for r in range(rows):
+        m = n - rows + r + 1
+        sc = np.einsum("hrd,htd->hrt", q[r], k[:, :m])
+        span = float((sc.max(-1) - sc.min(-1)).max())
+        e = np.exp(sc - sc.max(-1, keepdims=True))
+        l = e.sum(-1, keepdims=True)
+        p = e / l
+        mean = lambda x: np.einsum("hrt,htd->hrd", p, x[:, :m])
+        rel = (span + 8) * 2.0**-22 + (n / 16 + 16) * 2.0**-24
+        o = mean(v)
+        out[r] = o
+        tol[r] = (2.0**-11 * np.abs(o) + 2.0**-25 + (2.0**-13 + 15 * 2.0**-22) * mean(vs)
+                  + 15 * 2.0**-37 * m * vs[:, :m].max() / l + 2 * rel * mean(va))
+        add[:, :m] += p.sum(1)
+        add_tol[:, :m] += 2 * rel * p.sum(1)
+    return out.reshape(rows, -1), tol.reshape(rows, -1), add, add_tol
+
+
+def check_sharp(cache, q, n, rows=1, seqs=1, workspace=None, max_len=None, share=None):
+    """`seqs` sequences over the same pages (only read); share: the least part of the outputs' spread that the tolerance is."""
+    ref, tol, _, _ = sharp_attention(cache, q, n, rows)
+    if share is not None:
+        assert tol.max() <= share * np.abs(ref).max(), (tol.max(), np.abs(ref).max())
+    c = cache
+    if seqs > 1:
+        c = fg.PagedKVCache(cache.num_pages, cache.num_heads, cache.head_dim, cache.page_size,
+                            cache.page_table.repeat(seqs, 1).contiguous(), group=cache.group, arrays=cache.arrays())
+    pos = torch.full((seqs,), n - rows, dtype=torch.int32, device="cuda")
+    out = fg.fg_paged_attention(c, q.repeat(seqs, 1).contiguous(), pos, rows_per_seq=rows, max_len=max_len, workspace=workspace)
+    fg.fg_sync_status()
+    err = np.abs(out.view(seqs, rows, -1).cpu().numpy().astype(np.float64) - ref)
+    assert np.all(err <= tol), ((err / tol).max(), err.max(), np.abs(ref).max())
+
+
+SINKS = [  # D, G, page, kv heads, ratio, rows: one column, one tile, two tiles, four groups, several rows
+    (128, 64, 64, 2, 1, 1), (64, 64, 16, 2, 1, 1), (256, 128, 32, 1, 1, 1), (128, 128, 64, 1, 8, 1), (64, 64, 48, 1, 16, 1),
+    (256, 64, 16, 1, 4, 1), (128, 64, 32, 1, 3, 3)]
+
+
+def tail_span(n, mass=0.02, top=15 / 8):
+    """Nats below the sink at which n slots of -span + code / 8 hold about `mass` of the weight, a multiple of 1/8."""
+    return round(8 * np.log(n * np.expm1(top) / top / mass)) / 8
+
+
+@pytest.mark.parametrize("vscale", [0.03, 0.001])
+@pytest.mark.parametrize("way", ["short", "whole", "parts", "many"])
+@pytest.mark.parametrize("D,G,ps,H,R,rows", SINKS)
+def test_attention_sink_and_small_values(D, G, ps, H, R, rows, way, vscale):
+    """One slot with 98 % of the weight and the rest on thousands, V small: the rest's share of the output stands.  In one
+    run of a warp or CTA (short, whole, many: more items than warps), and in parts."""
+    rng = np.random.default_rng(D + R + len(way))
+    n = 1000 if way == "short" else 16384
+    c = sink_cache(rng, n, H, D, G, ps, vscale, tail_span(n))
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    check_sharp(c, unit_queries(rows, H * R, D), n, rows, seqs=2600 // H if way == "many" else 1,
+                workspace=none if way == "whole" else None, max_len=n, share=0.01)
+
+
+@pytest.mark.parametrize("sink", [0, 777, 15000, 16383])
+@pytest.mark.parametrize("R", [1, 4])
+def test_attention_sink_anywhere(R, sink):
+    n = 16384
+    c = sink_cache(np.random.default_rng(sink), n, 1, 128, 64, 64, 0.002, tail_span(n), sink=sink)
+    check_sharp(c, unit_queries(1, R, 128), n, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"), share=0.01)
+
+
+@pytest.mark.parametrize("R", [1, 5])
+@pytest.mark.parametrize("D,G", [(64, 64), (128, 64), (256, 64), (256, 128)])
+@pytest.mark.parametrize("span,n", [(0.0, 700), (300.0, 700), (300.0, 5000), (1.0, 1)])
+def test_attention_exact_scores(D, G, R, span, n):
+    """Equal and one-hot softmaxes of exact scores: the outputs to their own rounding and the sums'."""
+    rng = np.random.default_rng(n + R)
+    c = sink_cache(rng, n, 2, D, G, 32, 0.3, span, step=0.0)
+    check_sharp(c, unit_queries(1, 2 * R, D), n, share=0.01 if span else None)
+
+
+@pytest.mark.parametrize("R", [1, 4])
+@pytest.mark.parametrize("per_slot", [2.0**-6, 2.0**-5])
+def test_attention_largest_scales_and_rising_scores(R, per_slot):
+    """V from -65504 to 65504 (scales of 8733) under scores that rise by a binade or two from block to block: the running
+    maximum lags, and p is up to 4."""
+    rng = np.random.default_rng(R)
+    n, D = 700, 128
+    c = sink_cache(rng, n, 2, D, 64, 64, 1.0, 0.0, step=0.0)
+    t = c.page_table[0].cpu().tolist()
+    for i in range(n):
+        c.k_mins[t[i // 64], :, i % 64] = i * per_slot
+        c.v_mins[t[i // 64], :, i % 64] = -65504.0
+        c.v_scales[t[i // 64], :, i % 64] = 8733.0
+    q = unit_queries(1, 2 * R, D)
+    _, tol, _, _ = sharp_attention(c, q, n, 1)
+    assert tol.max() < 0.001 * 2 * 65504
+    check_sharp(c, q, n)
+
+
+@pytest.mark.parametrize("R", [1, 4, 12])
+def test_attention_scales_of_all_sizes(R):
+    """V's scales from 2^-24 to 8733 along the sequence, growing and shrinking, some 0: the tolerance is the largest's."""
+    rng = np.random.default_rng(R)
+    n, D = 3000, 128
+    c = sink_cache(rng, n, 1, D, 64, 64, 1.0, 0.0, step=2.0**-4)
+    t = c.page_table[0].cpu().tolist()
+    for i in range(n):
+        e = -24 + 37 * i / 2000 if i < 2000 else 13 - 37 * (i - 2000) / 1000
+        x = 0.0 if i % 17 == 0 else 2.0**e
+        c.v_scales[t[i // 64], :, i % 64] = x
+        c.v_mins[t[i // 64], :, i % 64] = -7.5 * x
+    for m in (30, 200, 1000, n):                                        # where only the small ones are seen, and all
+        check_sharp(c, unit_queries(1, R, D), m)
+
+
+@pytest.mark.parametrize("R", [1, 4])
+@pytest.mark.parametrize("n", [1000, 16384])
+def test_tracked_sink(R, n):
+    """The same with the weights gathered: the output and each slot's growth."""
+    D = 128
+    c = sink_cache(np.random.default_rng(n), n, 2, D, 64, 64, 0.01, tail_span(n), track=True)
+    c.weights.zero_()
+    q = unit_queries(1, 2 * R, D)
+    ref, tol, add, add_tol = sharp_attention(c, q, n, 1)
+    out = fg.fg_paged_attention(c, q, torch.tensor([n - 1], dtype=torch.int32, device="cuda"), accumulate=True, max_len=n)
+    fg.fg_sync_status()
+    assert np.all(np.abs(out.cpu().numpy().astype(np.float64) - ref) <= tol)
+    got = dense(c, c.weights, 0, n).astype(np.float64)
+    assert np.all(np.abs(got - add) <= add_tol + R * 2.0**-23 * add)
+
+
 # ------------------------------------------------------------------ eviction ----------
 
 
