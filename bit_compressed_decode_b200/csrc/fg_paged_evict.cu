@@ -411,7 +411,12 @@ __global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
 __global__ void paged_new_lengths_kernel(int32_t *lengths, int seqs, const EvictArgs a) {
   const int s = blockIdx.x, n = lengths[s];
   bool bad = n <= a.budget || n > a.limit;
-  for (int p = threadIdx.x * a.kv.ps; !bad && p < n; p += blockDim.x * a.kv.ps) bad = paged_slot(a.kv, s, 0, p) < 0;
+  // (page by page, not slot by slot: a page may have 2^30 slots)
+  const int pages = bad ? 0 : (n + a.kv.ps - 1) / a.kv.ps;
+  for (int i = threadIdx.x; i < pages; i += blockDim.x) {
+    const int page = a.kv.table[static_cast<int64_t>(s) * a.kv.max_pages + i];
+    bad |= page < 0 || page >= a.kv.num_pages;
+  }
   if (!__syncthreads_or(bad) && threadIdx.x == 0) lengths[s] = a.budget;
 }
 

@@ -729,6 +729,55 @@ def test_evict_flags_bad_sequences_only():
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+def evict_known(c, lengths, budget, gone, new_lengths=None):
+    """Evicts from a one-head cache whose weights are 1 but at the slots gone[s] (all below the budget), which are as many as
+    a sequence has above it, and checks what filled them; pages are the table's in order."""
+    ps = c.page_size
+    c.weights.fill_(1.0)
+    ln = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    at, fill = [], []
+    for s, n in enumerate(lengths):
+        if n <= budget:
+            continue
+        hole, mover = torch.tensor(sorted(gone[s]), device="cuda"), torch.arange(budget, n, device="cuda")
+        assert len(hole) == n - budget
+        t = c.page_table[s].long()
+        at.append((t[hole // ps], 0, hole % ps))
+        c.weights[at[-1]] = 0.0
+        src = (t[mover // ps], 0, mover % ps)
+        fill.append([a[src].clone() for a in c.arrays() + [c.weights, c.tokens]])
+    sums = [a.view(-1)[::4097].clone() for a in c.arrays()]             # what stays, by sample
+    new = fg.fg_paged_kv_evict(c, ln, ln, budget, 0, new_lengths=ln if new_lengths == "same" else None)
+    fg.fg_sync_status()
+    assert new.tolist() == [min(n, budget) for n in lengths]
+    for x, want in zip(at, fill):
+        for a, w in zip(c.arrays() + [c.weights, c.tokens], want):
+            assert torch.equal(a[x], w)
+    changed = sum(len(g) for g in gone)
+    for a, b in zip(c.arrays(), sums):
+        assert torch.count_nonzero(a.view(-1)[::4097] != b) <= changed
+
+
+@pytest.mark.parametrize("lengths", ["same", "apart"])
+@pytest.mark.parametrize("page_bits,pages,sizes,budget", [
+    (25, 1, [3000, 100, 2600], 2500),                                   # a page of max_len slots, as a contiguous cache has
+    (24, 2, [2**24 + 500, 2**24 - 700], 2**24 - 100)])                  # and lengths that end in a second one
+def test_evict_largest_pages(page_bits, pages, sizes, budget, lengths):
+    ps, S, D = 1 << page_bits, len(sizes), 64
+    if torch.cuda.mem_get_info()[0] < 3 * S * pages * ps * 80:
+        pytest.skip("not enough device memory")
+    rng = np.random.default_rng(page_bits)
+    order = torch.from_numpy(rng.permutation(S * pages).reshape(S, pages).astype(np.int32)).cuda()
+    c = fg.PagedKVCache(S * pages, 1, D, ps, order, track=True)
+    gen = torch.Generator("cuda").manual_seed(3)
+    for a in c.arrays():
+        a.copy_(torch.randint(0, 256, a.shape, dtype=torch.uint8, device="cuda", generator=gen))
+    c.tokens.copy_(torch.randint(0, 1 << 30, c.tokens.shape, dtype=torch.int32, device="cuda", generator=gen))
+    c.tokens.clamp_(max=budget - 1)                                     # (none counts as recent)
+    gone = [rng.choice(budget, max(0, n - budget), replace=False).tolist() for n in sizes]
+    evict_known(c, sizes, budget, gone, lengths)
+
+
 def test_evict_workspace():
     """More slots than a CTA's shared memory holds: scratch is asked for, and refused without."""
     c = make_cache(np.random.default_rng(2), [100, 100], 1, 64, 64, 64, track=True)
