@@ -350,61 +350,71 @@ __global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
   // ---- the moves: 16 bytes of codes at a time, and one number at a time (array by array, so that
   //      neighbouring moves' numbers are neighbours); V and N of them in flight per thread ----
   constexpr int V = B > 1 ? 2 : 4, N = B > 1 ? 2 : 3;  // (many CTAs per SM: fewer registers)
-  const int cv = a.code_vecs, vecs = moves * 2 * cv, nums = moves * 6;
+  // kMoves of them at a time, so that their vectors and numbers are counted in 32 bits (what fits in
+  // shared memory is less)
+  constexpr int kMoves = 1 << 24;
+  static_assert(kMoves * 16LL + 2 * V * T <= INT32_MAX && kMoves * 6LL + 2 * N * T <= INT32_MAX, "32-bit counters");
+  const int cv = a.code_vecs;
   const int cs = cv == 2 ? 1 : cv == 4 ? 2 : 3;  // log2(cv)
-  for (int v0 = tid, n0 = tid; v0 < vecs || n0 < nums; v0 += V * T, n0 += N * T) {
-    uint4 x[V];
-    uint4 *to[V];
+  int m0 = 0;
+  do {
+    const int count = Wide ? min(moves - m0, kMoves) : moves, vecs = count * 2 * cv, nums = count * 6;
+    const int *const hole = holes + m0, *const mover = movers + m0;
+    for (int v0 = tid, n0 = tid; v0 < vecs || n0 < nums; v0 += V * T, n0 += N * T) {
+      uint4 x[V];
+      uint4 *to[V];
 #pragma unroll
-    for (int u = 0; u < V; u++) {
-      const int v = v0 + u * T;
-      if (v < vecs) {
-        const int i = v >> (cs + 1), part = v & (2 * cv - 1);
-        uint4 *const pool = reinterpret_cast<uint4 *>(part >= cv ? a.kv.vc : a.kv.kc) + (part & (cv - 1));
-        to[u] = pool + pool_slot(holes[i]) * cv;
-        x[u] = pool[pool_slot(movers[i]) * cv];
+      for (int u = 0; u < V; u++) {
+        const int v = v0 + u * T;
+        if (v < vecs) {
+          const int i = v >> (cs + 1), part = v & (2 * cv - 1);
+          uint4 *const pool = reinterpret_cast<uint4 *>(part >= cv ? a.kv.vc : a.kv.kc) + (part & (cv - 1));
+          to[u] = pool + pool_slot(hole[i]) * cv;
+          x[u] = pool[pool_slot(mover[i]) * cv];
+        }
       }
-    }
-    uint2 y[N];
-    void *dst[N];
+      uint2 y[N];
+      void *dst[N];
 #pragma unroll
-    for (int u = 0; u < N; u++) {
-      const int k = n0 + u * T;
-      if (k < nums) {
-        const int arr = k / moves, i = k - arr * moves;
-        const int64_t src = pool_slot(movers[i]), d = pool_slot(holes[i]);
-        if (arr < 4) {
-          uint8_t *const b = reinterpret_cast<uint8_t *>(arr == 0   ? a.kv.km
-                                                         : arr == 1 ? a.kv.ks
-                                                         : arr == 2 ? a.kv.vm
-                                                                    : a.kv.vs);
-          dst[u] = b + d * a.meta;
-          if (a.meta == 4) y[u].x = *reinterpret_cast<const uint32_t *>(b + src * 4);
-          else if (a.meta == 2) y[u].x = *reinterpret_cast<const uint16_t *>(b + src * 2);
-          else y[u] = *reinterpret_cast<const uint2 *>(b + src * 8);
-        } else if (arr == 4) {
-          dst[u] = a.wout + d;
-          y[u].x = __float_as_uint(a.kv.weights[src]);
-        } else {
-          dst[u] = a.tout + d;
-          y[u].x = static_cast<uint32_t>(a.kv.tokens[src]);
+      for (int u = 0; u < N; u++) {
+        const int k = n0 + u * T;
+        if (k < nums) {
+          const int arr = k / count, i = k - arr * count;
+          const int64_t src = pool_slot(mover[i]), d = pool_slot(hole[i]);
+          if (arr < 4) {
+            uint8_t *const b = reinterpret_cast<uint8_t *>(arr == 0   ? a.kv.km
+                                                           : arr == 1 ? a.kv.ks
+                                                           : arr == 2 ? a.kv.vm
+                                                                      : a.kv.vs);
+            dst[u] = b + d * a.meta;
+            if (a.meta == 4) y[u].x = *reinterpret_cast<const uint32_t *>(b + src * 4);
+            else if (a.meta == 2) y[u].x = *reinterpret_cast<const uint16_t *>(b + src * 2);
+            else y[u] = *reinterpret_cast<const uint2 *>(b + src * 8);
+          } else if (arr == 4) {
+            dst[u] = a.wout + d;
+            y[u].x = __float_as_uint(a.kv.weights[src]);
+          } else {
+            dst[u] = a.tout + d;
+            y[u].x = static_cast<uint32_t>(a.kv.tokens[src]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < V; u++)
+        if (v0 + u * T < vecs) *to[u] = x[u];
+#pragma unroll
+      for (int u = 0; u < N; u++) {
+        const int k = n0 + u * T;
+        if (k < nums) {
+          const int meta = k < 4 * count ? a.meta : 4;
+          if (meta == 4) *static_cast<uint32_t *>(dst[u]) = y[u].x;
+          else if (meta == 2) *static_cast<uint16_t *>(dst[u]) = static_cast<uint16_t>(y[u].x);
+          else *static_cast<uint2 *>(dst[u]) = y[u];
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < V; u++)
-      if (v0 + u * T < vecs) *to[u] = x[u];
-#pragma unroll
-    for (int u = 0; u < N; u++) {
-      const int k = n0 + u * T;
-      if (k < nums) {
-        const int meta = k < 4 * moves ? a.meta : 4;
-        if (meta == 4) *static_cast<uint32_t *>(dst[u]) = y[u].x;
-        else if (meta == 2) *static_cast<uint16_t *>(dst[u]) = static_cast<uint16_t>(y[u].x);
-        else *static_cast<uint2 *>(dst[u]) = y[u];
-      }
-    }
-  }
+    m0 += kMoves;
+  } while (Wide && m0 < moves);
 }
 
 // new_lengths given as lengths itself: written once every CTA has read its length.

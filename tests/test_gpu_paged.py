@@ -778,6 +778,33 @@ def test_evict_largest_pages(page_bits, pages, sizes, budget, lengths):
     evict_known(c, sizes, budget, gone, lengths)
 
 
+def test_evict_more_moves_than_32_bits_of_vectors():
+    """2^27 slots of 256 values move: 2^31 vectors of codes.  k and v share their pools (both get the same moves)."""
+    n, D, ps = 1 << 28, 256, 1 << 20
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("not enough device memory")
+    pages = n // ps
+    codes = torch.empty((pages, 1, ps, D // 2), dtype=torch.uint8, device="cuda")
+    nums = torch.empty((pages, 1, ps, D // 128), dtype=torch.float16, device="cuda")
+    tokens = torch.arange(n, dtype=torch.int32, device="cuda").view(pages, 1, ps)
+    gen = torch.Generator("cuda").manual_seed(1)
+    for p in range(pages):
+        codes[p] = torch.randint(0, 256, codes[p].shape, dtype=torch.uint8, device="cuda", generator=gen)
+        nums[p] = torch.randn(nums[p].shape, dtype=torch.float16, device="cuda", generator=gen)
+    table = torch.from_numpy(np.random.default_rng(1).permutation(pages).reshape(1, -1).astype(np.int32)).cuda()
+    low, high = table[0, :pages // 2].long(), table[0, pages // 2:].long()
+    weights = torch.ones((pages, 1, ps), dtype=torch.float32, device="cuda")
+    weights[low] = 0.0
+    c = fg.PagedKVCache(pages, 1, D, ps, table, group=128, arrays=[codes, nums, nums] * 2, weights=weights, tokens=tokens)
+    i32 = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")
+    new = fg.fg_paged_kv_evict(c, i32(n), i32(2**30), n // 2, 0)
+    fg.fg_sync_status()
+    assert new.tolist() == [n // 2]
+    for a, b in zip(low.tolist(), high.tolist()):
+        for pool in (codes, nums, weights, tokens):
+            assert torch.equal(pool[a], pool[b])
+
+
 def test_evict_workspace():
     """More slots than a CTA's shared memory holds: scratch is asked for, and refused without."""
     c = make_cache(np.random.default_rng(2), [100, 100], 1, 64, 64, 64, track=True)
