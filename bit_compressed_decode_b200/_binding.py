@@ -351,7 +351,12 @@ class PagedKVCache:
     @staticmethod
     def from_cache(cache: KVCache, weights=None, tokens=None, track: bool = False) -> "PagedKVCache":
         """The contiguous cache as a paged one that shares its memory: one page of max_len slots per
-        sequence, so that a cache filled by fg_layer_prefill goes on in paged calls."""
+        sequence, so that a cache filled by fg_layer_prefill goes on in paged calls.  ``track=True``:
+        a slot's token is the slot's own number (as fg_paged_kv_append has it without first_tokens) and
+        its weight 0, where no pool is given for them."""
+        if track and tokens is None:
+            shape = (cache.num_seqs, cache.num_heads, cache.max_len)
+            tokens = torch.arange(cache.max_len, dtype=torch.int32, device=cache.k_codes.device).expand(shape).contiguous()
         table = torch.arange(cache.num_seqs, dtype=torch.int32, device=cache.k_codes.device).view(-1, 1)
         return PagedKVCache(cache.num_seqs, cache.num_heads, cache.head_dim, cache.max_len, table, group=cache.group,
                             arrays=cache.arrays(), weights=weights, tokens=tokens, track=track)

@@ -938,6 +938,24 @@ def test_prefilled_contiguous_cache_goes_on_in_paged_calls():
     check_evict(c, [P] * S, [P] * S, 16, 4)
 
 
+def test_prefilled_slots_carry_their_own_numbers():
+    """A prefilled cache that goes on as a tracked one: its prompt's last tokens are the recent ones."""
+    S, H, D, L, P, budget, recent = 2, 3, 64, 64, 40, 24, 16
+    cache = fg.KVCache(S, H, D, L)
+    k = torch.from_numpy(si.normal_f16(1, 22, (S * P, H * D), 1.0)).cuda()
+    v = torch.from_numpy(si.normal_f16(1, 23, (S * P, H * D), 1.0)).cuda()
+    fg.fg_kv_append(cache, k, v, torch.zeros(S, dtype=torch.int32, device="cuda"), rows_per_seq=P)
+    c = fg.PagedKVCache.from_cache(cache, track=True)
+    c.weights[:, :, :recent] = 1.0                                      # the oldest have all the weight
+    check_evict(c, [P] * S, [P] * S, budget, recent)
+    kept = c.tokens[:, :, :budget].cpu().numpy()
+    want = list(range(budget - recent)) + list(range(P - recent, P))
+    assert all(sorted(kept[s, h]) == want for s in range(S) for h in range(H))
+    given = torch.full_like(c.tokens, 7)                                # the caller's own pool stays as it is
+    assert fg.PagedKVCache.from_cache(cache, tokens=given, track=True).tokens is given and (given == 7).all()
+    assert fg.PagedKVCache.from_cache(cache).tokens is None
+
+
 def test_side_stream_and_graph_replay():
     """One step captured once and replayed, two graphs that share a workspace, and calls on a stream of their own."""
     rng = np.random.default_rng(21)
