@@ -324,6 +324,7 @@ class PagedKVCache:
         _need(page_table, torch.int32, "page_table")
         if page_table.dim() != 2:
             raise ValueError("page_table: expected [num_seqs, max_pages]")
+        group = group or 64  # (0: the default, as in fg.h)
         dev = page_table.device
         lead = (num_pages, num_heads, page_size)
         shapes = [lead + (head_dim // 2,), lead + (head_dim // group,), lead + (head_dim // group,)] * 2

@@ -1050,6 +1050,18 @@ def test_evict_in_a_graph():
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
+def test_group_zero_is_the_default():
+    table = torch.tensor([[0]], dtype=torch.int32, device="cuda")
+    a, b = (fg.PagedKVCache(1, 2, 128, 16, table, group=g) for g in (0, 64))
+    assert a.group == 64 and [x.shape for x in a.arrays()] == [x.shape for x in b.arrays()]
+    x = torch.from_numpy(si.normal_f16(1, 22, (1, 256), 1.0)).cuda()
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for c in (a, b):
+        fg.fg_paged_kv_append(c, x, x, zero)
+    fg.fg_sync_status()
+    assert all(torch.equal(p, q) for p, q in zip(a.arrays(), b.arrays()))
+
+
 def test_binding_refuses_what_it_can_see():
     rng = np.random.default_rng(1)
     c = make_cache(rng, [40, 40], 2, 128, 64, 16, track=True)
