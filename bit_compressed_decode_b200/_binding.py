@@ -386,7 +386,7 @@ def _rows(t: torch.Tensor, cache: PagedKVCache, name: str) -> tuple:
     ld, one = t.stride()
     if one != 1 and m > 1:
         raise ValueError(f"{name}: expected rows of unit element stride")
-    return n, m, ld if n > 1 or ld > m else m  # (a single row's stride says nothing)
+    return n, m, ld if n > 1 else m  # (a single row's stride says nothing)
 
 
 def _ints(t, cache: PagedKVCache, name: str, n: int):

@@ -1062,6 +1062,22 @@ def test_group_zero_is_the_default():
     assert all(torch.equal(p, q) for p, q in zip(a.arrays(), b.arrays()))
 
 
+def test_single_rows_of_any_stride():
+    """One row has no next one: k and v, q and out may come from tensors of different and of odd widths."""
+    H, R, D = 2, 2, 128
+    a, b = (make_cache(np.random.default_rng(3), [40], H, D, 64, 16) for _ in range(2))
+    pos = torch.tensor([39], dtype=torch.int32, device="cuda")
+    q, x = queries(np.random.default_rng(4), 1, H * R, D), queries(np.random.default_rng(5), 1, H * D, 1)
+    odd = lambda t, n: torch.cat([t, torch.zeros((1, n), dtype=t.dtype, device="cuda")], 1).repeat(2, 1)[:1, :t.shape[1]]
+    fg.fg_paged_kv_append(a, x, x, pos)
+    fg.fg_paged_kv_append(b, odd(x, 3), odd(x, 8), pos)
+    want = fg.fg_paged_attention(a, q, pos)
+    got = fg.fg_paged_attention(b, odd(q, 5), pos, out=odd(torch.zeros_like(q), 1))
+    fg.fg_sync_status()
+    assert all(torch.equal(m.view(torch.uint8), n.view(torch.uint8)) for m, n in zip(a.arrays(), b.arrays()))
+    assert torch.equal(want, got)
+
+
 def test_binding_refuses_what_it_can_see():
     rng = np.random.default_rng(1)
     c = make_cache(rng, [40, 40], 2, 128, 64, 16, track=True)
