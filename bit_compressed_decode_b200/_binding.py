@@ -374,8 +374,9 @@ class PagedKVCache:
 
 # The paged calls take a few microseconds of host time each, which is what a small launch costs: one
 # comparison per property of a tensor, plain integers for pointers, no objects per call.
-_get_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# (The two short ways are torch's own; a torch without them imports this file and has the public ones.)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _rows(t: torch.Tensor, cache: PagedKVCache, name: str) -> tuple:

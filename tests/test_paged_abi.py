@@ -1,5 +1,8 @@
 """Host checks of the paged KV cache's entry points (CPU only: no call here reaches a CUDA launch)."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -93,3 +96,23 @@ def test_evict_refusals():
     assert evict(max_len=-1) == INVALID
     assert evict(lengths=None) == INVALID and evict(next=None) == INVALID and evict(new=None) == INVALID
     assert evict(wout=P + 2) == INVALID and evict(tout=P + 1) == INVALID and evict(ws=P + 8) == INVALID
+
+
+def test_import_without_torch_internals():
+    """A torch built without CUDA has neither name; the package imports there and its host checks answer."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import bit_compressed_decode_b200 as fg
+try:
+    fg.PagedKVCache(4, 2, 128, 16, torch.zeros((1, 4), dtype=torch.int32))
+except ValueError as e:
+    assert "page_table" in str(e)
+else:
+    raise SystemExit("a table on the CPU was taken")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
