@@ -430,6 +430,12 @@ __global__ void paged_new_lengths_kernel(int32_t *lengths, int seqs, const Evict
   if (!__syncthreads_or(bad) && threadIdx.x == 0) lengths[s] = a.budget;
 }
 
+// Two arrays of n numbers have memory in common.
+bool overlap(const int32_t *a, const int32_t *b, int n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b), size = 4 * static_cast<uintptr_t>(n);
+  return x < y + size && y < x + size;
+}
+
 struct EvictPlan {
   bool wide;
   int threads, keys, pages, list, words;
@@ -489,6 +495,9 @@ extern "C" fg_status fg_paged_kv_evict(const fg_paged_kv *kv, const int32_t *len
   if (kv->num_seqs == 0) return FG_OK;
   if (!lengths || !next_tokens || !new_lengths || !fg_aligned16(workspace)) return FG_ERR_INVALID;
   if (!fg_aligned16(weights_out) || !fg_aligned16(tokens_out)) return FG_ERR_INVALID;
+  // (one head's CTA writes a sequence's new length while the others may not have read their inputs)
+  if (new_lengths != lengths && (overlap(new_lengths, lengths, kv->num_seqs) || overlap(new_lengths, next_tokens, kv->num_seqs)))
+    return FG_ERR_INVALID;
   if (static_cast<int64_t>(kv->num_seqs) * kv->num_heads > INT32_MAX) return FG_ERR_SHAPE;
   const EvictPlan p = evict_plan(kv, budget, max_len);
   if (p.lists > (workspace ? workspace_bytes : 0)) return FG_ERR_WORKSPACE;

@@ -273,7 +273,8 @@ FG_API fg_status fg_paged_attention(const fg_paged_kv *kv, const fg_half *q, int
  * into the holes below it, with their weight and token: attention does not depend on the slots'
  * order, and what moves is as little as the eviction frees.  new_lengths[s] = min(lengths[s],
  * budget); the pages behind are the caller's again.  Sequences within the budget are not touched.
- *   lengths, next_tokens, new_lengths: int32 device [num_seqs] (new_lengths may be lengths);
+ *   lengths, next_tokens, new_lengths: int32 device [num_seqs] (new_lengths may be lengths, and
+ *   overlaps neither of the others if it is not);
  *   next_tokens: the number that the sequence's next token will get.
  *   weights_out, tokens_out: pools like weights and tokens that receive the kept slots' numbers in
  *   place of those (every slot below new_lengths[s], moved or not); NULL, or the pool itself: in place.

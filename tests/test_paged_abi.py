@@ -98,6 +98,14 @@ def test_evict_refusals():
     assert evict(wout=P + 2) == INVALID and evict(tout=P + 1) == INVALID and evict(ws=P + 8) == INVALID
 
 
+def test_evict_refuses_lengths_that_are_written_while_they_are_read():
+    for new in (P * 2, P * 2 + 12, P * 2 - 12, P + 4, P - 4):           # next_tokens, or part of an input
+        assert evict(new=new) == INVALID
+    for clear in (dict(new=P * 2 + 16), dict(new=P * 2 - 16), dict(new=P), dict(new=P, next=P)):
+        assert evict(**clear, ws=P + 8) == INVALID                      # (refused for its workspace alone:)
+        assert evict(kv=cache(page_size=1 << 20), **clear) == WORKSPACE # beside, or the lengths in place
+
+
 def test_import_without_torch_internals():
     """A torch built without CUDA has neither name; the package imports there and its host checks answer."""
     code = """
