@@ -313,22 +313,14 @@ __global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
       hole = ~kept & mask;  // (the budget is below n: all of these are slots)
       mover = kept & ~mask;
     }
-    int th, tm, hi, mi;
-    if (a.list < 65536) {  // both counts in one scan
-      int total;
-      const int v = scan(__popc(hole) | __popc(mover) << 16, &total);
-      hi = v & 0xFFFF, mi = static_cast<unsigned>(v) >> 16;
-      th = total & 0xFFFF, tm = static_cast<unsigned>(total) >> 16;
-    } else {
-      hi = scan(__popc(hole), &th), mi = scan(__popc(mover), &tm);
-    }
-    hi += hole0, mi += mover0;
+    static_assert(32 * T < 65536, "holes and movers of T words in 16 bits each");
+    int total;
+    const int v = scan(__popc(hole) | __popc(mover) << 16, &total);  // both counts in one scan
     // the lists: the words in turn to the warps, a lane a bit (the histogram's place is free)
     if (w < words) {
       above[w] = mover;
       equal[w] = hole;
-      hist[tid] = hi;
-      hist[T + tid] = mi;
+      hist[tid] = v;
     }
     __syncthreads();
     const uint32_t below = (1u << lane) - 1u;
@@ -336,13 +328,14 @@ __global__ void __launch_bounds__(T, B) paged_evict_kernel(const EvictArgs a) {
       const uint32_t hw = equal[w0 + i], mw = above[w0 + i];
       if ((hw | mw) == 0) continue;
       const int p = 32 * (w0 + i) + lane;
-      const int hx = hist[i] + __popc(hw & below), mx = hist[T + i] + __popc(mw & below);
+      const unsigned at = hist[i];
+      const int hx = hole0 + (at & 0xFFFF) + __popc(hw & below), mx = mover0 + (at >> 16) + __popc(mw & below);
       if (hw >> lane & 1u && hx < a.list) holes[hx] = p;
       if (mw >> lane & 1u && mx < a.list) movers[mx] = p;
     }
     __syncthreads();
-    hole0 += th;
-    mover0 += tm;
+    hole0 += total & 0xFFFF;
+    mover0 += static_cast<unsigned>(total) >> 16;
   }
   const int moves = min(min(hole0, mover0), a.list);  // (as many of the ones as of the others)
   __syncthreads();

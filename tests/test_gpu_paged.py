@@ -702,6 +702,15 @@ def test_evict_long(n, budget, weights):
     check_evict(c, [n, 100], [n, 100], budget, min(budget, 128), max_len=n)
 
 
+@pytest.mark.parametrize("n,budget", [(140001, 70000), (131072, 65536)])
+def test_evict_more_than_65535_moves(n, budget):
+    """Holes and movers past 16 bits, all of a word's slots among them."""
+    c = make_cache(np.random.default_rng(n), [n], 1, 64, 64, 64, track=True)
+    tokens_in_order(c, [n])
+    c.weights.copy_(torch.where(c.tokens >= budget, 1.0 + c.weights, 0.0))
+    check_evict(c, [n], [n], budget, 0, max_len=n)
+
+
 def test_evict_writes_lengths_in_place():
     rng = np.random.default_rng(4)
     lengths = [300, 20, 64, -1, 0]
