@@ -965,6 +965,44 @@ def test_prefilled_slots_carry_their_own_numbers():
     assert fg.PagedKVCache.from_cache(cache).tokens is None
 
 
+def test_decode_layer_over_pages():
+    """A decode layer put together from the public calls over shuffled pages, against fg_layer_decode over the contiguous
+    cache: the same bits in the cache, the layer's output within 1e-2 of its change (what the layer's own tests allow)."""
+    h, H, F, S, P, ps, L = 256, 4, 512, 3, 20, 16, 64
+    D, qs = h // H, (h // H)**-0.5
+    cfg = fg.LayerConfig(h, H, F)
+    lw = fg.LayerWeights.from_fp16(cfg, si.layer_weights_f16(0, h, F, std=0.05, bias_std=0.05, ln_random=True))
+    flat = fg.KVCache(S, H, D, L)
+    x = torch.from_numpy(si.hidden_block(0, si.STREAM["prompt"], S, P, h)).cuda()
+    fg.fg_layer_prefill(cfg, lw, flat, x, torch.zeros(S, dtype=torch.int32, device="cuda"))
+    table = torch.from_numpy(np.random.default_rng(1).permutation(S * (L // ps)).reshape(S, -1).astype(np.int32)).cuda()
+    paged = fg.PagedKVCache(S * (L // ps), H, D, ps, table, track=True)
+    at = table.long()
+    pages = lambda a: a.view(S, H, L // ps, ps, -1).transpose(1, 2)
+    for a, b in zip(flat.arrays(), paged.arrays()):
+        b[at] = pages(a)
+    m, v = lw.matrix, lw.vector
+    for step in range(3):
+        x = torch.from_numpy(si.decode_inputs(0, step, S, h)).cuda()
+        pos = torch.full((S,), P + step, dtype=torch.int32, device="cuda")
+        want = fg.fg_layer_decode(cfg, lw, flat, x, pos)
+        a = fg.fg_layernorm(x, v("ln1_g"), v("ln1_b"))
+        qkv = fg.fg_linear_w4a16(a, m("wqkv"), bias=v("bqkv"), qscale_cols=h, qscale=qs)
+        fg.fg_paged_kv_append(paged, qkv[:, h:2 * h], qkv[:, 2 * h:], pos)
+        o = fg.fg_paged_attention(paged, qkv[:, :h], pos, max_len=L, accumulate=True)
+        h1 = fg.fg_linear_w4a16(o, m("wo"), bias=v("bo"), residual=x)
+        f = fg.fg_linear_w4a16(fg.fg_layernorm(h1, v("ln2_g"), v("ln2_b")), m("w1"), bias=v("b1"), relu=True)
+        y = fg.fg_linear_w4a16(f, m("w2"), bias=v("b2"), residual=h1)
+        fg.fg_sync_status()
+        for p, q in zip(flat.arrays(), paged.arrays()):
+            assert torch.equal(pages(p)[:, :2], q[at][:, :2])
+        change = (want.double() - x.double()).abs().max()
+        assert (y.double() - want.double()).abs().max() <= 1e-2 * change
+    # a head's three rows of probabilities: sums of 1
+    total = paged.weights[at].sum((1, 3)).double()
+    assert (total - 3.0).abs().max() <= 3 * 64 * 2.0**-23
+
+
 def test_side_stream_and_graph_replay():
     """One step captured once and replayed, two graphs that share a workspace, and calls on a stream of their own."""
     rng = np.random.default_rng(21)
