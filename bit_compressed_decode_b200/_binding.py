@@ -459,7 +459,8 @@ def fg_paged_attention(cache: PagedKVCache, q: torch.Tensor, positions: torch.Te
                        out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                        stream=None) -> torch.Tensor:
     """Attention of q [rows, num_q_heads * head_dim] over the cache; ``accumulate=True`` adds each
-    slot's probabilities to ``cache.weights``.  ``workspace``: None allocates it."""
+    slot's probabilities to ``cache.weights``.  ``workspace``: None allocates it; with ``accumulate``
+    it grows with ``max_len`` (None: all that the table's pages hold), so give the bound there is."""
     rows, width, ldq = _rows(q, cache, "q")
     hq = width // cache.head_dim
     if hq * cache.head_dim != width:

@@ -57,8 +57,10 @@ struct AppendArgs {
 // consecutive in the pool.  The group numbers (2 to 8 bytes of a row and array) go through shared
 // memory, so that a lane stores a row's of one array and the warp stores whole sectors where the
 // rows are a prompt's.  Bound: 4 D bytes read and D + 8 D/G written per row and head; what it spends
-// is instructions, 83 % of the issue slots (the quantiser's fp32 steps): 32 prompts of up to 512
-// tokens, 56 heads of 128, 315 MB in 95 us, 3.3 TB/s (a warp per row and head: 217 us).
+// is instructions, 83 % of the issue slots: the quantiser's fp32 steps, which alone run at 0.77 of a
+// copy's rate, and its own slots, shuffles and divisions, with no next tile's loads in flight behind
+// them.  32 prompts of up to 512 tokens, 56 heads of 128, 315 MB in 95 to 103 us, 3.3 to 3.0 TB/s (a
+// warp per row and head: 217 us).
 template <int D>
 struct Append {
   static constexpr int R = D == 256 ? 4 : 8;       // rows per warp

@@ -17,8 +17,8 @@
 // (page_size % 16 == 0), six copies each, issued by as many lanes; the lanes look the page table up
 // for 32 blocks at a time.  Two unrolled stages measured 210 us where three in a ring, whose
 // addresses are computed, took 219 (512 sequences of 513 to 544 slots, 32 heads of 128: 1.26 GB; 227
-// us since the sums are exact, 5.5 TB/s of 6.46 measured for a copy).  Which warp takes which blocks:
-// make_plan below.
+// us since the sums are exact, 5.5 TB/s of 6.46 measured for a copy; up to 265 on other cards and
+// power states).  Which warp takes which blocks: make_plan below.
 //
 // Both products run on the tensor cores straight from the codes (the group decomposition):
 //     q . k_t = sum_g ( min_tg * sum_{d in g} q_d  +  scale_tg * sum_{d in g} q_d c_td )
@@ -44,7 +44,8 @@
 // in fp32 registers: the tensor core's additions truncate, which grows with a sum.
 // What the tile kernel costs beyond the bytes is the fixed part of a launch (7 us from its start to
 // the first block's arrival, 6 us of join) and instructions: 24 sequences of 8192 slots and 8 heads of
-// 8 columns take 68 us for 214 MB.
+// 8 columns take 69 us for 214 MB.  Rows beyond a tile's 8 columns unpack the codes again: 512 rows of
+// 8 prompts of 512 over 8 heads of 128 take 125 us.
 #include <math.h>
 
 #include <type_traits>
@@ -1530,11 +1531,18 @@ void plan_bytes(Plan *p, int64_t items, int D, int limit, bool accumulate) {
 // share all blocks evenly (Walk) and a join.  Direct is for short items, and for somewhat longer
 // ones where there are many: 30 sequences of 2000 slots and 32 heads of 128 took 58.8 us direct and
 // 62.3 partitioned, 8 of them 23.9 and 26.0, one 21.4 and 19.5; 64 tracked ones of 1500 to 2112
-// slots 120 and 133; 24 ragged ones of up to 16384 slots and 8 shared heads 95 and 79.
+// slots 120 and 133; 24 ragged ones of up to 16384 slots and 8 shared heads 95 and 79.  The tile
+// kernel wants nearly the same limits (4 columns, heads of 128, half to all of the length; us direct
+// and partitioned): 500 slots, 8 items 10.6 and 13.7, 1200 items 42 and 50; 1000 slots, 8 items 15.2
+// and 14.3, 240 items 18 and 25; 2000 slots, 64 items 24 and 20, 240 items 30 and 34, 1200 items 94
+// and 96; 4000 slots, 240 items 51 and 44.  They are off by 11 % at 4000 slots and 1200 items (162 and
+// 146; tracked 259 and 213) and, tracked, by 15 to 21 % for a few items of 1000 slots (20.3 and 17.5); a
+// single column's by 4 to 15 % from 1200 items on (500 slots, 4800 items: 89 and 78).
 // Two column tiles to an item halve the unpacking; heads of 64 have the registers for it (24
 // sequences of 8192 slots, 8 heads of 16 columns: 77 us instead of 89).
 // Accumulating launches take the column tiles one after the other, so that a slot's weight is grown
-// by one CTA at a time and in a fixed order.
+// by one CTA at a time and in a fixed order; each reads the cache again (16 sequences of 4096 slots, 8
+// heads of 12 columns: 111 us, of 8 columns 60; the 512 prompt rows above, 64 tiles: 1.07 ms).
 Plan make_plan(int64_t pairs, int cols, int D, int G, int limit, bool accumulate, int64_t *items) {
   Plan p;
   p.one = cols == 1 && D / G <= 2;

@@ -246,11 +246,12 @@ FG_API fg_status fg_paged_kv_append(const fg_paged_kv *kv, const fg_half *k, con
  * num_heads, and the query heads j*R .. j*R + R-1 (R their ratio) read key-value head j.  Row i of
  * sequence s (r = s * rows_per_seq + i) sees the slots 0 .. positions[s] + i:
  *   p_t = softmax over them of q . k_t,  out = sum_t p_t v_t,  k_t, v_t = min + code * scale
- * (not rounded to fp16 in between; fp32 sums and softmax).  accumulate = 1 (needs weights): each
- * slot's weight grows by the sum over the call's rows and the R query heads of p_t, in a fixed
- * order: the same bits from run to run.
+ * (not rounded to fp16 in between; fp32 sums and softmax, p_t * scale in 22 bits, whatever the
+ * scales' size).  accumulate = 1 (needs weights): each slot's weight grows by the sum over the call's
+ * rows and the R query heads of p_t, in a fixed order: the same bits from run to run.
  * Rows i >= row_counts[s] and sequences with positions[s] = -1 see nothing: their output is zero.
- * max_len: a bound on the slots that any row sees, for the launch's plan (0: max_pages *
+ * max_len: a bound on the slots that any row sees, for the launch's plan and, with accumulate, the
+ * workspace, which holds a score for each of them per column and head (0: max_pages *
  * page_size).  A sequence with a row that would see more, a position below -1 or a bad count flags
  * FG_ERR_RANGE; its rows are zero and its weights do not grow.  A row that sees a slot in a bad page
  * flags it too and is zero; the sequence's other rows are zero or as they would be, and its weights
