@@ -544,406 +544,408 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<D, G, NT>::kCtas) paged_att
   uint32_t phase = 0;  // bit i: the parity of stage i's next phase
 
   while (true) {  // segments
-  const Walk walk = walks[warp];
-  const int ht = walk.ht, item = walk.s * a.kv.H * a.tiles + ht;
-  const Item it = load_item(a, walk.s, ht, !a.units && first == 0 && lane == 0);
-  // live columns' lengths: rows ascend with the column, so the last live one sees most
-  int lmin = 0, lmax = 0;
-  {
-    const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
-    if (last >= it.n0) {
-      lmin = it.len(it.n0, a.R);
-      lmax = it.len(last, a.R);
-    }
-  }
-  const int ran = a.units ? walk.run() : 0;
-  const int t_begin = a.units ? walk.b * kBlock : 0;
-  const int t_end = a.units ? min(lmax, t_begin + ran * kBlock) : lmax;
-  const int t_first = t_begin + first * kBlock;
-  const int steps = ok && t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
-  cp.bad = false;
-  if (steps > 0) {
-    cp.look_up(a, it.s, it.h, t_first, step, t_end, lane);
-    cp.issue(0, 0, bar0, lane);
-    if (steps > 1) cp.issue(1, S::STAGE_B, bar0 + 8, lane);
-  }
-  const Target target = target_of(a, walk, unit, item, ran, lane == 0);
-
-  // ---- q of column n0 + 8 nt + gid as the B operand of the score MMAs ----
-  // Word j of group g of lane class c: dims 2o .. 2o+7, o = g*G/2 + c*G/8 + 4j.  Low-nibble MMA
-  // (nibbles 0 and 2 of the halves): k slots (2c, 2c+1) = dims (2o, 2o+4), (2c+8, 2c+9) = (2o+2,
-  // 2o+6); high-nibble MMA: the same + 1.
-  uint32_t qf[NT][NG][KW][4];
-  float qsum[NT][2][NG];  // columns 2c, 2c+1: sum of q over the group, over kUnit
-  int len[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; nt++) {
-    const int col = nt * kCols + gid, n = it.n0 + col;
-    const bool on = col < it.ncols && it.len(n, a.R) > 0;
-    const __half *qrow = a.q + (static_cast<int64_t>(it.s) * a.rows_per_seq + n / a.R) * a.ldq +
-                         (static_cast<int64_t>(it.h) * a.R + n % a.R) * D;
-#pragma unroll
-    for (int g = 0; g < NG; g++) {
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < KW; j++) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (on) v = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
-        const __half *e = reinterpret_cast<const __half *>(&v);
-        q_operands(qf[nt][g][j], v);
-#pragma unroll
-        for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
+    const Walk walk = walks[warp];
+    const int ht = walk.ht, item = walk.s * a.kv.H * a.tiles + ht;
+    const Item it = load_item(a, walk.s, ht, !a.units && first == 0 && lane == 0);
+    // live columns' lengths: rows ascend with the column, so the last live one sees most
+    int lmin = 0, lmax = 0;
+    {
+      const int last = min(it.n0 + it.ncols, it.live * a.R) - 1;
+      if (last >= it.n0) {
+        lmin = it.len(it.n0, a.R);
+        lmax = it.len(last, a.R);
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      sum *= 1.0f / kUnit;
-      qsum[nt][0][g] = __shfl_sync(0xffffffffu, sum, 8 * c);
-      qsum[nt][1][g] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
     }
-#pragma unroll
-    for (int e = 0; e < 2; e++) {
-      const int m = nt * kCols + 2 * c + e;
-      len[nt][e] = m < it.ncols ? it.len(it.n0 + m, a.R) : 0;
+    const int ran = a.units ? walk.run() : 0;
+    const int t_begin = a.units ? walk.b * kBlock : 0;
+    const int t_end = a.units ? min(lmax, t_begin + ran * kBlock) : lmax;
+    const int t_first = t_begin + first * kBlock;
+    const int steps = ok && t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
+    cp.bad = false;
+    if (steps > 0) {
+      cp.look_up(a, it.s, it.h, t_first, step, t_end, lane);
+      cp.issue(0, 0, bar0, lane);
+      if (steps > 1) cp.issue(1, S::STAGE_B, bar0 + 8, lane);
     }
-  }
-  float *const srow = TRACK ? a.scores + static_cast<int64_t>(item) * NC * a.score_ld : nullptr;
-  // this lane's places in a stage: K code rows, group numbers, ldmatrix rows of V codes
-  const uint8_t *const kbase = wbase + gid * RB + c * (G / 8);
-  const __half *const nbase = reinterpret_cast<const __half *>(wbase + 2 * S::CODE_B) + gid * NG;
-  const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
+    const Target target = target_of(a, walk, unit, item, ran, lane == 0);
 
-  Fit fit;
-  float m[NT][2], l[NT][2];
-  float vacc[NT][2][NG];   // sum of p min over this lane's slots
-  float ov[NT][CH][2][4];  // chunk ch, x: dims 32 ch + 4 gid + 2x ([0], [1]: columns 2c, 2c+1) and + 1 ([2], [3])
+    // ---- q of column n0 + 8 nt + gid as the B operand of the score MMAs ----
+    // Word j of group g of lane class c: dims 2o .. 2o+7, o = g*G/2 + c*G/8 + 4j.  Low-nibble MMA
+    // (nibbles 0 and 2 of the halves): k slots (2c, 2c+1) = dims (2o, 2o+4), (2c+8, 2c+9) = (2o+2,
+    // 2o+6); high-nibble MMA: the same + 1.
+    uint32_t qf[NT][NG][KW][4];
+    float qsum[NT][2][NG];  // columns 2c, 2c+1: sum of q over the group, over kUnit
+    int len[NT][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; nt++) {
-    m[nt][0] = m[nt][1] = -INFINITY;
-    l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-    for (int g = 0; g < NG; g++) {
-      vacc[nt][0][g] = vacc[nt][1][g] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < CH; i++)
-#pragma unroll
-      for (int x = 0; x < 2; x++) ov[nt][i][x][0] = ov[nt][i][x][1] = ov[nt][i][x][2] = ov[nt][i][x][3] = 0.f;
-  }
-
-  // one block of 32 slots at t, in stage ST; EDGE: some live column does not see all of them
-  auto block = [&](auto stage, auto edge, int t) {
-    constexpr int OFF = decltype(stage)::value * S::STAGE_B;
-    constexpr bool EDGE = decltype(edge)::value;
-    // ---- scores (over kUnit) of slots t + 16u + gid + 8x, columns 2c + e ----
-    float sc[NT][2][2][2];
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-      const __half *const n0 = nbase + OFF / 2 + 16 * u * NG, *const n1 = n0 + 8 * NG;
-      const Nums<NG> km[2] = {Nums<NG>(n0), Nums<NG>(n1)};
-      const Nums<NG> ks[2] = {Nums<NG>(n0 + kBlock * NG), Nums<NG>(n1 + kBlock * NG)};
+    for (int nt = 0; nt < NT; nt++) {
+      const int col = nt * kCols + gid, n = it.n0 + col;
+      const bool on = col < it.ncols && it.len(n, a.R) > 0;
+      const __half *qrow = a.q + (static_cast<int64_t>(it.s) * a.rows_per_seq + n / a.R) * a.ldq +
+                           (static_cast<int64_t>(it.h) * a.R + n % a.R) * D;
 #pragma unroll
       for (int g = 0; g < NG; g++) {
-        uint32_t k0[KW], k1[KW];
-        load_words<KW>(kbase + OFF + 16 * u * RB + g * (G / 2), k0);
-        load_words<KW>(kbase + OFF + (16 * u + 8) * RB + g * (G / 2), k1);
-        float lo[NT][4], hi[NT][4];  // two chains of MMAs
+        float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < KW; j++) {
-          const Nibbles x0(k0[j]), x1(k1[j]);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (on) v = *reinterpret_cast<const uint4 *>(qrow + g * G + c * (G / 4) + 8 * j);
+          const __half *e = reinterpret_cast<const __half *>(&v);
+          q_operands(qf[nt][g][j], v);
 #pragma unroll
-          for (int nt = 0; nt < NT; nt++) {
-            if (j == 0) {
-              mma_f16_z(lo[nt], x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[nt][g][j][0], qf[nt][g][j][1]);
-              mma_f16_z(hi[nt], x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[nt][g][j][2], qf[nt][g][j][3]);
-            } else {
-              mma_f16(lo[nt], x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[nt][g][j][0], qf[nt][g][j][1]);
-              mma_f16(hi[nt], x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[nt][g][j][2], qf[nt][g][j][3]);
-            }
-          }
+          for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
         }
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-          const float mn = km[x].get(g), sl = ks[x].get(g);
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-              const float v = g == 0 ? mn * qsum[nt][e][g] : fmaf(mn, qsum[nt][e][g], sc[nt][u][x][e]);
-              sc[nt][u][x][e] = fmaf(sl, lo[nt][2 * x + e] + hi[nt][2 * x + e], v);
-            }
-        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        sum *= 1.0f / kUnit;
+        qsum[nt][0][g] = __shfl_sync(0xffffffffu, sum, 8 * c);
+        qsum[nt][1][g] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
       }
-    }
-    if constexpr (EDGE) {
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int u = 0; u < 2; u++)
-#pragma unroll
-          for (int x = 0; x < 2; x++)
-#pragma unroll
-            for (int e = 0; e < 2; e++)
-              if (t + 16 * u + gid + 8 * x >= min(len[nt][e], t_end)) sc[nt][u][x][e] = -INFINITY;
-    }
-    if constexpr (TRACK) {
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int e = 0; e < 2; e++)
-          if (len[nt][e] > 0)
-#pragma unroll
-            for (int u = 0; u < 2; u++)
-#pragma unroll
-              for (int x = 0; x < 2; x++) {
-                const int ts = t + 16 * u + gid + 8 * x;
-                if (!EDGE || ts < len[nt][e]) srow[(nt * kCols + 2 * c + e) * a.score_ld + ts] = sc[nt][u][x][e] * kScore;
-              }
-    }
-    // ---- running maximum: moves only when a score exceeds it by more than kSlack, so that
-    //      p = 2^(s - m) <= 2^kSlack and w = p * scale * fit.f stays inside fp16 ----
-    const __half *const vs0 = nbase + OFF / 2 + 3 * kBlock * NG;  // V scales of slots gid, gid + 8, ..
-    float vmax = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const Nums<NG> v(vs0 + 8 * i * NG);
-#pragma unroll
-      for (int g = 0; g < NG; g++)
-        if (!EDGE || t + 8 * i + gid < t_end) vmax = fmaxf(vmax, fabsf(v.get(g)));
-    }
-    float cmax[NT][2];
-    bool moves = vmax * fit.f > kFits;
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++)
 #pragma unroll
       for (int e = 0; e < 2; e++) {
-        cmax[nt][e] =
-            fmaxf(fmaxf(sc[nt][0][0][e], sc[nt][0][1][e]), fmaxf(sc[nt][1][0][e], sc[nt][1][1][e])) * kScore;
-        moves |= cmax[nt][e] > m[nt][e] + kSlack;
+        const int m = nt * kCols + 2 * c + e;
+        len[nt][e] = m < it.ncols ? it.len(it.n0 + m, a.R) : 0;
       }
-    if (__any_sync(0xffffffffu, moves)) {
+    }
+    float *const srow = TRACK ? a.scores + static_cast<int64_t>(item) * NC * a.score_ld : nullptr;
+    // this lane's places in a stage: K code rows, group numbers, ldmatrix rows of V codes
+    const uint8_t *const kbase = wbase + gid * RB + c * (G / 8);
+    const __half *const nbase = reinterpret_cast<const __half *>(wbase + 2 * S::CODE_B) + gid * NG;
+    const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
+
+    Fit fit;
+    float m[NT][2], l[NT][2];
+    float vacc[NT][2][NG];   // sum of p min over this lane's slots
+    float ov[NT][CH][2][4];  // chunk ch, x: dims 32 ch + 4 gid + 2x ([0], [1]: columns 2c, 2c+1) and + 1 ([2], [3])
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
-      if (vmax * fit.f > kFits) fit.fall(vmax);
+    for (int nt = 0; nt < NT; nt++) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < NT; nt++) {
-        float al[2];
+      for (int g = 0; g < NG; g++) {
+        vacc[nt][0][g] = vacc[nt][1][g] = 0.f;
+      }
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-          float mn = cmax[nt][e];
+      for (int i = 0; i < CH; i++)
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-          mn = fmaxf(m[nt][e], mn);
-          al[e] = mn == -INFINITY ? 1.f : fast_exp2(m[nt][e] - mn);
-          m[nt][e] = mn;
-          l[nt][e] *= al[e];
-        }
+        for (int x = 0; x < 2; x++) ov[nt][i][x][0] = ov[nt][i][x][1] = ov[nt][i][x][2] = ov[nt][i][x][3] = 0.f;
+    }
+
+    // one block of 32 slots at t, in stage ST; EDGE: some live column does not see all of them
+    auto block = [&](auto stage, auto edge, int t) {
+      constexpr int OFF = decltype(stage)::value * S::STAGE_B;
+      constexpr bool EDGE = decltype(edge)::value;
+      // ---- scores (over kUnit) of slots t + 16u + gid + 8x, columns 2c + e ----
+      float sc[NT][2][2][2];
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        const __half *const n0 = nbase + OFF / 2 + 16 * u * NG, *const n1 = n0 + 8 * NG;
+        const Nums<NG> km[2] = {Nums<NG>(n0), Nums<NG>(n1)};
+        const Nums<NG> ks[2] = {Nums<NG>(n0 + kBlock * NG), Nums<NG>(n1 + kBlock * NG)};
 #pragma unroll
         for (int g = 0; g < NG; g++) {
-          vacc[nt][0][g] *= al[0];
-          vacc[nt][1][g] *= al[1];
-        }
+          uint32_t k0[KW], k1[KW];
+          load_words<KW>(kbase + OFF + 16 * u * RB + g * (G / 2), k0);
+          load_words<KW>(kbase + OFF + (16 * u + 8) * RB + g * (G / 2), k1);
+          float lo[NT][4], hi[NT][4];  // two chains of MMAs
 #pragma unroll
-        for (int ch = 0; ch < CH; ch++)
+          for (int j = 0; j < KW; j++) {
+            const Nibbles x0(k0[j]), x1(k1[j]);
 #pragma unroll
-          for (int x = 0; x < 2; x++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) ov[nt][ch][x][i] *= al[i & 1];
-      }
-    }
-    // ---- p and the sums ----
-    uint32_t b[2][NT][NG][2], bl[2][NT][NG][2];  // w rounded, and the rest
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-      float p[NT][2][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int x = 0; x < 2; x++)
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            p[nt][x][e] = EDGE && sc[nt][u][x][e] == -INFINITY ? 0.f : fast_exp2(fmaf(sc[nt][u][x][e], kScore, -m[nt][e]));
-            l[nt][e] += p[nt][x][e];
-          }
-      const __half *const n0 = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG, *const n1 = n0 + 8 * NG;
-      const Nums<NG> vm[2] = {Nums<NG>(n0), Nums<NG>(n1)};
-      const Nums<NG> vsc[2] = {Nums<NG>(n0 + kBlock * NG), Nums<NG>(n1 + kBlock * NG)};
-#pragma unroll
-      for (int g = 0; g < NG; g++)
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-          const float vs = vsc[x].get(g) * fit.f, vb = vm[x].get(g);
-#pragma unroll
-          for (int nt = 0; nt < NT; nt++) {
-            float w0 = p[nt][x][0] * vs, w1 = p[nt][x][1] * vs, o0 = p[nt][x][0] * vb, o1 = p[nt][x][1] * vb;
-            if constexpr (EDGE) {  // masked slots may hold anything
-              if (p[nt][x][0] == 0.f) w0 = o0 = 0.f;
-              if (p[nt][x][1] == 0.f) w1 = o1 = 0.f;
+            for (int nt = 0; nt < NT; nt++) {
+              if (j == 0) {
+                mma_f16_z(lo[nt], x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[nt][g][j][0], qf[nt][g][j][1]);
+                mma_f16_z(hi[nt], x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[nt][g][j][2], qf[nt][g][j][3]);
+              } else {
+                mma_f16(lo[nt], x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[nt][g][j][0], qf[nt][g][j][1]);
+                mma_f16(hi[nt], x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[nt][g][j][2], qf[nt][g][j][3]);
+              }
             }
-            vacc[nt][0][g] += o0;
-            vacc[nt][1][g] += o1;
-            const uint32_t w = pack_h2(w0, w1);
-            const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-            b[u][nt][g][x] = transpose_8x8(w);
-            bl[u][nt][g][x] = transpose_8x8(pack_h2(w0 - r.x, w1 - r.y));
+          }
+#pragma unroll
+          for (int x = 0; x < 2; x++) {
+            const float mn = km[x].get(g), sl = ks[x].get(g);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+              for (int e = 0; e < 2; e++) {
+                const float v = g == 0 ? mn * qsum[nt][e][g] : fmaf(mn, qsum[nt][e][g], sc[nt][u][x][e]);
+                sc[nt][u][x][e] = fmaf(sl, lo[nt][2 * x + e] + hi[nt][2 * x + e], v);
+              }
           }
         }
-    }
-    // ---- the output product: a block's MMAs start from zero and are added in fp32 registers (the
-    //      tensor core's own additions truncate, and what they lose grows with the sum) ----
+      }
+      if constexpr (EDGE) {
 #pragma unroll
-    for (int ch = 0; ch < CH; ch += 2) {
-      uint32_t r[2][4];  // [u]: slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
-      ldmatrix_x4_trans(r[0], vbase + OFF + ch * 16);
-      ldmatrix_x4_trans(r[1], vbase + OFF + 16 * RB + ch * 16);
-      const int g = ch * 32 / G;
-#pragma unroll
-      for (int y = 0; y < 2; y++)
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-          uint32_t lo[2][2], hi[2][2];  // dims 2x (rows gid) and 2x + 1 (rows gid + 8) of the four
+        for (int nt = 0; nt < NT; nt++)
 #pragma unroll
           for (int u = 0; u < 2; u++)
 #pragma unroll
-            for (int z = 0; z < 2; z++) {
-              const uint32_t w = x ? r[u][2 * y + z] >> 8 : r[u][2 * y + z];
-              lo[u][z] = nibble0(w);
-              hi[u][z] = nibble1(w);
+            for (int x = 0; x < 2; x++)
+#pragma unroll
+              for (int e = 0; e < 2; e++)
+                if (t + 16 * u + gid + 8 * x >= min(len[nt][e], t_end)) sc[nt][u][x][e] = -INFINITY;
+      }
+      if constexpr (TRACK) {
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int e = 0; e < 2; e++)
+            if (len[nt][e] > 0)
+#pragma unroll
+              for (int u = 0; u < 2; u++)
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
+                  const int ts = t + 16 * u + gid + 8 * x;
+                  if (!EDGE || ts < len[nt][e])
+                    srow[(nt * kCols + 2 * c + e) * a.score_ld + ts] = sc[nt][u][x][e] * kScore;
+                }
+      }
+      // ---- running maximum: moves only when a score exceeds it by more than kSlack, so that
+      //      p = 2^(s - m) <= 2^kSlack and w = p * scale * fit.f stays inside fp16 ----
+      const __half *const vs0 = nbase + OFF / 2 + 3 * kBlock * NG;  // V scales of slots gid, gid + 8, ..
+      float vmax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const Nums<NG> v(vs0 + 8 * i * NG);
+#pragma unroll
+        for (int g = 0; g < NG; g++)
+          if (!EDGE || t + 8 * i + gid < t_end) vmax = fmaxf(vmax, fabsf(v.get(g)));
+      }
+      float cmax[NT][2];
+      bool moves = vmax * fit.f > kFits;
+#pragma unroll
+      for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          cmax[nt][e] =
+              fmaxf(fmaxf(sc[nt][0][0][e], sc[nt][0][1][e]), fmaxf(sc[nt][1][0][e], sc[nt][1][1][e])) * kScore;
+          moves |= cmax[nt][e] > m[nt][e] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, o));
+        if (vmax * fit.f > kFits) fit.fall(vmax);
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+          float al[2];
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            float mn = cmax[nt][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+            mn = fmaxf(m[nt][e], mn);
+            al[e] = mn == -INFINITY ? 1.f : fast_exp2(m[nt][e] - mn);
+            m[nt][e] = mn;
+            l[nt][e] *= al[e];
+          }
+#pragma unroll
+          for (int g = 0; g < NG; g++) {
+            vacc[nt][0][g] *= al[0];
+            vacc[nt][1][g] *= al[1];
+          }
+#pragma unroll
+          for (int ch = 0; ch < CH; ch++)
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+#pragma unroll
+              for (int i = 0; i < 4; i++) ov[nt][ch][x][i] *= al[i & 1];
+        }
+      }
+      // ---- p and the sums ----
+      uint32_t b[2][NT][NG][2], bl[2][NT][NG][2];  // w rounded, and the rest
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        float p[NT][2][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+          for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              const float v = sc[nt][u][x][e];
+              p[nt][x][e] = EDGE && v == -INFINITY ? 0.f : fast_exp2(fmaf(v, kScore, -m[nt][e]));
+              l[nt][e] += p[nt][x][e];
             }
+        const __half *const n0 = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG, *const n1 = n0 + 8 * NG;
+        const Nums<NG> vm[2] = {Nums<NG>(n0), Nums<NG>(n1)};
+        const Nums<NG> vsc[2] = {Nums<NG>(n0 + kBlock * NG), Nums<NG>(n1 + kBlock * NG)};
 #pragma unroll
-          for (int nt = 0; nt < NT; nt++) {
-            float d[4];
-            mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][nt][g][0], b[0][nt][g][1]);
-            mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], b[1][nt][g][0], b[1][nt][g][1]);
-            mma_f16(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], bl[0][nt][g][0], bl[0][nt][g][1]);
-            mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], bl[1][nt][g][0], bl[1][nt][g][1]);
-            float(&o)[4] = ov[nt][ch + y][x];
+        for (int g = 0; g < NG; g++)
 #pragma unroll
-            for (int i = 0; i < 4; i++) o[i] = fmaf(d[i], fit.inv, o[i]);
+          for (int x = 0; x < 2; x++) {
+            const float vs = vsc[x].get(g) * fit.f, vb = vm[x].get(g);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+              float w0 = p[nt][x][0] * vs, w1 = p[nt][x][1] * vs, o0 = p[nt][x][0] * vb, o1 = p[nt][x][1] * vb;
+              if constexpr (EDGE) {  // masked slots may hold anything
+                if (p[nt][x][0] == 0.f) w0 = o0 = 0.f;
+                if (p[nt][x][1] == 0.f) w1 = o1 = 0.f;
+              }
+              vacc[nt][0][g] += o0;
+              vacc[nt][1][g] += o1;
+              const uint32_t w = pack_h2(w0, w1);
+              const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+              b[u][nt][g][x] = transpose_8x8(w);
+              bl[u][nt][g][x] = transpose_8x8(pack_h2(w0 - r.x, w1 - r.y));
+            }
+          }
+      }
+      // ---- the output product: a block's MMAs start from zero and are added in fp32 registers (the
+      //      tensor core's own additions truncate, and what they lose grows with the sum) ----
+#pragma unroll
+      for (int ch = 0; ch < CH; ch += 2) {
+        uint32_t r[2][4];  // [u]: slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
+        ldmatrix_x4_trans(r[0], vbase + OFF + ch * 16);
+        ldmatrix_x4_trans(r[1], vbase + OFF + 16 * RB + ch * 16);
+        const int g = ch * 32 / G;
+#pragma unroll
+        for (int y = 0; y < 2; y++)
+#pragma unroll
+          for (int x = 0; x < 2; x++) {
+            uint32_t lo[2][2], hi[2][2];  // dims 2x (rows gid) and 2x + 1 (rows gid + 8) of the four
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+              for (int z = 0; z < 2; z++) {
+                const uint32_t w = x ? r[u][2 * y + z] >> 8 : r[u][2 * y + z];
+                lo[u][z] = nibble0(w);
+                hi[u][z] = nibble1(w);
+              }
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+              float d[4];
+              mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][nt][g][0], b[0][nt][g][1]);
+              mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], b[1][nt][g][0], b[1][nt][g][1]);
+              mma_f16(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], bl[0][nt][g][0], bl[0][nt][g][1]);
+              mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], bl[1][nt][g][0], bl[1][nt][g][1]);
+              float(&o)[4] = ov[nt][ch + y][x];
+#pragma unroll
+              for (int i = 0; i < 4; i++) o[i] = fmaf(d[i], fit.inv, o[i]);
+            }
+          }
+      }
+    };
+
+    int t = t_first;
+    // one step: wait for stage ST, its block, and the copy of the block two steps on
+    auto run = [&](auto stage, int k) -> bool {
+      constexpr int ST = decltype(stage)::value;
+      if (!mbar_wait_bounded(bar0 + 8 * ST, phase >> ST & 1, nullptr, a.kv.err)) {
+        // gave up: the copy in flight lands (or times out) before the stages are written again
+        if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), phase >> (ST ^ 1) & 1, nullptr, a.kv.err);
+        ok = false;
+        return false;
+      }
+      phase ^= 1u << ST;
+      if (t + kBlock > min(lmin, t_end)) block(stage, std::true_type{}, t);
+      else block(stage, std::false_type{}, t);
+      if (k + 2 < steps) {
+        fence_proxy_async_smem();  // every lane has used the stage before the copy that refills it
+        __syncwarp();
+        if (((k + 2) & 31) == 0) cp.look_up(a, it.s, it.h, t + 2 * step, step, t_end, lane);
+        cp.issue((k + 2) & 31, ST * S::STAGE_B, bar0 + 8 * ST, lane);
+      }
+      t += step;
+      return true;
+    };
+    for (int k = 0; k < steps; k += 2) {
+      if (!run(std::integral_constant<int, 0>{}, k)) break;
+      if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1)) break;
+    }
+    const bool any_bad = __any_sync(0xffffffffu, cp.bad);
+    if (any_bad && lane == 0) {
+      atomicOr(a.kv.err, FG_DEVERR_RANGE);
+      if (a.shared_unit) bad_page = 1;
+    }
+
+    // ---- this warp's columns: totals, and outputs ----
+    float *const wo = reinterpret_cast<float *>(wbase);  // [NC][D], in the (drained) stages, for the join below
+    const bool good_warp = ok && !any_bad;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
+#pragma unroll
+        for (int g = 0; g < NG; g++)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) vacc[nt][e][g] += __shfl_xor_sync(0xffffffffu, vacc[nt][e][g], o);
+        const int n = nt * kCols + 2 * c + e;
+        if (gid == 0) {
+          red_m[warp][n] = m[nt][e];
+          red_l[warp][n] = l[nt][e];
+        }
+        if (n >= it.ncols) continue;
+        const int cn = it.n0 + n;
+        const float inv = len[nt][e] > 0 && good_warp ? 1.0f / l[nt][e] : 0.f;
+        const int64_t pi = target.index * NC + n;
+        if (!a.shared_unit && !target.whole && gid == 0) a.ml[pi] = make_float2(m[nt][e], good_warp ? l[nt][e] : -1.f);
+        __half *const orow = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
+                             (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + 4 * gid;
+#pragma unroll
+        for (int ch = 0; ch < CH; ch++) {
+          const float base = vacc[nt][e][ch * 32 / G];
+          float v[4];
+#pragma unroll
+          for (int x = 0; x < 2; x++) {
+            v[2 * x] = ov[nt][ch][x][e] * kUnit + base;
+            v[2 * x + 1] = ov[nt][ch][x][2 + e] * kUnit + base;
+          }
+          if (a.shared_unit) {
+            *reinterpret_cast<float4 *>(wo + n * D + ch * 32 + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
+          } else if (!target.whole) {
+            *reinterpret_cast<float4 *>(a.po + pi * D + ch * 32 + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+            uint2 r = make_uint2(0u, 0u);  // (a row that sees nothing, or a bad page: zero, whatever v is)
+            if (inv != 0.f) r = make_uint2(pack_h2(v[0] * inv, v[1] * inv), pack_h2(v[2] * inv, v[3] * inv));
+            *reinterpret_cast<uint2 *>(orow + ch * 32) = r;
           }
         }
-    }
-  };
-
-  int t = t_first;
-  // one step: wait for stage ST, its block, and the copy of the block two steps on
-  auto run = [&](auto stage, int k) -> bool {
-    constexpr int ST = decltype(stage)::value;
-    if (!mbar_wait_bounded(bar0 + 8 * ST, phase >> ST & 1, nullptr, a.kv.err)) {
-      // gave up: the copy in flight lands (or times out) before the stages are written again
-      if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), phase >> (ST ^ 1) & 1, nullptr, a.kv.err);
-      ok = false;
-      return false;
-    }
-    phase ^= 1u << ST;
-    if (t + kBlock > min(lmin, t_end)) block(stage, std::true_type{}, t);
-    else block(stage, std::false_type{}, t);
-    if (k + 2 < steps) {
-      fence_proxy_async_smem();  // every lane has used the stage before the copy that refills it
-      __syncwarp();
-      if (((k + 2) & 31) == 0) cp.look_up(a, it.s, it.h, t + 2 * step, step, t_end, lane);
-      cp.issue((k + 2) & 31, ST * S::STAGE_B, bar0 + 8 * ST, lane);
-    }
-    t += step;
-    return true;
-  };
-  for (int k = 0; k < steps; k += 2) {
-    if (!run(std::integral_constant<int, 0>{}, k)) break;
-    if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1)) break;
-  }
-  const bool any_bad = __any_sync(0xffffffffu, cp.bad);
-  if (any_bad && lane == 0) {
-    atomicOr(a.kv.err, FG_DEVERR_RANGE);
-    if (a.shared_unit) bad_page = 1;
-  }
-
-  // ---- this warp's columns: totals, and outputs ----
-  float *const wo = reinterpret_cast<float *>(wbase);  // [NC][D], in the (drained) stages, for the join below
-  const bool good_warp = ok && !any_bad;
-#pragma unroll
-  for (int nt = 0; nt < NT; nt++) {
-#pragma unroll
-    for (int e = 0; e < 2; e++) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], o);
-#pragma unroll
-      for (int g = 0; g < NG; g++)
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) vacc[nt][e][g] += __shfl_xor_sync(0xffffffffu, vacc[nt][e][g], o);
-      const int n = nt * kCols + 2 * c + e;
-      if (gid == 0) {
-        red_m[warp][n] = m[nt][e];
-        red_l[warp][n] = l[nt][e];
-      }
-      if (n >= it.ncols) continue;
-      const int cn = it.n0 + n;
-      const float inv = len[nt][e] > 0 && good_warp ? 1.0f / l[nt][e] : 0.f;
-      const int64_t pi = target.index * NC + n;
-      if (!a.shared_unit && !target.whole && gid == 0) a.ml[pi] = make_float2(m[nt][e], good_warp ? l[nt][e] : -1.f);
-      __half *const orow = a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
-                           (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + 4 * gid;
-#pragma unroll
-      for (int ch = 0; ch < CH; ch++) {
-        const float base = vacc[nt][e][ch * 32 / G];
-        float v[4];
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-          v[2 * x] = ov[nt][ch][x][e] * kUnit + base;
-          v[2 * x + 1] = ov[nt][ch][x][2 + e] * kUnit + base;
-        }
-        if (a.shared_unit) {
-          *reinterpret_cast<float4 *>(wo + n * D + ch * 32 + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
-        } else if (!target.whole) {
-          *reinterpret_cast<float4 *>(a.po + pi * D + ch * 32 + 4 * gid) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-          uint2 r = make_uint2(0u, 0u);  // (a row that sees nothing, or a bad page: zero, whatever v is)
-          if (inv != 0.f) r = make_uint2(pack_h2(v[0] * inv, v[1] * inv), pack_h2(v[2] * inv, v[3] * inv));
-          *reinterpret_cast<uint2 *>(orow + ch * 32) = r;
-        }
       }
     }
-  }
-  bool good = good_warp;
-  const int w0 = a.shared_unit ? 0 : warp, w1 = a.shared_unit ? kWarps : warp + 1;
-  const int me = a.shared_unit ? tid : lane, all = a.shared_unit ? kWarps * 32 : 32;
-  if (a.shared_unit) {  // the CTA's warps joined
-    good = __syncthreads_and(ok) && !bad_page;
-    for (int i = tid; i < it.ncols * (D / 4); i += kWarps * 32) {
-      const int n = i / (D / 4), d = 4 * (i % (D / 4));
-      float M = -INFINITY, den = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; w++) M = fmaxf(M, red_m[w][n]);
-#pragma unroll
-      for (int w = 0; w < kWarps; w++) {
-        const float f = red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M);
-        const float4 v = *reinterpret_cast<const float4 *>(smem + w * S::WARP_B + (n * D + d) * 4);
-        den += f * red_l[w][n];
-        if (f != 0.f) o = make_float4(o.x + f * v.x, o.y + f * v.y, o.z + f * v.z, o.w + f * v.w);
-      }
-      const int cn = it.n0 + n;
-      const float inv = 1.0f / den;
-      uint2 r = make_uint2(0u, 0u);
-      if (it.len(cn, a.R) > 0 && good) r = make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
-      *reinterpret_cast<uint2 *>(a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
-                                 (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + d) = r;
-    }
-  } else {
-    __syncwarp();
-  }
-  if (TRACK && target.whole && good) {  // the unit saw whole rows: its slots' weights
-    for (int i = 4 * me; i < lmax; i += 4 * all) {
-      float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int n = 0; n < it.ncols; n++) {
-        const int end = it.len(it.n0 + n, a.R);
+    bool good = good_warp;
+    const int w0 = a.shared_unit ? 0 : warp, w1 = a.shared_unit ? kWarps : warp + 1;
+    const int me = a.shared_unit ? tid : lane, all = a.shared_unit ? kWarps * 32 : 32;
+    if (a.shared_unit) {  // the CTA's warps joined
+      good = __syncthreads_and(ok) && !bad_page;
+      for (int i = tid; i < it.ncols * (D / 4); i += kWarps * 32) {
+        const int n = i / (D / 4), d = 4 * (i % (D / 4));
         float M = -INFINITY, den = 0.f;
-        for (int w = w0; w < w1; w++) M = fmaxf(M, red_m[w][n]);
-        for (int w = w0; w < w1; w++) den += red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M) * red_l[w][n];
-        grow_by(&add, srow + n * a.score_ld, i, end, M, 1.0f / den);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) M = fmaxf(M, red_m[w][n]);
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+          const float f = red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M);
+          const float4 v = *reinterpret_cast<const float4 *>(smem + w * S::WARP_B + (n * D + d) * 4);
+          den += f * red_l[w][n];
+          if (f != 0.f) o = make_float4(o.x + f * v.x, o.y + f * v.y, o.z + f * v.z, o.w + f * v.w);
+        }
+        const int cn = it.n0 + n;
+        const float inv = 1.0f / den;
+        uint2 r = make_uint2(0u, 0u);
+        if (it.len(cn, a.R) > 0 && good) r = make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2 *>(a.out + (static_cast<int64_t>(it.s) * a.rows_per_seq + cn / a.R) * a.ldo +
+                                   (static_cast<int64_t>(it.h) * a.R + cn % a.R) * D + d) = r;
       }
-      grow4(a, it.s, it.h, i, lmax, add);
+    } else {
+      __syncwarp();
     }
-  }
-  if (!a.units || !advance(a, &walks[warp], lane)) return;
+    if (TRACK && target.whole && good) {  // the unit saw whole rows: its slots' weights
+      for (int i = 4 * me; i < lmax; i += 4 * all) {
+        float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int n = 0; n < it.ncols; n++) {
+          const int end = it.len(it.n0 + n, a.R);
+          float M = -INFINITY, den = 0.f;
+          for (int w = w0; w < w1; w++) M = fmaxf(M, red_m[w][n]);
+          for (int w = w0; w < w1; w++) den += red_m[w][n] == -INFINITY ? 0.f : exp2f(red_m[w][n] - M) * red_l[w][n];
+          grow_by(&add, srow + n * a.score_ld, i, end, M, 1.0f / den);
+        }
+        grow4(a, it.s, it.h, i, lmax, add);
+      }
+    }
+    if (!a.units || !advance(a, &walks[warp], lane)) return;
   }
 }
 
@@ -1017,306 +1019,306 @@ __global__ void __launch_bounds__(kWarps * 32, One<D, G>::kCtas) paged_attn_one_
   uint32_t phase = 0;  // bit i: the parity of stage i's next phase
 
   while (true) {  // segments
-  const Walk walk = walks[warp];
-  const int s = walk.s, h = walk.ht, item = s * a.kv.H + h;
-  const int len = load_item(a, s, h, !a.units && first == 0 && lane == 0).len(0, 1);
-  const int ran = a.units ? walk.run() : 0;
-  const int t_begin = a.units ? walk.b * kBlock : 0;
-  const int t_end = a.units ? min(len, t_begin + ran * kBlock) : len;
-  const int t_first = t_begin + first * kBlock;
-  const int steps = ok && t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
-  cp.bad = false;
-  if (steps > 0) {
-    cp.look_up(a, s, h, t_first, step, t_end, lane);
-    cp.issue(0, 0, bar0, lane);
-    if (steps > 1) cp.issue(1, S::STAGE_B, bar0 + 8, lane);
-  }
-  const Target target = target_of(a, walk, unit, item, ran, lane == 0);
-
-  // ---- q as the B operand; word j of lane class c: dims 2o .. 2o+7 ----
-  const __half *qrow = a.q + static_cast<int64_t>(s) * a.ldq + static_cast<int64_t>(h) * D;
-  uint32_t qf[KW][4];
-  float ql;  // sum of q over this lane's group, over kUnit
-  const int g = NG == 2 ? c & 1 : 0;
-  {
-    float part[NG];
-#pragma unroll
-    for (int i = 0; i < NG; i++) part[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < KW; j++) {
-      const int o = D == 64 ? 8 * c + 4 * j : 64 * (j >> 2) + 16 * c + 4 * (j & 3);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (len > 0) v = *reinterpret_cast<const uint4 *>(qrow + 2 * o);
-      const __half *e = reinterpret_cast<const __half *>(&v);
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
-#pragma unroll
-      for (int i = 0; i < NG; i++) part[i] += o / (G / 2) == i ? sum : 0.f;
-      const bool on = !(gid & 1) && (NG == 1 || o / (G / 2) == ((gid >> 1) & 1));
-      if (!on) v = make_uint4(0, 0, 0, 0);
-      q_operands(qf[j], v);
+    const Walk walk = walks[warp];
+    const int s = walk.s, h = walk.ht, item = s * a.kv.H + h;
+    const int len = load_item(a, s, h, !a.units && first == 0 && lane == 0).len(0, 1);
+    const int ran = a.units ? walk.run() : 0;
+    const int t_begin = a.units ? walk.b * kBlock : 0;
+    const int t_end = a.units ? min(len, t_begin + ran * kBlock) : len;
+    const int t_first = t_begin + first * kBlock;
+    const int steps = ok && t_end > t_first ? (t_end - t_first + step - 1) / step : 0;
+    cp.bad = false;
+    if (steps > 0) {
+      cp.look_up(a, s, h, t_first, step, t_end, lane);
+      cp.issue(0, 0, bar0, lane);
+      if (steps > 1) cp.issue(1, S::STAGE_B, bar0 + 8, lane);
     }
-#pragma unroll
-    for (int i = 0; i < NG; i++) {
-      part[i] += __shfl_xor_sync(0xffffffffu, part[i], 1);
-      part[i] += __shfl_xor_sync(0xffffffffu, part[i], 2);
-    }
-    ql = (NG == 2 && g ? part[NG - 1] : part[0]) * (1.0f / kUnit);
-  }
-  const bool upper = c & 2;  // this lane's slot is gid + 8 of the 16
-  const int tq = gid + (upper ? 8 : 0);
-  float *const srow = TRACK ? a.scores + static_cast<int64_t>(item) * a.score_ld : nullptr;
-  // this lane's places in a stage: K code rows, group numbers, ldmatrix rows of V codes
-  const uint8_t *const kbase = wbase + gid * RB + (D == 64 ? 8 : 16) * c;
-  const __half *const nbase = reinterpret_cast<const __half *>(wbase + 2 * S::CODE_B) + tq * NG + g;
-  const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
+    const Target target = target_of(a, walk, unit, item, ran, lane == 0);
 
-  Fit fit;
-  float m = -INFINITY, l = 0.f, vacc = 0.f;
-  float ov[CH][2][2];  // chunk ch, x: dims 32 ch + 4 gid + 2x and + 1
+    // ---- q as the B operand; word j of lane class c: dims 2o .. 2o+7 ----
+    const __half *qrow = a.q + static_cast<int64_t>(s) * a.ldq + static_cast<int64_t>(h) * D;
+    uint32_t qf[KW][4];
+    float ql;  // sum of q over this lane's group, over kUnit
+    const int g = NG == 2 ? c & 1 : 0;
+    {
+      float part[NG];
 #pragma unroll
-  for (int i = 0; i < CH; i++)
-#pragma unroll
-    for (int x = 0; x < 2; x++) ov[i][x][0] = ov[i][x][1] = 0.f;
-
-  // one block of 32 slots at t, in stage ST; EDGE: some of them are not seen
-  auto block = [&](auto stage, auto edge, int t) {
-    constexpr int OFF = decltype(stage)::value * S::STAGE_B;
-    constexpr bool EDGE = decltype(edge)::value;
-    float sc[2];
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-      uint32_t k0[KW], k1[KW];
-#pragma unroll
-      for (int j = 0; j < KW; j += (D == 64 ? 2 : 4)) {
-        const uint8_t *p = kbase + OFF + 16 * u * RB + (D == 64 ? 0 : 16 * j);
-        if constexpr (D == 64) {
-          const uint2 x = *reinterpret_cast<const uint2 *>(p), y = *reinterpret_cast<const uint2 *>(p + 8 * RB);
-          k0[j] = x.x, k0[j + 1] = x.y, k1[j] = y.x, k1[j + 1] = y.y;
-        } else {
-          const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + 8 * RB);
-          k0[j] = x.x, k0[j + 1] = x.y, k0[j + 2] = x.z, k0[j + 3] = x.w;
-          k1[j] = y.x, k1[j + 1] = y.y, k1[j + 2] = y.z, k1[j + 3] = y.w;
-        }
-      }
-      float lo[4], hi[4];  // two chains of MMAs
+      for (int i = 0; i < NG; i++) part[i] = 0.f;
 #pragma unroll
       for (int j = 0; j < KW; j++) {
-        const Nibbles x0(k0[j]), x1(k1[j]);
-        if (j == 0) {
-          mma_f16_z(lo, x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[j][0], qf[j][1]);
-          mma_f16_z(hi, x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[j][2], qf[j][3]);
-        } else {
-          mma_f16(lo, x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[j][0], qf[j][1]);
-          mma_f16(hi, x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[j][2], qf[j][3]);
-        }
-      }
-      const __half *n = nbase + OFF / 2 + 16 * u * NG;
-      float part = fmaf(__half2float(n[kBlock * NG]), upper ? lo[2] + hi[2] : lo[0] + hi[0], __half2float(n[0]) * ql);
-      if constexpr (NG == 2) part += __shfl_xor_sync(0xffffffffu, part, 1);
-      sc[u] = part;
-    }
-    if constexpr (EDGE) {
+        const int o = D == 64 ? 8 * c + 4 * j : 64 * (j >> 2) + 16 * c + 4 * (j & 3);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (len > 0) v = *reinterpret_cast<const uint4 *>(qrow + 2 * o);
+        const __half *e = reinterpret_cast<const __half *>(&v);
+        float sum = 0.f;
 #pragma unroll
-      for (int u = 0; u < 2; u++)
-        if (t + 16 * u + tq >= t_end) sc[u] = -INFINITY;
+        for (int i = 0; i < 8; i++) sum += __half2float(e[i]);
+#pragma unroll
+        for (int i = 0; i < NG; i++) part[i] += o / (G / 2) == i ? sum : 0.f;
+        const bool on = !(gid & 1) && (NG == 1 || o / (G / 2) == ((gid >> 1) & 1));
+        if (!on) v = make_uint4(0, 0, 0, 0);
+        q_operands(qf[j], v);
+      }
+#pragma unroll
+      for (int i = 0; i < NG; i++) {
+        part[i] += __shfl_xor_sync(0xffffffffu, part[i], 1);
+        part[i] += __shfl_xor_sync(0xffffffffu, part[i], 2);
+      }
+      ql = (NG == 2 && g ? part[NG - 1] : part[0]) * (1.0f / kUnit);
     }
-    if constexpr (TRACK) {
-      if (!(c & 1))
+    const bool upper = c & 2;  // this lane's slot is gid + 8 of the 16
+    const int tq = gid + (upper ? 8 : 0);
+    float *const srow = TRACK ? a.scores + static_cast<int64_t>(item) * a.score_ld : nullptr;
+    // this lane's places in a stage: K code rows, group numbers, ldmatrix rows of V codes
+    const uint8_t *const kbase = wbase + gid * RB + (D == 64 ? 8 : 16) * c;
+    const __half *const nbase = reinterpret_cast<const __half *>(wbase + 2 * S::CODE_B) + tq * NG + g;
+    const uint32_t vbase = smem_u32(wbase) + S::CODE_B + ((lane >> 3 & 1) * 8 + (lane & 7)) * RB + (lane >> 4) * 16;
+
+    Fit fit;
+    float m = -INFINITY, l = 0.f, vacc = 0.f;
+    float ov[CH][2][2];  // chunk ch, x: dims 32 ch + 4 gid + 2x and + 1
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+#pragma unroll
+      for (int x = 0; x < 2; x++) ov[i][x][0] = ov[i][x][1] = 0.f;
+
+    // one block of 32 slots at t, in stage ST; EDGE: some of them are not seen
+    auto block = [&](auto stage, auto edge, int t) {
+      constexpr int OFF = decltype(stage)::value * S::STAGE_B;
+      constexpr bool EDGE = decltype(edge)::value;
+      float sc[2];
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        uint32_t k0[KW], k1[KW];
+#pragma unroll
+        for (int j = 0; j < KW; j += (D == 64 ? 2 : 4)) {
+          const uint8_t *p = kbase + OFF + 16 * u * RB + (D == 64 ? 0 : 16 * j);
+          if constexpr (D == 64) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p), y = *reinterpret_cast<const uint2 *>(p + 8 * RB);
+            k0[j] = x.x, k0[j + 1] = x.y, k1[j] = y.x, k1[j + 1] = y.y;
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + 8 * RB);
+            k0[j] = x.x, k0[j + 1] = x.y, k0[j + 2] = x.z, k0[j + 3] = x.w;
+            k1[j] = y.x, k1[j + 1] = y.y, k1[j + 2] = y.z, k1[j + 3] = y.w;
+          }
+        }
+        float lo[4], hi[4];  // two chains of MMAs
+#pragma unroll
+        for (int j = 0; j < KW; j++) {
+          const Nibbles x0(k0[j]), x1(k1[j]);
+          if (j == 0) {
+            mma_f16_z(lo, x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[j][0], qf[j][1]);
+            mma_f16_z(hi, x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[j][2], qf[j][3]);
+          } else {
+            mma_f16(lo, x0.n[0], x1.n[0], x0.n[2], x1.n[2], qf[j][0], qf[j][1]);
+            mma_f16(hi, x0.n[1], x1.n[1], x0.n[3], x1.n[3], qf[j][2], qf[j][3]);
+          }
+        }
+        const __half *n = nbase + OFF / 2 + 16 * u * NG;
+        float part = fmaf(__half2float(n[kBlock * NG]), upper ? lo[2] + hi[2] : lo[0] + hi[0], __half2float(n[0]) * ql);
+        if constexpr (NG == 2) part += __shfl_xor_sync(0xffffffffu, part, 1);
+        sc[u] = part;
+      }
+      if constexpr (EDGE) {
 #pragma unroll
         for (int u = 0; u < 2; u++)
-          if (!EDGE || t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u] * kScore;
-    }
-    float cmax = fmaxf(sc[0], sc[1]) * kScore;  // scores are held over kUnit
-    float vs[2];
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-      vs[u] = __half2float(nbase[OFF / 2 + (3 * kBlock + 16 * u) * NG]);
-      if (EDGE && t + 16 * u + tq >= t_end) vs[u] = 0.f;  // masked slots may hold anything
-    }
-    const float vmax = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
-    if (__any_sync(0xffffffffu, cmax > m + kSlack || vmax * fit.f > kFits)) {  // the running maximum moves, or F falls
-      float v = vmax;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-      if (v * fit.f > kFits) fit.fall(v);
-#pragma unroll
-      for (int o = 2; o < 32; o <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
-      cmax = fmaxf(m, cmax);
-      const float al = cmax == -INFINITY ? 1.f : fast_exp2(m - cmax);
-      m = cmax;
-      l *= al;
-      vacc *= al;
-#pragma unroll
-      for (int i = 0; i < CH; i++)
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-          ov[i][x][0] *= al;
-          ov[i][x][1] *= al;
-        }
-    }
-    uint32_t b[2][2];
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-      const __half *n = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG;
-      const float p = fast_exp2(fmaf(sc[u], kScore, -m));
-      float w = p * (vs[u] * fit.f), pm = p * __half2float(n[0]);
-      if (EDGE && t + 16 * u + tq >= t_end) w = pm = 0.f;  // (their p is 0)
-      l += p;
-      vacc += pm;
-      // w rounded, and the rest, in columns 2c and 2c+1 of the slot's row
-      uint32_t wp = pack_h2(w, w - __half2float(__float2half_rn(w)));
-      if (NG == 1 && (c & 1)) wp = 0u;
-      const uint32_t wt = transpose_8x8(wp);
-      b[u][0] = gid < 4 ? wt : 0u;
-      b[u][1] = gid < 4 ? 0u : wt;
-    }
-    // the block's MMAs start from zero and are added in fp32 registers (the tensor core's own
-    // additions truncate, and what they lose grows with the sum)
-#pragma unroll
-    for (int ch = 0; ch < CH; ch += 2) {
-      uint32_t r[2][4];  // [u]: slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
-      ldmatrix_x4_trans(r[0], vbase + OFF + ch * 16);
-      ldmatrix_x4_trans(r[1], vbase + OFF + 16 * RB + ch * 16);
-#pragma unroll
-      for (int y = 0; y < 2; y++)
-#pragma unroll
-        for (int x = 0; x < 2; x++) {
-          uint32_t lo[2][2], hi[2][2];  // dims 2x (rows gid) and 2x + 1 (rows gid + 8) of the four
+          if (t + 16 * u + tq >= t_end) sc[u] = -INFINITY;
+      }
+      if constexpr (TRACK) {
+        if (!(c & 1))
 #pragma unroll
           for (int u = 0; u < 2; u++)
+            if (!EDGE || t + 16 * u + tq < t_end) srow[t + 16 * u + tq] = sc[u] * kScore;
+      }
+      float cmax = fmaxf(sc[0], sc[1]) * kScore;  // scores are held over kUnit
+      float vs[2];
 #pragma unroll
-            for (int z = 0; z < 2; z++) {
-              const uint32_t w = x ? r[u][2 * y + z] >> 8 : r[u][2 * y + z];
-              lo[u][z] = nibble0(w);
-              hi[u][z] = nibble1(w);
-            }
-          float d[4];
-          mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][0], b[0][1]);
-          mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], b[1][0], b[1][1]);
-          ov[ch + y][x][0] = fmaf(d[0] + d[1], fit.inv, ov[ch + y][x][0]);  // both columns of w
-          ov[ch + y][x][1] = fmaf(d[2] + d[3], fit.inv, ov[ch + y][x][1]);
+      for (int u = 0; u < 2; u++) {
+        vs[u] = __half2float(nbase[OFF / 2 + (3 * kBlock + 16 * u) * NG]);
+        if (EDGE && t + 16 * u + tq >= t_end) vs[u] = 0.f;  // masked slots may hold anything
+      }
+      const float vmax = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
+      if (__any_sync(0xffffffffu, cmax > m + kSlack || vmax * fit.f > kFits)) {  // the running maximum moves, or F falls
+        float v = vmax;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        if (v * fit.f > kFits) fit.fall(v);
+#pragma unroll
+        for (int o = 2; o < 32; o <<= 1) cmax = fmaxf(cmax, __shfl_xor_sync(0xffffffffu, cmax, o));
+        cmax = fmaxf(m, cmax);
+        const float al = cmax == -INFINITY ? 1.f : fast_exp2(m - cmax);
+        m = cmax;
+        l *= al;
+        vacc *= al;
+#pragma unroll
+        for (int i = 0; i < CH; i++)
+#pragma unroll
+          for (int x = 0; x < 2; x++) {
+            ov[i][x][0] *= al;
+            ov[i][x][1] *= al;
+          }
+      }
+      uint32_t b[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
+        const __half *n = nbase + OFF / 2 + (2 * kBlock + 16 * u) * NG;
+        const float p = fast_exp2(fmaf(sc[u], kScore, -m));
+        float w = p * (vs[u] * fit.f), pm = p * __half2float(n[0]);
+        if (EDGE && t + 16 * u + tq >= t_end) w = pm = 0.f;  // (their p is 0)
+        l += p;
+        vacc += pm;
+        // w rounded, and the rest, in columns 2c and 2c+1 of the slot's row
+        uint32_t wp = pack_h2(w, w - __half2float(__float2half_rn(w)));
+        if (NG == 1 && (c & 1)) wp = 0u;
+        const uint32_t wt = transpose_8x8(wp);
+        b[u][0] = gid < 4 ? wt : 0u;
+        b[u][1] = gid < 4 ? 0u : wt;
+      }
+      // the block's MMAs start from zero and are added in fp32 registers (the tensor core's own
+      // additions truncate, and what they lose grows with the sum)
+#pragma unroll
+      for (int ch = 0; ch < CH; ch += 2) {
+        uint32_t r[2][4];  // [u]: slots 0-7 and 8-15 of chunk ch, then of chunk ch + 1
+        ldmatrix_x4_trans(r[0], vbase + OFF + ch * 16);
+        ldmatrix_x4_trans(r[1], vbase + OFF + 16 * RB + ch * 16);
+#pragma unroll
+        for (int y = 0; y < 2; y++)
+#pragma unroll
+          for (int x = 0; x < 2; x++) {
+            uint32_t lo[2][2], hi[2][2];  // dims 2x (rows gid) and 2x + 1 (rows gid + 8) of the four
+#pragma unroll
+            for (int u = 0; u < 2; u++)
+#pragma unroll
+              for (int z = 0; z < 2; z++) {
+                const uint32_t w = x ? r[u][2 * y + z] >> 8 : r[u][2 * y + z];
+                lo[u][z] = nibble0(w);
+                hi[u][z] = nibble1(w);
+              }
+            float d[4];
+            mma_f16_z(d, lo[0][0], hi[0][0], lo[0][1], hi[0][1], b[0][0], b[0][1]);
+            mma_f16(d, lo[1][0], hi[1][0], lo[1][1], hi[1][1], b[1][0], b[1][1]);
+            ov[ch + y][x][0] = fmaf(d[0] + d[1], fit.inv, ov[ch + y][x][0]);  // both columns of w
+            ov[ch + y][x][1] = fmaf(d[2] + d[3], fit.inv, ov[ch + y][x][1]);
+          }
+      }
+    };
+
+    int t = t_first;
+    // one step: wait for stage ST, its block, and the copy of the block two steps on
+    auto run = [&](auto stage, int k) -> bool {
+      constexpr int ST = decltype(stage)::value;
+      if (!mbar_wait_bounded(bar0 + 8 * ST, phase >> ST & 1, nullptr, a.kv.err)) {
+        // gave up: the copy in flight lands (or times out) before the stages are written again
+        if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), phase >> (ST ^ 1) & 1, nullptr, a.kv.err);
+        ok = false;
+        return false;
+      }
+      phase ^= 1u << ST;
+      if (t + kBlock > t_end) block(stage, std::true_type{}, t);
+      else block(stage, std::false_type{}, t);
+      if (k + 2 < steps) {
+        fence_proxy_async_smem();  // every lane has used the stage before the copy that refills it
+        __syncwarp();
+        if (((k + 2) & 31) == 0) cp.look_up(a, s, h, t + 2 * step, step, t_end, lane);
+        cp.issue((k + 2) & 31, ST * S::STAGE_B, bar0 + 8 * ST, lane);
+      }
+      t += step;
+      return true;
+    };
+    for (int k = 0; k < steps; k += 2) {
+      if (!run(std::integral_constant<int, 0>{}, k)) break;
+      if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1)) break;
+    }
+    const bool any_bad = __any_sync(0xffffffffu, cp.bad);
+    if (any_bad && lane == 0) {
+      atomicOr(a.kv.err, FG_DEVERR_RANGE);
+      if (a.shared_unit) bad_page = 1;
+    }
+
+    // ---- totals of the warp: every slot was counted by two lanes; group i's min sum in lane i ----
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    l *= 0.5f;
+#pragma unroll
+    for (int o = 2; o < 32; o <<= 1) vacc += __shfl_xor_sync(0xffffffffu, vacc, o);
+    float o4[CH / NG][4];  // lanes c = group: dims 4 gid .. 4 gid + 3 of its chunks
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+      const int cg = i / (CH / NG);
+      float v[4];
+#pragma unroll
+      for (int x = 0; x < 2; x++) {
+        v[2 * x] = ov[i][x][0] * kUnit;
+        v[2 * x + 1] = ov[i][x][1] * kUnit;
+      }
+#pragma unroll
+      for (int x = 0; x < 4; x++) {
+        v[x] += __shfl_xor_sync(0xffffffffu, v[x], 2);
+        if (NG == 1 || c == cg) o4[i % (CH / NG)][x] = v[x] + vacc;
+      }
+    }
+    const int64_t pi = target.index;
+    __half *const orow = a.out + static_cast<int64_t>(s) * a.ldo + static_cast<int64_t>(h) * D;
+    if (!a.shared_unit) {
+      const bool good = ok && !any_bad;
+      if (!target.whole && lane == 0) a.ml[pi] = make_float2(m, good ? l : -1.f);
+      const float inv = 1.0f / l;
+      const bool on = len > 0 && good;
+      if (c < NG) {
+#pragma unroll
+        for (int i = 0; i < CH / NG; i++) {
+          const int d = (c * (CH / NG) + i) * 32 + 4 * gid;
+          if (!target.whole) {
+            *reinterpret_cast<float4 *>(a.po + pi * D + d) = make_float4(o4[i][0], o4[i][1], o4[i][2], o4[i][3]);
+          } else {
+            uint2 r = make_uint2(0u, 0u);
+            if (on) r = make_uint2(pack_h2(o4[i][0] * inv, o4[i][1] * inv), pack_h2(o4[i][2] * inv, o4[i][3] * inv));
+            *reinterpret_cast<uint2 *>(orow + d) = r;
+          }
         }
+      }
+      if (TRACK && target.whole && on) {  // this warp saw the whole row: its slots' weights
+        __syncwarp();
+        grow_row(a, s, h, srow, 0, t_end, m, inv, lane, 32);
+      }
+      if (!a.units || !advance(a, &walks[warp], lane)) return;
+      continue;
     }
-  };
-
-  int t = t_first;
-  // one step: wait for stage ST, its block, and the copy of the block two steps on
-  auto run = [&](auto stage, int k) -> bool {
-    constexpr int ST = decltype(stage)::value;
-    if (!mbar_wait_bounded(bar0 + 8 * ST, phase >> ST & 1, nullptr, a.kv.err)) {
-      // gave up: the copy in flight lands (or times out) before the stages are written again
-      if (k + 1 < steps) mbar_wait_bounded(bar0 + 8 * (ST ^ 1), phase >> (ST ^ 1) & 1, nullptr, a.kv.err);
-      ok = false;
-      return false;
+    float *wo = reinterpret_cast<float *>(wbase);
+    if (c < NG)
+#pragma unroll
+      for (int i = 0; i < CH / NG; i++)
+        *reinterpret_cast<float4 *>(wo + (c * (CH / NG) + i) * 32 + 4 * gid) =
+            make_float4(o4[i][0], o4[i][1], o4[i][2], o4[i][3]);
+    if (lane == 0) {
+      red_m[warp] = m;
+      red_l[warp] = l;
     }
-    phase ^= 1u << ST;
-    if (t + kBlock > t_end) block(stage, std::true_type{}, t);
-    else block(stage, std::false_type{}, t);
-    if (k + 2 < steps) {
-      fence_proxy_async_smem();  // every lane has used the stage before the copy that refills it
-      __syncwarp();
-      if (((k + 2) & 31) == 0) cp.look_up(a, s, h, t + 2 * step, step, t_end, lane);
-      cp.issue((k + 2) & 31, ST * S::STAGE_B, bar0 + 8 * ST, lane);
+    const bool good = __syncthreads_and(ok) && !bad_page;
+    float M = -INFINITY, den = 0.f, f[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) M = fmaxf(M, red_m[w]);
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+      f[w] = red_m[w] == -INFINITY ? 0.f : exp2f(red_m[w] - M);
+      den += f[w] * red_l[w];
     }
-    t += step;
-    return true;
-  };
-  for (int k = 0; k < steps; k += 2) {
-    if (!run(std::integral_constant<int, 0>{}, k)) break;
-    if (k + 1 < steps && !run(std::integral_constant<int, 1>{}, k + 1)) break;
-  }
-  const bool any_bad = __any_sync(0xffffffffu, cp.bad);
-  if (any_bad && lane == 0) {
-    atomicOr(a.kv.err, FG_DEVERR_RANGE);
-    if (a.shared_unit) bad_page = 1;
-  }
-
-  // ---- totals of the warp: every slot was counted by two lanes; group i's min sum in lane i ----
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  l *= 0.5f;
-#pragma unroll
-  for (int o = 2; o < 32; o <<= 1) vacc += __shfl_xor_sync(0xffffffffu, vacc, o);
-  float o4[CH / NG][4];  // lanes c = group: dims 4 gid .. 4 gid + 3 of its chunks
-#pragma unroll
-  for (int i = 0; i < CH; i++) {
-    const int cg = i / (CH / NG);
-    float v[4];
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-      v[2 * x] = ov[i][x][0] * kUnit;
-      v[2 * x + 1] = ov[i][x][1] * kUnit;
-    }
-#pragma unroll
-    for (int x = 0; x < 4; x++) {
-      v[x] += __shfl_xor_sync(0xffffffffu, v[x], 2);
-      if (NG == 1 || c == cg) o4[i % (CH / NG)][x] = v[x] + vacc;
-    }
-  }
-  const int64_t pi = target.index;
-  __half *const orow = a.out + static_cast<int64_t>(s) * a.ldo + static_cast<int64_t>(h) * D;
-  if (!a.shared_unit) {
-    const bool good = ok && !any_bad;
-    if (!target.whole && lane == 0) a.ml[pi] = make_float2(m, good ? l : -1.f);
-    const float inv = 1.0f / l;
+    const float inv = 1.0f / den;
     const bool on = len > 0 && good;
-    if (c < NG) {
+    for (int d = 2 * tid; d < D; d += 2 * kWarps * 32) {
+      float o0 = 0.f, o1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < CH / NG; i++) {
-        const int d = (c * (CH / NG) + i) * 32 + 4 * gid;
-        if (!target.whole) {
-          *reinterpret_cast<float4 *>(a.po + pi * D + d) = make_float4(o4[i][0], o4[i][1], o4[i][2], o4[i][3]);
-        } else {
-          uint2 r = make_uint2(0u, 0u);
-          if (on) r = make_uint2(pack_h2(o4[i][0] * inv, o4[i][1] * inv), pack_h2(o4[i][2] * inv, o4[i][3] * inv));
-          *reinterpret_cast<uint2 *>(orow + d) = r;
+      for (int w = 0; w < kWarps; w++)
+        if (f[w] != 0.f) {
+          const float2 v = *reinterpret_cast<const float2 *>(smem + w * S::WARP_B + d * 4);
+          o0 += f[w] * v.x;
+          o1 += f[w] * v.y;
         }
-      }
+      *reinterpret_cast<__half2 *>(orow + d) = on ? __floats2half2_rn(o0 * inv, o1 * inv) : __floats2half2_rn(0.f, 0.f);
     }
-    if (TRACK && target.whole && on) {  // this warp saw the whole row: its slots' weights
-      __syncwarp();
-      grow_row(a, s, h, srow, 0, t_end, m, inv, lane, 32);
-    }
-    if (!a.units || !advance(a, &walks[warp], lane)) return;
-    continue;
-  }
-  float *wo = reinterpret_cast<float *>(wbase);
-  if (c < NG)
-#pragma unroll
-    for (int i = 0; i < CH / NG; i++)
-      *reinterpret_cast<float4 *>(wo + (c * (CH / NG) + i) * 32 + 4 * gid) =
-          make_float4(o4[i][0], o4[i][1], o4[i][2], o4[i][3]);
-  if (lane == 0) {
-    red_m[warp] = m;
-    red_l[warp] = l;
-  }
-  const bool good = __syncthreads_and(ok) && !bad_page;
-  float M = -INFINITY, den = 0.f, f[kWarps];
-#pragma unroll
-  for (int w = 0; w < kWarps; w++) M = fmaxf(M, red_m[w]);
-#pragma unroll
-  for (int w = 0; w < kWarps; w++) {
-    f[w] = red_m[w] == -INFINITY ? 0.f : exp2f(red_m[w] - M);
-    den += f[w] * red_l[w];
-  }
-  const float inv = 1.0f / den;
-  const bool on = len > 0 && good;
-  for (int d = 2 * tid; d < D; d += 2 * kWarps * 32) {
-    float o0 = 0.f, o1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; w++)
-      if (f[w] != 0.f) {
-        const float2 v = *reinterpret_cast<const float2 *>(smem + w * S::WARP_B + d * 4);
-        o0 += f[w] * v.x;
-        o1 += f[w] * v.y;
-      }
-    *reinterpret_cast<__half2 *>(orow + d) = on ? __floats2half2_rn(o0 * inv, o1 * inv) : __floats2half2_rn(0.f, 0.f);
-  }
-  if (TRACK && on)  // (the CTA's scores were published by the barrier above)
-    grow_row(a, s, h, srow, 0, t_end, M, inv, tid, kWarps * 32);
-  return;
+    if (TRACK && on)  // (the CTA's scores were published by the barrier above)
+      grow_row(a, s, h, srow, 0, t_end, M, inv, tid, kWarps * 32);
+    return;
   }
 }
 
